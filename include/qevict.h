@@ -342,6 +342,80 @@ qevict_status qevict_route_rd_mixed(qevict_cache *cache, int32_t layer, const fl
 qevict_status qevict_k_channel_weights(qevict_cache *cache, int32_t layer, const void *q_obs, int64_t n_q,
                                       const void *k_full, int64_t n_tokens, float *weights, void *stream);
 
+/* From a layer's projections to its cache: the head norms and the rotation of
+ * queries and keys, the attention of a prompt (or of single tokens) over
+ * uncompressed keys, and the window scores on which qevict_prefill routes. The
+ * three calls take their head counts, sequences and window size from the cache
+ * (with per-head tiers too: [batch] is the number of sequences and Hq, Hkv the
+ * model's heads), read nothing else of it unless said so, keep no scratch and
+ * may run concurrently with one another and with decodes. The cache's device
+ * must be current (INVALID_ARG otherwise).
+ *
+ * For every token and head x of 128 channels of q and k: y = x / sqrt(mean(x^2)
+ * + eps) * weight, then each pair (a, b) of channels turns by the angle t =
+ * position * inv_freq[pair] into (a cos t - b sin t, b cos t + a sin t). fp32
+ * throughout (the angle is reduced exactly), rounded to bf16 once. v is copied.
+ *  q, k, v     bf16 [batch][n_tokens] tokens of [Hq] or [Hkv][head_dim], device;
+ *              consecutive tokens lie q_stride (k_stride, v_stride) elements
+ *              apart: a multiple of 8, at least the heads' own length (so the
+ *              three can be parts of one fused projection). v may be NULL.
+ *  positions   int64 [batch][n_tokens], device, any value (accurate to fp32
+ *              below 2^37), or NULL: the layer's length on the device as the
+ *              call runs, onwards (graph replays advance with it).
+ *  q_weight, k_weight  bf16 [head_dim], device, or NULL: no norm of q (of k).
+ *  eps         finite, >= 0.
+ *  inv_freq    fp32 [head_dim / 2], device, finite: radians per position.
+ *  interleaved 0: pair i is channels (i, i + 64); nonzero: (2 i, 2 i + 1).
+ *  q_out, k_out, v_out  bf16 [batch][n_tokens][heads][head_dim], dense, as
+ *              every other call takes them. q_out may be q (k_out k, v_out v)
+ *              where that is dense; any other overlap is INVALID_ARG.
+ * Tensors and weights are 16-byte aligned, positions and inv_freq 8-byte. */
+qevict_status qevict_qk_norm_rope(qevict_cache *cache, int32_t layer, const void *q, int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride, int32_t n_tokens,
+                                  const int64_t *positions, const void *q_weight, const void *k_weight, float eps,
+                                  const float *inv_freq, int32_t interleaved, void *q_out, void *k_out, void *v_out,
+                                  void *stream);
+
+/* Causal softmax attention over uncompressed keys with a sliding span and sink
+ * tokens. Sequence b has kv_len[b] keys and q_len[b] queries, its last
+ * positions: query i sits at p = kv_len[b] - q_len[b] + i and sees key j iff
+ * j <= p and (j > p - span or j < sinks). n_q = n_kv is a prompt, n_q < n_kv a
+ * chunk of one, n_q = 1 a decode step over a full cache.
+ *  q     bf16 [batch][n_q][Hq][head_dim], k and v bf16 [batch][n_kv][Hkv]
+ *        [head_dim], device, 16-byte aligned, dense. Query head h reads KV head
+ *        h / (Hq / Hkv).
+ *  q_len, kv_len  int32 [batch], device, or NULL: n_q, n_kv for every sequence.
+ *        Lengths below 0 or above n_q (n_kv) count as 0 and n_q (n_kv).
+ *  span  tokens a query sees, itself included; 0: all before it.
+ *  sinks first tokens that every later query sees besides.
+ *  out   bf16 [batch][n_q][Hq][head_dim], 16-byte aligned: softmax(q K^T /
+ *        sqrt(d)) V over the visible keys. fp32 sums; the probabilities enter
+ *        their product with V as bf16.
+ *  lse   fp32 [batch][Hq][n_q] or NULL: log(sum(exp(q K^T / sqrt(d)))).
+ * A query that sees no key (p < 0) gets out 0 and lse -inf. Rows at or past
+ * q_len[b] are not written. Keys and values that no query of the call sees
+ * (at or past kv_len, before the span) may hold anything, NaN included.
+ * n_q and n_kv are in [1, 2^29]. */
+qevict_status qevict_span_attention(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
+                                    const void *v, int32_t n_kv, const int32_t *q_len, const int32_t *kv_len,
+                                    int32_t span, int32_t sinks, void *out, float *lse, void *stream);
+
+/* The attention mass that each cache window receives from a set of queries
+ * (QEvict "Cumulatieve Scoring": the scores a prompt's routing starts from):
+ * scores[b][w] = sum over the queries i of sequence b of the mean over the Hq
+ * query heads of sum over the visible keys j of window w of exp(q_i k_j /
+ * sqrt(d) - lse[i]). Arguments as qevict_span_attention, whose lse it takes:
+ * the same queries, or the last of them (n_q rows of their own, with q_len and
+ * kv_len placing them) to score by an observation window.
+ *  lse     fp32 [batch][Hq][n_q], device.
+ *  scores  fp32 [batch][ceil(n_kv / window)], device, written (0 for windows
+ *          past kv_len); with per-head tiers [batch * Hkv][ceil(n_kv / window)],
+ *          the mean over the G query heads of each KV head.
+ * Sums are fp32 in a fixed order: every call gives the same scores. */
+qevict_status qevict_span_scores(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
+                                 int32_t n_kv, const int32_t *q_len, const int32_t *kv_len, int32_t span,
+                                 int32_t sinks, const float *lse, float *scores, void *stream);
+
 /* The rate-distortion routing event with RDKV's K-channel half ("Technische
  * Samenvatting: RDKV", 2.2 Fase 2 and 3, 2.3 Zone A). First the window widths
  * of qevict_route_rd_mixed (every window is then full precision or evicted,

@@ -31,6 +31,7 @@ EXPORTS = ["qevict_pool_capacity", "qevict_cache_create", "qevict_cache_destroy"
            "qevict_refresh_lengths", "qevict_decode_attention_static_scratch",
            "qevict_get_tier_move_counts", "qevict_future_missed_mass", "qevict_route_global", "qevict_route_logsparse", "qevict_route_rd",
            "qevict_route_rd_mixed", "qevict_k_channel_weights", "qevict_route_rd_kv",
+           "qevict_qk_norm_rope", "qevict_span_attention", "qevict_span_scores",
            "qevict_length",
            "qevict_last_error"]
 
@@ -123,6 +124,9 @@ def load() -> ctypes.CDLL:
         "qevict_route_rd_mixed": [P, I32, P, P, P],
         "qevict_k_channel_weights": [P, I32, P, I64, P, I64, P, P],
         "qevict_route_rd_kv": [P, I32, P, P, P],
+        "qevict_qk_norm_rope": [P, I32, P, I64, P, I64, P, I64, I32, P, P, P, ctypes.c_float, P, I32, P, P, P, P],
+        "qevict_span_attention": [P, I32, P, I32, P, P, I32, P, P, I32, I32, P, P, P],
+        "qevict_span_scores": [P, I32, P, I32, P, I32, P, P, I32, I32, P, P, P],
         "qevict_future_missed_mass": [P, I32, P, P, I64, P, P],
         "qevict_length": [P, I32],
         "qevict_last_error": [],
@@ -395,6 +399,115 @@ class TieredCache:
         if not v.k_group_bits:
             return None
         return device_tensor(v.k_group_bits, (v.batch, v.num_kv_heads, 4), "|u1").cpu()
+
+    # ---- from projections to the cache ------------------------------------------
+    def _heads(self, t, heads, what, dtype=torch.bfloat16):
+        """Sequences and tokens of a [B][n][heads][128] (or [B][heads][128]) tensor, checked."""
+        if t.dtype is not dtype or t.dim() not in (3, 4) or t.shape[0] != self.B or \
+                t.shape[-2] != heads or t.shape[-1] != HEAD_DIM:
+            raise ValueError(f"{what} must be {dtype} [{self.B}][n][{heads}][{HEAD_DIM}], got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if not t.is_cuda or t.device.index != self.device:
+            raise ValueError(f"{what} must be on cuda:{self.device}")
+        return t.shape[1] if t.dim() == 4 else 1
+
+    def _side(self, t, shape, dtype, what):
+        """A dense tensor of the given shape and type on the cache's device, or None."""
+        if t is None:
+            return None
+        if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda or \
+                t.device.index != self.device:
+            raise ValueError(f"{what} must be dense {dtype} {list(shape)} on cuda:{self.device}, got {t.dtype} "
+                             f"{list(t.shape)}")
+        return t.data_ptr()
+
+    def _token_stride(self, t, n, heads, what):
+        """Elements between consecutive tokens of t, whose tokens must be evenly spaced and dense inside."""
+        s = t.stride()
+        if t.dim() == 4:
+            step = s[1] if n > 1 else s[0]
+            even = t.shape[0] == 1 or s[0] == n * step
+            if n == 1 and t.shape[0] == 1:
+                step = heads * HEAD_DIM
+        else:
+            step, even = (s[0] if t.shape[0] > 1 else heads * HEAD_DIM), True
+        if not even or s[-1] != 1 or (heads > 1 and s[-2] != HEAD_DIM):
+            raise ValueError(f"{what}: tokens must be evenly spaced, with dense heads (strides {s})")
+        return step
+
+    def qk_norm_rope(self, layer, q, k, inv_freq, v=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, q_out=None, k_out=None, v_out=None, stream=None):
+        """Head norms and rotation of q [B][n][Hq][128] and k [B][n][Hkv][128] (and a dense copy of v), which
+        may be parts of one fused projection; positions int64 [B][n], or None: the layer's length onwards.
+        [B][heads][128] tensors are one token. Returns (q, k), or (q, k, v), dense."""
+        n = self._heads(q, self.Hq, "q")
+        ins = [(q, self.Hq, "q", q_out), (k, self.Hkv, "k", k_out)]
+        if v is not None:
+            ins.append((v, self.Hkv, "v", v_out))
+        elif v_out is not None:
+            raise ValueError("v_out without v")
+        steps, outs = [], []
+        for t, heads, what, o in ins:
+            if what != "q" and self._heads(t, heads, what) != n:
+                raise ValueError(f"{what} must have q's {n} tokens")
+            steps.append(self._token_stride(t, n, heads, what))
+            if o is None:
+                o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            else:
+                self._side(o, tuple(t.shape), torch.bfloat16, what + "_out")
+            outs.append(o)
+        side = self._side
+        rc = self.lib.qevict_qk_norm_rope(
+            self.handle, layer, q.data_ptr(), steps[0], k.data_ptr(), steps[1],
+            None if v is None else v.data_ptr(), 0 if v is None else steps[2], n,
+            side(positions, (self.B, n), torch.int64, "positions"),
+            side(q_weight, (HEAD_DIM,), torch.bfloat16, "q_weight"),
+            side(k_weight, (HEAD_DIM,), torch.bfloat16, "k_weight"), eps,
+            side(inv_freq, (HEAD_DIM // 2,), torch.float32, "inv_freq"), 1 if interleaved else 0,
+            outs[0].data_ptr(), outs[1].data_ptr(), None if v is None else outs[2].data_ptr(), _stream(stream))
+        self._check(rc)
+        return tuple(outs)
+
+    def _dense(self, t, heads, what):
+        n = self._heads(t, heads, what)
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be dense (strides {t.stride()})")
+        return n
+
+    def span_attention(self, layer, q, k, v, span=0, sinks=0, q_len=None, kv_len=None, out=None, lse=None,
+                       want_lse=True, stream=None):
+        """Causal attention of q [B][n_q][Hq][128], the last positions, over k, v [B][n_kv][Hkv][128]; a query
+        sees the `span` latest keys (0: all) and the first `sinks`. Returns (out bf16, lse fp32 [B][Hq][n_q]
+        or None). Rows past q_len[b] of caller-owned out and lse are left as they were."""
+        n_q, n_kv = self._dense(q, self.Hq, "q"), self._dense(k, self.Hkv, "k")
+        if self._dense(v, self.Hkv, "v") != n_kv:
+            raise ValueError(f"v must have k's {n_kv} tokens")
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(self.B, self.Hq, n_q, dtype=torch.float32, device=q.device)
+        side, B = self._side, self.B
+        self._check(self.lib.qevict_span_attention(
+            self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), v.data_ptr(), n_kv,
+            side(q_len, (B,), torch.int32, "q_len"), side(kv_len, (B,), torch.int32, "kv_len"), span, sinks,
+            side(out, tuple(q.shape), torch.bfloat16, "out"), side(lse, (B, self.Hq, n_q), torch.float32, "lse"),
+            _stream(stream)))
+        return out, lse
+
+    def span_scores(self, layer, q, k, lse, span=0, sinks=0, q_len=None, kv_len=None, out=None, stream=None):
+        """fp32 [units][ceil(n_kv / window)]: the attention mass each window of k [B][n_kv][Hkv][128] receives
+        from the queries q [B][n_q][Hq][128], whose span_attention gave lse [B][Hq][n_q]; what prefill takes."""
+        n_q, n_kv = self._dense(q, self.Hq, "q"), self._dense(k, self.Hkv, "k")
+        W = -(-n_kv // self.w)
+        if out is None:
+            out = torch.empty(self.units, W, dtype=torch.float32, device=q.device)
+        side, B = self._side, self.B
+        self._check(self.lib.qevict_span_scores(
+            self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), n_kv, side(q_len, (B,), torch.int32, "q_len"),
+            side(kv_len, (B,), torch.int32, "kv_len"), span, sinks,
+            side(lse, (B, self.Hq, n_q), torch.float32, "lse"),
+            side(out, (self.units, W), torch.float32, "out"), _stream(stream)))
+        return out
 
     # ---- RDKV's K-channel half -----------------------------------------------
     def k_channel_weights(self, layer, q_obs, k_full, stream=None):

@@ -159,6 +159,16 @@ qevict_status check_int2_only(const qevict_cache *c, const char *what) {
     return QEVICT_OK;
 }
 
+// The kernels run on the current device, so it has to be the cache's.
+qevict_status check_device(const qevict_cache *c) {
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "current device");
+    if (dev != c->device)
+        return fail(QEVICT_ERR_INVALID_ARG, "the cache is on device %d, the current device is %d", c->device, dev);
+    return QEVICT_OK;
+}
+
 void note_op(qevict_cache *c, int layer, void *stream) {
     c->prev_layer = layer;
     c->prev_stream = stream;
@@ -613,6 +623,162 @@ qevict_status qevict_k_channel_weights(qevict_cache *c, int32_t layer, const voi
     cudaError_t e = launch_k_channel_weights(c->layers[layer].dev, (const __nv_bfloat16 *)q_obs, (int)n_q,
                                              (const __nv_bfloat16 *)k_full, n_tokens, weights, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "K channel weights kernel");
+    note_op(c, -1, stream);
+    return QEVICT_OK;
+}
+
+// The model's heads and sequences behind a cache's units.
+static SpanArgs span_args(const qevict_cache *c, int n_q, int n_kv, const int32_t *q_len, const int32_t *kv_len,
+                          int span, int sinks) {
+    SpanArgs a{};
+    a.B = c->cfg.batch / c->hs;
+    a.Hq = c->cfg.num_q_heads * c->hs;
+    a.Hkv = c->cfg.num_kv_heads * c->hs;
+    a.G = c->G;
+    a.n_q = n_q;
+    a.n_kv = n_kv;
+    a.span = span == 0 || span > n_kv ? n_kv : span;
+    a.sinks = sinks > n_kv ? n_kv : sinks;
+    a.q_len = q_len;
+    a.kv_len = kv_len;
+    return a;
+}
+
+// [sequences][tokens][heads][128] bf16 in boxes of 64 channels x `bh` heads x `bt` tokens
+static cudaError_t encode_tokens(CUtensorMap *map, const void *base, int seqs, int tokens, int heads, int bh, int bt) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {kHeadDim, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)seqs};
+    const cuuint64_t row = (cuuint64_t)heads * kHeadDim * 2;
+    const cuuint64_t strides[3] = {kHeadDim * 2, row, row * (cuuint64_t)tokens};
+    const cuuint32_t box[4] = {64, (cuuint32_t)bh, (cuuint32_t)bt, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+static qevict_status check_span(const qevict_cache *c, const void *q, int32_t n_q, const void *k, int32_t n_kv,
+                                int32_t span, int32_t sinks) {
+    if (n_q < 1 || n_kv < 1 || n_q > kMaxSpanTokens || n_kv > kMaxSpanTokens)
+        return fail(QEVICT_ERR_INVALID_ARG, "n_q (%d) and n_kv (%d) must be in [1, %d]", n_q, n_kv, kMaxSpanTokens);
+    if (span < 0 || sinks < 0) return fail(QEVICT_ERR_INVALID_ARG, "span (%d) and sinks (%d) must be >= 0", span, sinks);
+    if (((uintptr_t)q | (uintptr_t)k) & 15) return fail(QEVICT_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+    return check_device(c);
+}
+
+qevict_status qevict_qk_norm_rope(qevict_cache *c, int32_t layer, const void *q, int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride, int32_t n_tokens,
+                                  const int64_t *positions, const void *q_weight, const void *k_weight, float eps,
+                                  const float *inv_freq, int32_t interleaved, void *q_out, void *k_out, void *v_out,
+                                  void *stream) {
+    qevict_status st = check_layer(c, layer);
+    if (st) return st;
+    if (!q || !k || !q_out || !k_out || !inv_freq)
+        return fail(QEVICT_ERR_INVALID_ARG, "q, k, inv_freq, q_out and k_out must not be NULL");
+    if ((v == nullptr) != (v_out == nullptr)) return fail(QEVICT_ERR_INVALID_ARG, "give both of v and v_out or neither");
+    if (n_tokens < 1) return fail(QEVICT_ERR_INVALID_ARG, "n_tokens must be >= 1");
+    if (!(eps >= 0.f) || isinf(eps)) return fail(QEVICT_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    RopeArgs a{};
+    a.Hq = c->cfg.num_q_heads * c->hs;
+    a.Hkv = c->cfg.num_kv_heads * c->hs;
+    const struct {
+        int64_t stride;
+        int heads;
+    } in[3] = {{q_stride, a.Hq}, {k_stride, a.Hkv}, {v ? v_stride : (int64_t)a.Hkv * kHeadDim, a.Hkv}};
+    for (const auto &x : in)
+        if (x.stride < (int64_t)x.heads * kHeadDim || x.stride % 8 || x.stride > (int64_t)1 << 32)
+            return fail(QEVICT_ERR_INVALID_ARG, "a token stride of %lld elements: a multiple of 8, at least the token's "
+                        "%d heads and at most 2^32", (long long)x.stride, x.heads);
+    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_out | (uintptr_t)v_out |
+         (uintptr_t)q_weight | (uintptr_t)k_weight) & 15)
+        return fail(QEVICT_ERR_INVALID_ARG, "q, k, v, their outputs and the weights must be 16-byte aligned");
+    if (((uintptr_t)inv_freq | (uintptr_t)positions) & 7)
+        return fail(QEVICT_ERR_INVALID_ARG, "inv_freq and positions must be 8-byte aligned");
+    a.tokens = (int64_t)(c->cfg.batch / c->hs) * n_tokens;
+    // reads and writes of different heads are not ordered, so only exact in-place calls may overlap
+    const struct {
+        const void *src, *dst;
+        int64_t stride;
+        int heads;
+    } io[3] = {{q, q_out, q_stride, a.Hq}, {k, k_out, k_stride, a.Hkv}, {v, v_out, v_stride, a.Hkv}};
+    for (int i = 0; i < 3; ++i) {
+        if (!io[i].src) continue;
+        const uintptr_t o0 = (uintptr_t)io[i].dst, o1 = o0 + a.tokens * io[i].heads * kHeadDim * 2;
+        for (int j = 0; j < 3; ++j) {
+            if (!io[j].src) continue;
+            const uintptr_t s0 = (uintptr_t)io[j].src;
+            const uintptr_t s1 = s0 + ((a.tokens - 1) * io[j].stride + (int64_t)io[j].heads * kHeadDim) * 2;
+            const bool same = i == j && o0 == s0 && io[j].stride == (int64_t)io[j].heads * kHeadDim;
+            if (o0 < s1 && s0 < o1 && !same)
+                return fail(QEVICT_ERR_INVALID_ARG, "an output overlaps an input (in place needs the same dense tensor)");
+            if (j < i && o0 < (uintptr_t)io[j].dst + a.tokens * io[j].heads * kHeadDim * 2 && (uintptr_t)io[j].dst < o1)
+                return fail(QEVICT_ERR_INVALID_ARG, "two outputs overlap");
+        }
+    }
+    st = check_device(c);
+    if (st) return st;
+    a.q = (const __nv_bfloat16 *)q;
+    a.k = (const __nv_bfloat16 *)k;
+    a.v = (const __nv_bfloat16 *)v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_tokens = n_tokens;
+    a.positions = positions;
+    a.q_weight = (const __nv_bfloat16 *)q_weight;
+    a.k_weight = (const __nv_bfloat16 *)k_weight;
+    a.inv_freq = inv_freq;
+    a.eps = eps;
+    a.interleaved = interleaved;
+    a.q_out = (__nv_bfloat16 *)q_out;
+    a.k_out = (__nv_bfloat16 *)k_out;
+    a.v_out = (__nv_bfloat16 *)v_out;
+    const cudaError_t e = launch_rope(c->layers[layer].dev, a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotation kernel");
+    note_op(c, -1, stream);
+    return QEVICT_OK;
+}
+
+qevict_status qevict_span_attention(qevict_cache *c, int32_t layer, const void *q, int32_t n_q, const void *k,
+                                    const void *v, int32_t n_kv, const int32_t *q_len, const int32_t *kv_len,
+                                    int32_t span, int32_t sinks, void *out, float *lse, void *stream) {
+    qevict_status st = check_layer(c, layer);
+    if (st) return st;
+    if (!q || !k || !v || !out) return fail(QEVICT_ERR_INVALID_ARG, "q, k, v and out must not be NULL");
+    st = check_span(c, q, n_q, k, n_kv, span, sinks);
+    if (st) return st;
+    if (((uintptr_t)v | (uintptr_t)out) & 15) return fail(QEVICT_ERR_INVALID_ARG, "v and out must be 16-byte aligned");
+    const SpanArgs a = span_args(c, n_q, n_kv, q_len, kv_len, span, sinks);
+    CUtensorMap qm, km, vm;
+    cudaError_t e = encode_tokens(&qm, q, a.B, n_q, a.Hq, a.G, span_tile_tokens(a.G));
+    if (e == cudaSuccess) e = encode_tokens(&km, k, a.B, n_kv, a.Hkv, 1, 128);
+    if (e == cudaSuccess) e = encode_tokens(&vm, v, a.B, n_kv, a.Hkv, 1, 128);
+    if (e == cudaSuccess)
+        e = launch_span_attention(a, c->cdev, layer, qm, km, vm, (__nv_bfloat16 *)out, lse, c->num_sms,
+                                  (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "span attention kernel");
+    note_op(c, -1, stream);
+    return QEVICT_OK;
+}
+
+qevict_status qevict_span_scores(qevict_cache *c, int32_t layer, const void *q, int32_t n_q, const void *k, int32_t n_kv,
+                                 const int32_t *q_len, const int32_t *kv_len, int32_t span, int32_t sinks,
+                                 const float *lse, float *scores, void *stream) {
+    qevict_status st = check_layer(c, layer);
+    if (st) return st;
+    if (!q || !k || !lse || !scores) return fail(QEVICT_ERR_INVALID_ARG, "q, k, lse and scores must not be NULL");
+    st = check_span(c, q, n_q, k, n_kv, span, sinks);
+    if (st) return st;
+    const SpanArgs a = span_args(c, n_q, n_kv, q_len, kv_len, span, sinks);
+    CUtensorMap qm, km;
+    cudaError_t e = encode_tokens(&qm, q, a.B, n_q, a.Hq, a.G, span_tile_tokens(a.G));
+    if (e == cudaSuccess) e = encode_tokens(&km, k, a.B, n_kv, a.Hkv, 1, 128);
+    if (e == cudaSuccess)
+        e = launch_span_scores(a, c->cdev, layer, qm, km, lse, scores, c->cfg.window, c->hs > 1, c->num_sms,
+                               (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "span scores kernel");
     note_op(c, -1, stream);
     return QEVICT_OK;
 }

@@ -19,6 +19,7 @@ constexpr int kGroup = 32;             // channels per INT2 group
 constexpr int kGroups = kHeadDim / kGroup;
 constexpr int kMaxG = 8;               // query heads per KV head
 constexpr int kMaxSplits = 32;         // decode CTAs per (sequence, KV head)
+constexpr int kMaxSpanTokens = 1 << 29; // tokens per sequence of the span calls (int sums stay in range)
 constexpr int kVTile = 16;             // tokens per transposed V-code word
 constexpr int kCtrN = 16;              // counters per sequence
 
@@ -181,6 +182,30 @@ struct GlobalArgs {
     int32_t *cnt;                      // [sequences][4]: candidates, forced, non-finite (0 between events)
 };
 
+// One qevict_qk_norm_rope call (include/qevict.h); strides in elements between tokens.
+struct RopeArgs {
+    const __nv_bfloat16 *q, *k, *v;            // v may be NULL
+    int64_t q_stride, k_stride, v_stride;
+    int64_t tokens;                            // sequences * n_tokens
+    int n_tokens, Hq, Hkv;
+    const int64_t *positions;                  // [tokens] or NULL: the layer's length onwards
+    const __nv_bfloat16 *q_weight, *k_weight;  // [128] or NULL
+    const float *inv_freq;                     // [64]
+    float eps;
+    int interleaved;
+    __nv_bfloat16 *q_out, *k_out, *v_out;
+};
+
+// What qevict_span_attention and qevict_span_scores have in common: query i of
+// sequence b sits at position kv_len[b] - q_len[b] + i and sees key j iff
+// j <= p and (j > p - span or j < sinks).
+struct SpanArgs {
+    int B, Hq, Hkv, G;         // sequences and heads of the model (units unfolded)
+    int n_q, n_kv;
+    int span, sinks;           // span in [1, n_kv], sinks in [0, n_kv]
+    const int32_t *q_len, *kv_len;   // [B] or NULL: n_q, n_kv
+};
+
 // ---- launchers (each enqueues on `s`, returns the launch error) -----------
 cudaError_t launch_init_layer(const LayerDev &L, cudaStream_t s);
 // Keys (all layers in parallel), then budget, counts and the two thresholds of
@@ -226,6 +251,18 @@ cudaError_t launch_decode(const LayerDev &L, const CacheDev &C, const DecodeScra
                           cudaStream_t s);
 cudaError_t launch_k_channel_weights(const LayerDev &L, const __nv_bfloat16 *q, int n_q, const __nv_bfloat16 *k,
                                      int64_t n_tok, float *out, cudaStream_t s);
+cudaError_t launch_rope(const LayerDev &L, const RopeArgs &a, cudaStream_t s);
+// qmap: q [B][n_q][Hq][128] as a 4-D tiled map, boxes of 64 channels x G heads x
+// span_tile_tokens(G) tokens; kmap, vmap: [B][n_kv][Hkv][128], boxes of 64
+// channels x 1 head x 128 tokens; 128-byte swizzle. out bf16, lse fp32 or NULL.
+__host__ __device__ inline int span_tile_tokens(int G) { return 128 / G; }
+cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap, __nv_bfloat16 *out, float *lse,
+                                  int num_sms, cudaStream_t s);
+// scores fp32 [B][n_win], or [B * Hkv][n_win] with per_head
+cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
+                               const CUtensorMap &kmap, const float *lse, float *scores, int w, bool per_head,
+                               int num_sms, cudaStream_t s);
 cudaError_t launch_read_lengths(const LayerDev &L, int32_t *out, cudaStream_t s);
 // kmap: k_full [sequences * n_tokens][Hkv * hs][128] bf16 as a 3-D tiled map,
 // boxes of 64 channels x 1 KV head x 16 tokens, 128-byte swizzle
