@@ -392,111 +392,343 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (warp == 0) tc_free<512>(tm);
 }
 
-// Window scores: one CTA per (key tile, sequence), or per (key tile, sequence,
-// KV head) with per-head units. The logits are computed transposed, keys as
-// the 128 lanes and the rows of a query tile as the 128 columns, so that a key's
-// mass is a sum over its own lane's registers.
-__global__ void __launch_bounds__(128) span_scores_simple(const SpanArgs a, const CacheDev C, int layer,
-                                                          const __grid_constant__ CUtensorMap qmap,
-                                                          const __grid_constant__ CUtensorMap kmap, const float *lse,
-                                                          float *scores, int w, int n_win, int per_head) {
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2];
-    __shared__ uint32_t slot;
-    __shared__ int stop;
-    __shared__ float ls[kTile], keys[kTile];
-    __shared__ int ps[kTile];
-    const int b = blockIdx.y;
-    const int tk = kTile / w * w;   // whole windows of one tile
-    const int k0 = blockIdx.x * tk;
-    const int T = span_tile_tokens(a.G), rows = T * a.G;
-    const int q_len = clamped(a.q_len, b, a.n_q), kv_len = clamped(a.kv_len, b, a.n_kv);
-    const int shift = kv_len - q_len;
-    const int k_hi = min(k0 + tk, kv_len) - 1;
-    // queries that see some key of the tile
-    int i_lo = max(0, k0 - shift), i_hi = q_len;
-    if (k0 >= a.sinks) i_hi = min(i_hi, k_hi + a.span - shift);
-    if (k_hi < k0) i_hi = 0;
+// ---- window scores --------------------------------------------------------------
+//
+// The logits are computed transposed, S^T = K Q^T: keys are the 128 lanes of
+// tensor memory and the rows of a query tile its 128 columns, so that a key's
+// mass is a sum along its own lane, in one register, over all query tiles.
+// An item is a run of 256 keys (rounded down to whole windows) of one sequence
+// (of one KV head with per-head units); its steps are the (KV head, query tile)
+// pairs that see some of them. A cluster of CTAs shares an item's steps
+// evenly and adds its sums in rank order; with one CTA per item the CTAs
+// are persistent and the copies of the next item run under this one.
+// Warps as in the attention: two groups that each take the masses of one of the
+// two key tiles, one thread for the products, one for the copies, and a warp that
+// fetches the rows' log-sum-exps. Two logit tiles per group alternate.
+constexpr int kScThreads = kSoftmax + 96;
+constexpr int kScLs = 4;                      // steps whose log-sum-exps are in shared memory
+constexpr int kScQ = 3;                       // query tile slots; the keys have two sets of two tiles
+// what lies behind the tiles in shared memory
+struct ScoreTail {
+    float ls[kScLs][kTile];     // of a step's rows: -lse in log2 units
+    float segs[2][8], wins[2][8];   // masses of 16 keys, and of windows
+    uint64_t bars[4 + 2 * kScQ + 8 + 2 * kScLs + 1];
+    uint8_t tok[kTile];         // token of a query tile's row, 255 for the rows past the last
+    uint32_t slot;
+    int stop;
+};
+constexpr int kScSmem = (4 + kScQ) * kTileBytes + (int)sizeof(ScoreTail);
+static_assert(kScSmem <= 227 * 1024, "shared memory of one CTA");
 
-    const uint32_t sm = (smem_u32(raw) + 1023) & ~1023u;
-    const uint32_t sk = sm, sq = sm + kTileBytes;
-    uint8_t *gen = raw + (sm - smem_u32(raw));
+struct ScoreItem {
+    int b, h0, nh, k0;      // sequence, KV heads, first key
+    int qa, nq;             // query tiles [qa, qa + nq)
+    int q_len, kv_len;
+};
+// The steps [s, end) of one CTA of an item's cluster, as KV head h and query tile q.
+struct ScoreSteps {
+    int64_t left;
+    int h, q, qa, qz;
+    __device__ __forceinline__ ScoreSteps(const ScoreItem &it, int rank, int cl) {
+        const int64_t steps = (int64_t)it.nh * it.nq, s = steps * rank / cl;
+        left = steps * (rank + 1) / cl - s;
+        qa = it.qa;
+        qz = it.qa + it.nq;
+        h = it.h0 + (it.nq ? (int)(s / it.nq) : 0);
+        q = it.qa + (it.nq ? (int)(s % it.nq) : 0);
+    }
+    // true: the next step is another KV head's
+    __device__ __forceinline__ bool next() {
+        --left;
+        if (++q < qz) return false;
+        q = qa;
+        ++h;
+        return true;
+    }
+};
+__device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int64_t item, int keys, int T,
+                                                bool per_head) {
+    // runs of the first keys, which the most queries see, come first
+    ScoreItem it;
+    const int units = per_head ? a.B * a.Hkv : a.B;
+    const int u = (int)(item % units);
+    it.b = per_head ? u / a.Hkv : u;
+    it.h0 = per_head ? u % a.Hkv : 0;
+    it.nh = per_head ? 1 : a.Hkv;
+    it.k0 = (int)(item / units) * keys;
+    it.q_len = clamped(a.q_len, it.b, a.n_q);
+    it.kv_len = clamped(a.kv_len, it.b, a.n_kv);
+    const int shift = it.kv_len - it.q_len, k_hi = min(it.k0 + keys, it.kv_len) - 1;
+    int lo = max(0, it.k0 - shift), hi = it.q_len;
+    if (it.k0 >= a.sinks) hi = min(hi, k_hi + a.span - shift);
+    it.qa = lo / T;
+    it.nq = k_hi < it.k0 || hi <= lo ? 0 : (hi - 1) / T + 1 - it.qa;
+    return it;
+}
+
+__global__ void __launch_bounds__(kScThreads, 1)
+    span_scores_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kmap, const float *lse, float *scores, int w, int n_win,
+                       int per_head, int64_t items, int cl) {
+    extern __shared__ __align__(1024) uint8_t gen[];
+    ScoreTail &tail = *reinterpret_cast<ScoreTail *>(gen + (4 + kScQ) * kTileBytes);
+    const int T = span_tile_tokens(a.G), rows = T * a.G;
+    const int tk = kTile / w * w;
+    const int rank = blockIdx.x % cl;
+    const int64_t item0 = blockIdx.x / cl, stride = gridDim.x / cl;
+
+    const uint32_t sm = smem_u32(gen), sq = sm + 4 * kTileBytes;
     const int tid = threadIdx.x, warp = tid >> 5;
-    const uint32_t b_l = smem_u32(&bars[0]), b_m = smem_u32(&bars[1]);
+    const uint32_t bar0 = smem_u32(tail.bars);
+    auto k_full = [&](int s) { return bar0 + 8 * s; };
+    auto k_empty = [&](int s) { return bar0 + 16 + 8 * s; };
+    auto q_full = [&](int s) { return bar0 + 32 + 8 * s; };
+    auto q_empty = [&](int s) { return bar0 + 32 + 8 * (kScQ + s); };
+    auto s_full = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 * t + x); };
+    auto s_empty = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + 2 * t + x); };
+    auto l_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
+    auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + kScLs + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 8 + 2 * kScLs);
     if (tid == 0) {
-        tc_mbar_init(b_l, 1);
-        tc_mbar_init(b_m, 1);
-        stop = 0;
+        // s_empty and l_empty: one arrival of each of the warps that read
+        for (int i = 0; i < 4 + 2 * kScQ + 8 + 2 * kScLs + 1; ++i) {
+            const uint32_t bar = bar0 + 8 * i;
+            tc_mbar_init(bar, bar >= s_empty(0, 0) && bar < l_full(0) ? 4 : bar >= l_empty(0) && bar < drained ? 8 : 1);
+        }
+        tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) tc_alloc<128>(smem_u32(&slot));
+    if (warp == 0) tc_alloc<512>(smem_u32(&tail.slot));
+    if (tid < kTile) tail.tok[tid] = tid < rows ? tid / a.G : 255;
+    // rows of a query tile that no query fills stay zero
+    for (int i = tid; i < kScQ * 2 * (kTile - rows) * 8; i += kScThreads) {
+        const int x = i & 7, r = (i >> 3) % (kTile - rows), h = (i >> 3) / (kTile - rows);
+        *reinterpret_cast<int4 *>(gen + 4 * kTileBytes + h * kHalf + (rows + r) * 128 + 16 * x) = make_int4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = slot, lane_tm = tm + ((uint32_t)(warp * 32) << 16);
-    const float c = kLog2e * rsqrtf((float)kHeadDim);
-    const int j = k0 + tid;
-    const bool mine = tid < tk && j < kv_len;
-    float sum = 0.f;
-    uint32_t ph = 0;
+    const uint32_t tm = tail.slot;   // logits of group t, buffer x at column 256 t + 128 x
     bool ok = true;
-    const int h0 = per_head ? blockIdx.z : 0, h1 = per_head ? h0 + 1 : a.Hkv;
-    for (int kvh = h0; kvh < h1 && ok; ++kvh)
-        for (int i0 = i_lo / T * T; i0 < i_hi && ok; i0 += T) {
-            if (tid == 0) {
-                const bool first = i0 == i_lo / T * T;
-                tc_expect_tx(b_l, rows * 256 + (first ? kTileBytes : 0));
-                for (int h = 0; h < 2; ++h) {
-                    if (first) tc_tma_4d(sk + h * kHalf, &kmap, 64 * h, kvh, k0, b, b_l);
-                    tc_tma_4d(sq + h * kHalf, &qmap, 64 * h, kvh * a.G, i0, b, b_l);
+
+    if (warp == 9) {
+        if (tid == 9 * 32) {
+            int nk = 0, nq = 0;   // runs of one KV head and query tiles so far
+            for (int64_t item = item0; item < items && ok; item += stride) {
+                const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+                bool head = true;
+                for (ScoreSteps s(it, rank, cl); s.left > 0; head = s.next()) {
+                    if (head) {
+                        const int set = nk & 1;
+                        if (nk >= 2 && !(ok = tc_wait(k_empty(set), ((nk >> 1) - 1) & 1, &tail.stop))) break;
+                        tc_expect_tx(k_full(set), 2 * kTileBytes);
+                        for (int t = 0; t < 2; ++t)
+                            for (int c = 0; c < 2; ++c)
+                                tc_tma_4d(sm + (2 * set + t) * kTileBytes + c * kHalf, &kmap, 64 * c, s.h, it.k0 + t * tk,
+                                          it.b, k_full(set));
+                        ++nk;
+                    }
+                    const int q = nq % kScQ;
+                    if (nq >= kScQ && !(ok = tc_wait(q_empty(q), (nq / kScQ - 1) & 1, &tail.stop))) break;
+                    tc_expect_tx(q_full(q), rows * 256);
+                    for (int c = 0; c < 2; ++c)
+                        tc_tma_4d(sq + q * kTileBytes + c * kHalf, &qmap, 64 * c, s.h * a.G, s.q * T, it.b, q_full(q));
+                    ++nq;
                 }
             }
-            {
-                const int i = i0 + tid / a.G;
-                const bool v = tid < rows && i < q_len;
-                ps[tid] = v ? shift + i : -1;
-                ls[tid] = v ? lse[((int64_t)b * a.Hq + kvh * a.G + tid % a.G) * a.n_q + i] * kLog2e : 0.f;
+            if (!ok) {   // gave up: the copies in flight land before the CTA ends
+                const long long t0 = clock64();
+                for (int o = max(0, nk - 2); o < nk; ++o)
+                    while (!tc_try_wait(k_full(o & 1), (o >> 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+                for (int o = max(0, nq - kScQ); o < nq; ++o)
+                    while (!tc_try_wait(q_full(o % kScQ), (o / kScQ) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
             }
-            ok = tc_wait(b_l, ph, &stop);
-            ok = __syncthreads_and(ok);
-            if (!ok) break;
-            if (tid == 0) {
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t o = (s >> 2) * kHalf + (s & 3) * 32;
-                    tc_mma_ss(tm, tc_desc_k(sk + o), tc_desc_k(sq + o), tc_idesc(false), s > 0);
-                }
-                tc_commit(b_m);
-            }
-            ok = tc_wait(b_m, ph, &stop);
-            ph ^= 1;
-            tc_fence_after();
-            for (int q = 0; q < 4; ++q) {
-                float x[32];
-                tc_ld32(lane_tm + 32 * q, x);
-                tc_wait_ld();
-                tc_tie(x);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float y = tc_ex2(fmaf(x[e], c, -ls[32 * q + e]));
-                    if (visible(a, j, ps[32 * q + e])) sum += y;
-                }
-            }
-            tc_fence_before();
-            ok = __syncthreads_and(ok);
         }
-    keys[tid] = mine ? sum : 0.f;
-    __syncthreads();
-    const int win = k0 / w + tid;
-    if (tid < tk / w && win < n_win) {
-        float y = 0.f;
-        for (int e = 0; e < w; ++e) y += keys[tid * w + e];
-        const int u = per_head ? b * a.Hkv + blockIdx.z : b;
-        scores[(int64_t)u * n_win + win] = y / (per_head ? a.G : a.Hq);
+        __syncwarp();
+    } else if (warp == 8) {
+        if (tid == 8 * 32) {
+            int nk = 0, nq = 0;
+            for (int64_t item = item0; item < items && ok; item += stride) {
+                const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+                bool head = true;
+                for (ScoreSteps s(it, rank, cl); s.left > 0;) {
+                    if (head) {
+                        ok = tc_wait(k_full(nk & 1), (nk >> 1) & 1, &tail.stop);
+                        if (!ok) break;
+                        ++nk;
+                    }
+                    const int q = nq % kScQ, set = (nk - 1) & 1;
+                    ok = tc_wait(q_full(q), (nq / kScQ) & 1, &tail.stop);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (nq >= 2) ok = tc_wait(s_empty(t, nq & 1), ((nq >> 1) - 1) & 1, &tail.stop);
+                        if (!ok) break;
+                        tc_fence_after();
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t o = (i >> 2) * kHalf + (i & 3) * 32;
+                            tc_mma_ss(tm + 256 * t + 128 * (nq & 1), tc_desc_k(sm + (2 * set + t) * kTileBytes + o),
+                                      tc_desc_k(sq + q * kTileBytes + o), tc_idesc(false), i > 0);
+                        }
+                        tc_commit(s_full(t, nq & 1));
+                    }
+                    if (!ok) break;
+                    tc_commit(q_empty(q));
+                    head = s.next();
+                    if (head || s.left == 0) tc_commit(k_empty(set));
+                    ++nq;
+                }
+            }
+            if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
+                tc_commit(drained);
+                const long long t0 = clock64();
+                while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        const int lane = tid & 31;
+        int nq = 0;
+        for (int64_t item = item0; item < items; item += stride) {
+            const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+            const float *l0 = lse + (int64_t)it.b * a.Hq * a.n_q;
+            float v[4];
+            auto fetch = [&](const ScoreSteps &s) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = lane + 32 * e, i = s.q * T + r / a.G;
+                    v[e] = s.left > 0 && r < rows && i < it.q_len
+                               ? -kLog2e * __ldg(l0 + (int64_t)(s.h * a.G + r % a.G) * a.n_q + i)
+                               : -INFINITY;
+                }
+            };
+            ScoreSteps s(it, rank, cl);
+            fetch(s);
+            for (; s.left > 0 && ok; ++nq) {
+                const int x = nq % kScLs;
+                float now[4] = {v[0], v[1], v[2], v[3]};
+                s.next();
+                fetch(s);
+                if (nq >= kScLs) ok = __all_sync(~0u, tc_wait(l_empty(x), (nq / kScLs - 1) & 1, &tail.stop));
+                if (!ok) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tail.ls[x][lane + 32 * e] = now[e];
+                __syncwarp();
+                if (lane == 0) tc_arrive(l_full(x));
+            }
+            if (!ok) break;
+        }
+    } else {
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t lane_tm = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t;
+        const float c = kLog2e * rsqrtf((float)kHeadDim);
+        const uint64_t cc = pair2(c, c);
+        int nq = 0;
+        for (int64_t item = item0; item < items; item += stride) {
+            const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+            const int shift = it.kv_len - it.q_len, k0 = it.k0 + t * tk, j = k0 + r;
+            float sum = 0.f;
+            for (ScoreSteps s(it, rank, cl); s.left > 0 && ok; s.next(), ++nq) {
+                const int x = nq & 1, y = nq % kScLs;
+                const int i0 = s.q * T, p_lo = shift + i0;
+                ok = __all_sync(~0u, tc_wait(l_full(y), (nq / kScLs) & 1, &tail.stop) &&
+                                         tc_wait(s_full(t, x), (nq >> 1) & 1, &tail.stop));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tS = lane_tm + 128 * x;
+                const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[y]);
+                uint64_t acc[2] = {0, 0};
+                if (i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks)) {
+                    float v[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_ld32(tS + 32 * q, v[q]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_tie(v[q]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const ulonglong2 lv = l2[8 * q + e / 4];
+                            float u[4];
+                            split2(fma2(pair2(v[q][e], v[q][e + 1]), cc, lv.x), u[0], u[1]);
+                            split2(fma2(pair2(v[q][e + 2], v[q][e + 3]), cc, lv.y), u[2], u[3]);
+                            acc[0] = add2(acc[0], pair2(tc_ex2(u[0]), tc_ex2(u[1])));
+                            acc[1] = add2(acc[1], pair2(tc_ex2(u[2]), tc_ex2(u[3])));
+                        }
+                } else {   // some pair is masked: a key at a time looks at its rows' positions
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float v[32];
+                        tc_ld32(tS + 32 * q, v);
+                        tc_wait_ld();
+                        tc_tie(v);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const uchar4 tv = *reinterpret_cast<const uchar4 *>(&tail.tok[32 * q + e]);
+                            const int tok[4] = {tv.x, tv.y, tv.z, tv.w};
+                            const ulonglong2 lv = l2[8 * q + e / 4];
+                            float u[4];
+                            split2(fma2(pair2(v[e], v[e + 1]), cc, lv.x), u[0], u[1]);
+                            split2(fma2(pair2(v[e + 2], v[e + 3]), cc, lv.y), u[2], u[3]);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                u[z] = tok[z] < T && i0 + tok[z] < it.q_len && visible(a, j, p_lo + tok[z]) ? tc_ex2(u[z])
+                                                                                                            : 0.f;
+                            acc[0] = add2(acc[0], pair2(u[0], u[1]));
+                            acc[1] = add2(acc[1], pair2(u[2], u[3]));
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                }
+                __syncwarp();
+                if ((tid & 31) == 0) tc_arrive(l_empty(y));
+                float s0, s1;
+                split2(add2(acc[0], acc[1]), s0, s1);
+                sum += s0 + s1;
+            }
+            // 16 keys at a time (a window is a multiple of 16), then the windows
+            if (r >= tk || j >= it.kv_len) sum = 0.f;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            if ((r & 15) == 0) tail.segs[t][r >> 4] = sum;
+            asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
+            const int win = k0 / w + r;
+            if (r < tk / w) {
+                float y = 0.f;
+                for (int e = 0; e < w / 16; ++e) y += tail.segs[t][r * (w / 16) + e];
+                tail.wins[t][r] = y;
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
+            if (cl > 1) {
+                __syncwarp();
+                cl_sync();
+            }
+            if (rank == 0 && r < tk / w && win < n_win) {
+                float y = tail.wins[t][r];
+                for (int x = 1; x < cl; ++x) y += cl_ld1(cl_addr(smem_u32(&tail.wins[t][r]), x));
+                const int u = per_head ? it.b * a.Hkv + it.h0 : it.b;
+                scores[(int64_t)u * n_win + win] = y / (per_head ? a.G : a.Hq);
+            }
+            if (cl > 1) {
+                __syncwarp();
+                cl_sync();
+            }
+        }
     }
-    if (tid == 0 && !ok) set_status(C, QEVICT_ERR_TIMEOUT, layer, b, k0);
+    if (cl > 1 && warp >= 8) {   // clusters take one item
+        cl_sync();
+        cl_sync();
+    }
+    __syncwarp();
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tc_free<128>(tm);
-    (void)gen;
+    if (tid == 0 && tail.stop) set_status(C, QEVICT_ERR_TIMEOUT, layer, 0, 0);
+    if (warp == 0) tc_free<512>(tm);
 }
 
 }  // namespace
@@ -551,16 +783,40 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
                                const CUtensorMap &kmap, const float *lse, float *scores, int w, bool per_head,
                                int num_sms, cudaStream_t s) {
-    constexpr int smem = 2 * kTileBytes + 1024;
     cudaError_t e = once_per_device(0, [&] {
-        return cudaFuncSetAttribute(span_scores_simple, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t r =
+            cudaFuncSetAttribute(span_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScSmem);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(span_scores_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return r;
     });
     if (e != cudaSuccess) return e;
-    const int tk = kTile / w * w;
-    const int n_win = (a.n_kv + w - 1) / w;
-    const dim3 grid((a.n_kv + tk - 1) / tk, a.B, per_head ? a.Hkv : 1);
-    span_scores_simple<<<grid, 128, smem, s>>>(a, C, layer, qmap, kmap, lse, scores, w, n_win, per_head);
-    return cudaGetLastError();
+    const int keys = 2 * (kTile / w * w), T = span_tile_tokens(a.G);
+    const int runs = (a.n_kv + keys - 1) / keys, n_win = (a.n_kv + w - 1) / w;
+    const int64_t items = (int64_t)runs * (per_head ? a.B * a.Hkv : a.B);
+    // steps of the longest item
+    const int64_t seen = a.sinks > 0 || a.span >= a.n_q ? a.n_q : (int64_t)a.span + keys < a.n_q ? a.span + keys : a.n_q;
+    const int64_t steps = ((seen + T - 1) / T) * (per_head ? 1 : a.Hkv);
+    int cl = 1;
+    while (cl < 8 && items * cl * 2 <= 4 * num_sms && steps >= 2 * cl) cl *= 2;
+    int64_t grid = items * cl;
+    if (cl == 1 && grid > num_sms) grid = num_sms;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kScThreads);
+    cfg.dynamicSmemBytes = kScSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cl;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    if (cl > 1) {
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, span_scores_kernel, a, C, layer, qmap, kmap, lse, scores, w, n_win, per_head ? 1 : 0,
+                              items, cl);
 }
 
 }  // namespace qevict
