@@ -4,6 +4,7 @@
 // key j iff j <= p and (j > p - span or j < sinks).
 #include "qevict_tc.cuh"
 
+#include <limits.h>
 #include <math.h>
 
 namespace qevict {
@@ -407,17 +408,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // fetches the rows' log-sum-exps. Two logit tiles per group alternate.
 constexpr int kScThreads = kSoftmax + 96;
 constexpr int kScLs = 4;                      // steps whose log-sum-exps are in shared memory
-constexpr int kScQ = 3;                       // query tile slots; the keys have two sets of two tiles
+constexpr int kScK = 2;                       // sets of two key tiles
+constexpr int kScQ = 7 - 2 * kScK;            // query tile slots
 // what lies behind the tiles in shared memory
 struct ScoreTail {
     float ls[kScLs][kTile];     // of a step's rows: -lse in log2 units
     float segs[2][8], wins[2][8];   // masses of 16 keys, and of windows
     uint64_t bars[4 + 2 * kScQ + 8 + 2 * kScLs + 1];
-    uint8_t tok[kTile];         // token of a query tile's row, 255 for the rows past the last
     uint32_t slot;
     int stop;
 };
-constexpr int kScSmem = (4 + kScQ) * kTileBytes + (int)sizeof(ScoreTail);
+constexpr int kScSmem = (2 * kScK + kScQ) * kTileBytes + (int)sizeof(ScoreTail);
 static_assert(kScSmem <= 227 * 1024, "shared memory of one CTA");
 
 struct ScoreItem {
@@ -471,13 +472,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
                        const __grid_constant__ CUtensorMap kmap, const float *lse, float *scores, int w, int n_win,
                        int per_head, int64_t items, int cl) {
     extern __shared__ __align__(1024) uint8_t gen[];
-    ScoreTail &tail = *reinterpret_cast<ScoreTail *>(gen + (4 + kScQ) * kTileBytes);
+    ScoreTail &tail = *reinterpret_cast<ScoreTail *>(gen + (2 * kScK + kScQ) * kTileBytes);
     const int T = span_tile_tokens(a.G), rows = T * a.G;
     const int tk = kTile / w * w;
     const int rank = blockIdx.x % cl;
     const int64_t item0 = blockIdx.x / cl, stride = gridDim.x / cl;
 
-    const uint32_t sm = smem_u32(gen), sq = sm + 4 * kTileBytes;
+    const uint32_t sm = smem_u32(gen), sq = sm + 2 * kScK * kTileBytes;
     const int tid = threadIdx.x, warp = tid >> 5;
     const uint32_t bar0 = smem_u32(tail.bars);
     auto k_full = [&](int s) { return bar0 + 8 * s; };
@@ -499,11 +500,10 @@ __global__ void __launch_bounds__(kScThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tc_alloc<512>(smem_u32(&tail.slot));
-    if (tid < kTile) tail.tok[tid] = tid < rows ? tid / a.G : 255;
     // rows of a query tile that no query fills stay zero
     for (int i = tid; i < kScQ * 2 * (kTile - rows) * 8; i += kScThreads) {
         const int x = i & 7, r = (i >> 3) % (kTile - rows), h = (i >> 3) / (kTile - rows);
-        *reinterpret_cast<int4 *>(gen + 4 * kTileBytes + h * kHalf + (rows + r) * 128 + 16 * x) = make_int4(0, 0, 0, 0);
+        *reinterpret_cast<int4 *>(gen + 2 * kScK * kTileBytes + h * kHalf + (rows + r) * 128 + 16 * x) = make_int4(0, 0, 0, 0);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 bool head = true;
                 for (ScoreSteps s(it, rank, cl); s.left > 0; head = s.next()) {
                     if (head) {
-                        const int set = nk & 1;
-                        if (nk >= 2 && !(ok = tc_wait(k_empty(set), ((nk >> 1) - 1) & 1, &tail.stop))) break;
+                        const int set = nk % kScK;
+                        if (nk >= kScK && !(ok = tc_wait(k_empty(set), (nk / kScK - 1) & 1, &tail.stop))) break;
                         tc_expect_tx(k_full(set), 2 * kTileBytes);
                         for (int t = 0; t < 2; ++t)
                             for (int c = 0; c < 2; ++c)
@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
             }
             if (!ok) {   // gave up: the copies in flight land before the CTA ends
                 const long long t0 = clock64();
-                for (int o = max(0, nk - 2); o < nk; ++o)
-                    while (!tc_try_wait(k_full(o & 1), (o >> 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+                for (int o = max(0, nk - kScK); o < nk; ++o)
+                    while (!tc_try_wait(k_full(o % kScK), (o / kScK) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
                 for (int o = max(0, nq - kScQ); o < nq; ++o)
                     while (!tc_try_wait(q_full(o % kScQ), (o / kScQ) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
             }
@@ -554,11 +554,11 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 bool head = true;
                 for (ScoreSteps s(it, rank, cl); s.left > 0;) {
                     if (head) {
-                        ok = tc_wait(k_full(nk & 1), (nk >> 1) & 1, &tail.stop);
+                        ok = tc_wait(k_full(nk % kScK), (nk / kScK) & 1, &tail.stop);
                         if (!ok) break;
                         ++nk;
                     }
-                    const int q = nq % kScQ, set = (nk - 1) & 1;
+                    const int q = nq % kScQ, set = (nk - 1) % kScK;
                     ok = tc_wait(q_full(q), (nq / kScQ) & 1, &tail.stop);
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (nq >= 2) ok = tc_wait(s_empty(t, nq & 1), ((nq >> 1) - 1) & 1, &tail.stop);
@@ -586,36 +586,50 @@ __global__ void __launch_bounds__(kScThreads, 1)
         }
         __syncwarp();
     } else if (warp == 10) {
+        // each lane has four of a query tile's rows; the loads run kAhead steps ahead of the stores
+        constexpr int kAhead = 4;
         const int lane = tid & 31;
+        int tok[4];
+        int64_t off[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = lane + 32 * e;
+            tok[e] = r < rows ? r / a.G : INT_MAX / 2;
+            off[e] = (int64_t)(r % a.G) * a.n_q + r / a.G;
+        }
         int nq = 0;
-        for (int64_t item = item0; item < items; item += stride) {
+        for (int64_t item = item0; item < items && ok; item += stride) {
             const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
             const float *l0 = lse + (int64_t)it.b * a.Hq * a.n_q;
-            float v[4];
-            auto fetch = [&](const ScoreSteps &s) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = lane + 32 * e, i = s.q * T + r / a.G;
-                    v[e] = s.left > 0 && r < rows && i < it.q_len
-                               ? -kLog2e * __ldg(l0 + (int64_t)(s.h * a.G + r % a.G) * a.n_q + i)
-                               : -INFINITY;
-                }
-            };
+            const int64_t head = (int64_t)a.G * a.n_q;
             ScoreSteps s(it, rank, cl);
-            fetch(s);
-            for (; s.left > 0 && ok; ++nq) {
-                const int x = nq % kScLs;
-                float now[4] = {v[0], v[1], v[2], v[3]};
-                s.next();
-                fetch(s);
-                if (nq >= kScLs) ok = __all_sync(~0u, tc_wait(l_empty(x), (nq / kScLs - 1) & 1, &tail.stop));
-                if (!ok) break;
+            int64_t left = s.left;
+            float v[kAhead][4];
+            auto fetch = [&](float (&w)[4]) {
+                if (s.left <= 0) return;
+                const float *p = l0 + s.h * head + s.q * T;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tail.ls[x][lane + 32 * e] = now[e];
-                __syncwarp();
-                if (lane == 0) tc_arrive(l_full(x));
+                for (int e = 0; e < 4; ++e) w[e] = tok[e] < it.q_len - s.q * T ? __ldg(p + off[e]) : INFINITY;
+                s.next();
+            };
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) fetch(v[u]);
+            while (left > 0 && ok) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (left <= 0) break;
+                    const int x = nq % kScLs;
+                    if (nq >= kScLs) ok = ok && __all_sync(~0u, tc_wait(l_empty(x), (nq / kScLs - 1) & 1, &tail.stop));
+                    if (!ok) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tail.ls[x][lane + 32 * e] = -kLog2e * v[u][e];
+                    __syncwarp();
+                    if (lane == 0) tc_arrive(l_full(x));
+                    fetch(v[u]);
+                    --left;
+                    ++nq;
+                }
             }
-            if (!ok) break;
         }
     } else {
         const int t = warp >> 2, r = tid & 127;
@@ -637,16 +651,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 const uint32_t tS = lane_tm + 128 * x;
                 const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[y]);
                 uint64_t acc[2] = {0, 0};
-                if (i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks)) {
-                    float v[4][32];
+                float v[4][32];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tc_ld32(tS + 32 * q, v[q]);
-                    tc_wait_ld();
+                for (int q = 0; q < 4; ++q) tc_ld32(tS + 32 * q, v[q]);
+                tc_wait_ld();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tc_tie(v[q]);
-                    tc_fence_before();
-                    __syncwarp();
-                    if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                for (int q = 0; q < 4; ++q) tc_tie(v[q]);
+                tc_fence_before();
+                __syncwarp();
+                if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                auto masses = [&](auto seen) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -655,35 +669,20 @@ __global__ void __launch_bounds__(kScThreads, 1)
                             float u[4];
                             split2(fma2(pair2(v[q][e], v[q][e + 1]), cc, lv.x), u[0], u[1]);
                             split2(fma2(pair2(v[q][e + 2], v[q][e + 3]), cc, lv.y), u[2], u[3]);
-                            acc[0] = add2(acc[0], pair2(tc_ex2(u[0]), tc_ex2(u[1])));
-                            acc[1] = add2(acc[1], pair2(tc_ex2(u[2]), tc_ex2(u[3])));
-                        }
-                } else {   // some pair is masked: a key at a time looks at its rows' positions
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float v[32];
-                        tc_ld32(tS + 32 * q, v);
-                        tc_wait_ld();
-                        tc_tie(v);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const uchar4 tv = *reinterpret_cast<const uchar4 *>(&tail.tok[32 * q + e]);
-                            const int tok[4] = {tv.x, tv.y, tv.z, tv.w};
-                            const ulonglong2 lv = l2[8 * q + e / 4];
-                            float u[4];
-                            split2(fma2(pair2(v[e], v[e + 1]), cc, lv.x), u[0], u[1]);
-                            split2(fma2(pair2(v[e + 2], v[e + 3]), cc, lv.y), u[2], u[3]);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                u[z] = tok[z] < T && i0 + tok[z] < it.q_len && visible(a, j, p_lo + tok[z]) ? tc_ex2(u[z])
-                                                                                                            : 0.f;
+                            for (int z = 0; z < 4; ++z) u[z] = tc_ex2(seen(32 * q + e + z) ? u[z] : -INFINITY);
                             acc[0] = add2(acc[0], pair2(u[0], u[1]));
                             acc[1] = add2(acc[1], pair2(u[2], u[3]));
                         }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                };
+                if (i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks)) {
+                    masses([](int) { return true; });
+                } else {
+                    // the queries that see key j are a run of positions, so a run of columns
+                    const int first = min(max(0, j - p_lo), T);
+                    const int end = min(min(it.q_len - i0, T), j < a.sinks ? T : j + a.span - p_lo);
+                    const unsigned c0 = first * a.G, n = max(0, end - first) * a.G;
+                    masses([&](int col) { return (unsigned)col - c0 < n; });
                 }
                 __syncwarp();
                 if ((tid & 31) == 0) tc_arrive(l_empty(y));
