@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     constexpr int QT = SPLIT ? 1 : 2;              // query tiles of the CTA
     constexpr int NS = kAttSlots - QT;             // ring slots
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * NS + 7];
+    __shared__ uint64_t bars[2 * NS + 9];
     __shared__ uint32_t slot;
     __shared__ int stop;
 
@@ -93,16 +93,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t sm = (smem_u32(raw) + 1023) & ~1023u;
     uint8_t *gen = raw + (sm - smem_u32(raw));
     const uint32_t ring = sm + QT * kTileBytes;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8 * s; };
     auto empty = [&](int s) { return bar0 + 8 * (NS + s); };
     auto s_full = [&](int t) { return bar0 + 8 * (2 * NS + t); };
-    auto p_full = [&](int t) { return bar0 + 8 * (2 * NS + 2 + t); };
-    auto o_full = [&](int t) { return bar0 + 8 * (2 * NS + 4 + t); };
-    const uint32_t q_full = bar0 + 8 * (2 * NS + 6);
+    auto p_full = [&](int t, int h) { return bar0 + 8 * (2 * NS + 5 + 2 * t + h); };   // h: half of the keys
+    auto o_full = [&](int t) { return bar0 + 8 * (2 * NS + 2 + t); };
+    const uint32_t q_full = bar0 + 8 * (2 * NS + 4);
     if (tid == 0) {
-        for (int i = 0; i < 2 * NS + 7; ++i) tc_mbar_init(bar0 + 8 * i, i == 2 * NS + 2 || i == 2 * NS + 3 ? 4 : 1);
+        for (int i = 0; i < 2 * NS + 9; ++i) tc_mbar_init(bar0 + 8 * i, i >= 2 * NS + 5 ? 4 : 1);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -141,53 +141,73 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 }
             }
         }
-        if (tid == 8 * 32 && n > 0) {
-            bool ok = tc_wait(q_full, 0, &stop);
-            auto logits = [&](int t, int j) {   // S_t = Q K_j^T
-                const uint32_t k = ring + k_item(j) % NS * kTileBytes, q = sm + (SPLIT ? 0 : t * kTileBytes);
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t o = (s >> 2) * kHalf + (s & 3) * 32;
-                    tc_mma_ss(tm + 128 * t, tc_desc_k(q + o), tc_desc_k(k + o), tc_idesc(false), s > 0);
-                }
-                tc_commit(s_full(t));
-            };
-            auto wait_item = [&](int i) {
-                ok = ok && tc_wait(full(i % NS), (i / NS) & 1, &stop);
+        if (warp == 8 && n > 0) {   // the whole warp keeps step, one lane issues
+            const bool lead = tc_elect();
+            const uint32_t tmu = __shfl_sync(~0u, tm, 0);
+            const int nu = __shfl_sync(~0u, n, 0);
+            bool ok = true;
+            auto wait = [&](uint32_t bar, int parity) {
+                ok = __all_sync(~0u, tc_wait(bar, parity, &stop));
                 return ok;
             };
-            if (wait_item(k_item(0))) {
-                logits(0, 0);
-                if (!SPLIT) logits(1, 0);
-                tc_commit(empty(k_item(0) % NS));
-            }
-            if (SPLIT && n > 1 && wait_item(k_item(1))) {
-                logits(1, 1);
-                tc_commit(empty(k_item(1) % NS));
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                if (!wait_item(v_item(j))) break;
-                const uint32_t v = ring + v_item(j) % NS * kTileBytes;
-                const int ahead = SPLIT ? j + 2 : j + 1;
-                for (int x = 0; x < QT && ok; ++x) {
-                    const int t = SPLIT ? j & 1 : x;
-                    ok = tc_wait(p_full(t), (SPLIT ? j >> 1 : j) & 1, &stop);
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (int s = 0; s < 8; ++s)
-                        tc_mma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * s, tc_desc_mn(v + s * 2048, kHalf), tc_idesc(true),
-                                  j >= (SPLIT ? 2 : 1) || s > 0);
-                    if (x == QT - 1) tc_commit(empty(v_item(j) % NS));
-                    if (ahead < n) {
-                        if (!wait_item(k_item(ahead))) break;
-                        logits(t, ahead);
-                        if (x == QT - 1) tc_commit(empty(k_item(ahead) % NS));
-                    } else {
-                        tc_commit(o_full(t));
-                    }
+            auto commit = [&](uint32_t bar) {
+                if (lead) tc_commit(bar);
+            };
+            // The ring slots of the next key tile for S and of the next value tile; a slot's parity flips as it wraps.
+            int ks = k_item(0), kp = 0, vs = SPLIT && nu > 1 ? 2 : 1, vp = 0;
+            auto ahead_of = [&](int &slot_, int &par, int by) {
+                slot_ += by;
+                if (slot_ >= NS) slot_ -= NS, par ^= 1;
+            };
+            auto logits = [&](int t) {   // S_t = Q K^T
+                if (lead) tc_mma_tile(tmu + 128 * t, sm + (SPLIT ? 0 : t * kTileBytes), ring + ks * kTileBytes, kHalf);
+                commit(s_full(t));
+            };
+            if (wait(q_full, 0) && wait(full(0), 0)) {
+                logits(0);
+                if (!SPLIT) logits(1);
+                commit(empty(0));
+                ahead_of(ks, kp, SPLIT ? 1 : 2);
+                if (SPLIT && nu > 1 && wait(full(ks), kp)) {
+                    logits(1);
+                    commit(empty(ks));
+                    ahead_of(ks, kp, 2);
                 }
             }
+            for (int j = 0; j < nu && ok; ++j) {
+                if (!wait(full(vs), vp)) break;
+                const uint32_t v = tc_desc_mn(ring + vs * kTileBytes, kHalf);
+                const bool more = j + (SPLIT ? 2 : 1) < nu;
+#pragma unroll
+                for (int x = 0; x < QT; ++x) {
+                    const int t = SPLIT ? j & 1 : x, par = (SPLIT ? j >> 1 : j) & 1;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!ok || !wait(p_full(t, h), par)) break;
+                        tc_fence_after();
+                        if (lead) {
+#pragma unroll
+                            for (int s = 4 * h; s < 4 * h + 4; ++s)
+                                tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true),
+                                          s > 0 || j >= (SPLIT ? 2 : 1));
+                        }
+                    }
+                    if (!ok) break;
+                    if (x == QT - 1) commit(empty(vs));
+                    if (more) {
+                        if (x == 0 && !wait(full(ks), kp)) break;
+                        logits(t);
+                        if (x == QT - 1) commit(empty(ks));
+                    } else {
+                        commit(o_full(t));
+                    }
+                }
+                if (more) ahead_of(ks, kp, 2);
+                // split: the last value tile follows its predecessor directly
+                ahead_of(vs, vp, SPLIT && j == nu - 2 ? 1 : 2);
+            }
             if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
-                tc_commit(q_full);
+                commit(q_full);
                 const long long t0 = clock64();
                 while (!tc_try_wait(q_full, 1) && clock64() - t0 < kDefaultWaitCycles) {}
             }
@@ -216,25 +236,28 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const int k0 = tl.key(first + j);
-            float x[4][32];
+            const bool masked = masked_tile(a, k0, g_lo, g_hi);
+            const int hi = pos - k0, lo = hi - a.span, sk = a.sinks - k0;
+            float x[4][32], mx[4];
+            tc_ld32(tS, x[0]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tc_ld32(tS + 32 * q, x[q]);
-            tc_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tc_tie(x[q]);
-            if (masked_tile(a, k0, g_lo, g_hi)) {
-                const int hi = pos - k0, lo = hi - a.span, sk = a.sinks - k0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) {   // the maximum of a quarter is taken while the next is on its way
+                tc_wait_ld();
+                tc_tie(x[q]);
+                if (q < 3) tc_ld32(tS + 32 * (q + 1), x[q + 1]);
+                if (masked) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (32 * q + e > hi || (32 * q + e <= lo && 32 * q + e >= sk)) x[q][e] = -INFINITY;
+                }
+                float y[2] = {fmaxf(x[q][0], x[q][1]), fmaxf(x[q][2], x[q][3])};
+#pragma unroll
+                for (int e = 4; e < 32; e += 4) {
+                    y[0] = max3(y[0], x[q][e], x[q][e + 1]);
+                    y[1] = max3(y[1], x[q][e + 2], x[q][e + 3]);
+                }
+                mx[q] = fmaxf(y[0], y[1]);
             }
-            float mx[4] = {x[0][0], x[1][0], x[2][0], x[3][0]};
-#pragma unroll
-            for (int e = 1; e < 32; ++e)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], x[q][e]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // The reference follows the maximum only when it has grown by more than
             // kRescale in the exponent: probabilities stay below 2^kRescale, and O is
@@ -257,27 +280,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                 }
             }
-            const float mc = m == -INFINITY ? 0.f : -m * c;
-            const uint64_t mm = pair2(mc, mc);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float u, v;
-                    split2(fma2(pair2(x[q][2 * e], x[q][2 * e + 1]), cc, mm), u, v);
-                    u = tc_ex2(u);
-                    v = tc_ex2(v);
-                    sum[e & 1] = add2(sum[e & 1], pair2(u, v));
-                    const __nv_bfloat162 pk = __floats2bfloat162_rn(u, v);
-                    p[e] = *reinterpret_cast<const uint32_t *>(&pk);
-                }
-                tc_st16(tS + 16 * q, p);
-            }
-            float s0, s1;
-            split2(add2(sum[0], sum[1]), s0, s1);
-            l += s0 + s1;
             // Values of keys that no row of the CTA sees may be anything: as zeros they stay out of the product.
             if ((SPLIT || t == 0) && (k0 + kTile - 1 > p_hi || (k0 <= p_lo - a.span && k0 + kTile > a.sinks))) {
                 const int i = v_item(j), s = i % NS;
@@ -294,10 +296,34 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
             }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if ((tid & 31) == 0) tc_arrive(p_full(t));
+            const float mc = m == -INFINITY ? 0.f : -m * c;
+            const uint64_t mm = pair2(mc, mc);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // the product starts on the first half of the keys
+#pragma unroll
+                for (int q = 2 * h; q < 2 * h + 2; ++q) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float u, v;
+                        split2(fma2(pair2(x[q][2 * e], x[q][2 * e + 1]), cc, mm), u, v);
+                        u = tc_ex2(u);
+                        v = tc_ex2(v);
+                        sum[e & 1] = add2(sum[e & 1], pair2(u, v));
+                        const __nv_bfloat162 pk = __floats2bfloat162_rn(u, v);
+                        p[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                    }
+                    tc_st16(tS + 16 * q, p);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if ((tid & 31) == 0) tc_arrive(p_full(t, h));
+            }
+            float s0, s1;
+            split2(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
         }
         if (ok && done > 0) ok = __all_sync(~0u, tc_wait(o_full(t), 0, &stop));
         tc_fence_after();
@@ -479,7 +505,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     const int64_t item0 = blockIdx.x / cl, stride = gridDim.x / cl;
 
     const uint32_t sm = smem_u32(gen), sq = sm + 2 * kScK * kTileBytes;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
     const uint32_t bar0 = smem_u32(tail.bars);
     auto k_full = [&](int s) { return bar0 + 8 * s; };
     auto k_empty = [&](int s) { return bar0 + 16 + 8 * s; };
@@ -547,42 +573,45 @@ __global__ void __launch_bounds__(kScThreads, 1)
         }
         __syncwarp();
     } else if (warp == 8) {
-        if (tid == 8 * 32) {
-            int nk = 0, nq = 0;
-            for (int64_t item = item0; item < items && ok; item += stride) {
-                const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
-                bool head = true;
-                for (ScoreSteps s(it, rank, cl); s.left > 0;) {
-                    if (head) {
-                        ok = tc_wait(k_full(nk % kScK), (nk / kScK) & 1, &tail.stop);
-                        if (!ok) break;
-                        ++nk;
-                    }
-                    const int q = nq % kScQ, set = (nk - 1) % kScK;
-                    ok = tc_wait(q_full(q), (nq / kScQ) & 1, &tail.stop);
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (nq >= 2) ok = tc_wait(s_empty(t, nq & 1), ((nq >> 1) - 1) & 1, &tail.stop);
-                        if (!ok) break;
-                        tc_fence_after();
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t o = (i >> 2) * kHalf + (i & 3) * 32;
-                            tc_mma_ss(tm + 256 * t + 128 * (nq & 1), tc_desc_k(sm + (2 * set + t) * kTileBytes + o),
-                                      tc_desc_k(sq + q * kTileBytes + o), tc_idesc(false), i > 0);
-                        }
-                        tc_commit(s_full(t, nq & 1));
-                    }
-                    if (!ok) break;
-                    tc_commit(q_empty(q));
-                    head = s.next();
-                    if (head || s.left == 0) tc_commit(k_empty(set));
-                    ++nq;
+        // the whole warp keeps step, one lane issues
+        const bool lead = tc_elect();
+        const uint32_t tmu = __shfl_sync(~0u, tm, 0);
+        auto wait = [&](uint32_t bar, int parity) {
+            ok = ok && __all_sync(~0u, tc_wait(bar, parity, &tail.stop));
+            return ok;
+        };
+        int set = kScK - 1, kp = 1, qs = 0, qp = 0, buf = 0, sp = 1;   // slots and their parities
+        for (int64_t item = item0; item < items && ok; item += stride) {
+            const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+            bool head = true;
+            for (ScoreSteps s(it, rank, cl); s.left > 0;) {
+                if (head) {
+                    if (++set == kScK) set = 0, kp ^= 1;
+                    if (!wait(k_full(set), kp)) break;
                 }
+                if (!wait(q_full(qs), qp)) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || !wait(s_empty(t, buf), sp)) break;   // passes at once for the first of each buffer
+                    tc_fence_after();
+                    if (lead) {
+                        tc_mma_tile(tmu + 256 * t + 128 * buf, sm + (2 * set + t) * kTileBytes, sq + qs * kTileBytes, kHalf);
+                        tc_commit(s_full(t, buf));
+                    }
+                }
+                if (!ok) break;
+                if (lead) tc_commit(q_empty(qs));
+                head = s.next();
+                if (lead && (head || s.left == 0)) tc_commit(k_empty(set));
+                if (++qs == kScQ) qs = 0, qp ^= 1;
+                buf ^= 1;
+                sp ^= buf == 0;
             }
-            if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
-                tc_commit(drained);
-                const long long t0 = clock64();
-                while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
-            }
+        }
+        if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
+            if (lead) tc_commit(drained);
+            const long long t0 = clock64();
+            while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
         }
         __syncwarp();
     } else if (warp == 10) {

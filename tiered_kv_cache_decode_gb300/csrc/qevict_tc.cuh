@@ -76,34 +76,46 @@ __device__ __forceinline__ void tc_free(uint32_t addr) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS) : "memory");
 }
 
-// Shared-memory operand descriptors, 128-byte swizzle. K-major: rows of 64
-// channels (128 B), 8-row groups 1024 B apart. MN-major (rows run along K):
-// 8-row groups along K 1024 B apart, blocks of 64 along M or N `lead` B apart.
-constexpr uint64_t kDescBase = (uint64_t(1) << 46) | (uint64_t(2) << 61) | (uint64_t(1024 >> 4) << 32);
-__device__ __forceinline__ uint64_t tc_desc_k(uint32_t addr) {
-    return kDescBase | (uint64_t(1) << 16) | ((addr & 0x3ffff) >> 4);
-}
-__device__ __forceinline__ uint64_t tc_desc_mn(uint32_t addr, uint32_t lead) {
-    return kDescBase | (uint64_t(lead >> 4) << 16) | ((addr & 0x3ffff) >> 4);
+// Shared-memory operand descriptors, 128-byte swizzle, as their low words (the
+// high word is kDescHi). K-major: rows of 64 channels (128 B), 8-row groups 1024
+// B apart. MN-major (rows run along K): 8-row groups along K 1024 B apart,
+// blocks of 64 along M or N `lead` B apart.
+constexpr uint32_t kDescHi = (1u << 14) | (2u << 29) | (1024u >> 4);
+__device__ __forceinline__ uint32_t tc_desc_k(uint32_t addr) { return (1u << 16) | ((addr & 0x3ffff) >> 4); }
+__device__ __forceinline__ uint32_t tc_desc_mn(uint32_t addr, uint32_t lead) {
+    return ((lead >> 4) << 16) | ((addr & 0x3ffff) >> 4);
 }
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 128, N = 128; B MN-major or K-major.
 __host__ __device__ constexpr uint32_t tc_idesc(bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// D (+)= A B over K = 16, A in shared (ss) or tensor (ts) memory. One lane issues
+// them inside a warp that is otherwise of one mind: with operands that are the
+// same in every lane they come out of uniform registers, which is what lets an
+// issue keep ahead of the 64 cycles that a 128 x 128 x 16 product takes (from a
+// branch of one thread an issue took 80 to 97 cycles).
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi)
         : "memory");
+}
+// a 128 x 128 x 128 product of two tiles in shared memory, halves of 64 channels `half` bytes apart
+__device__ __forceinline__ void tc_mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t half) {
+    const uint32_t da = tc_desc_k(a), db = tc_desc_k(b), h = half >> 4;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) tc_mma_ss(d, da + (s >> 2) * h + (s & 3) * 2, db + (s >> 2) * h + (s & 3) * 2, tc_idesc(false), s > 0);
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -169,6 +181,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
