@@ -433,14 +433,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // two key tiles, one thread for the products, one for the copies, and a warp that
 // fetches the rows' log-sum-exps. Two logit tiles per group alternate.
 constexpr int kScThreads = kSoftmax + 96;
-constexpr int kScLs = 4;                      // steps whose log-sum-exps are in shared memory
 constexpr int kScK = 2;                       // sets of two key tiles
 constexpr int kScQ = 7 - 2 * kScK;            // query tile slots
 // what lies behind the tiles in shared memory
 struct ScoreTail {
-    float ls[kScLs][kTile];     // of a step's rows: -lse in log2 units
+    float ls[2][kTile];         // of a step's rows: -lse in log2 units
     float segs[2][8], wins[2][8];   // masses of 16 keys, and of windows
-    uint64_t bars[4 + 2 * kScQ + 8 + 2 * kScLs + 1];
+    uint64_t bars[4 + 2 * kScQ + 8 + 3];
     uint32_t slot;
     int stop;
 };
@@ -513,14 +512,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto q_empty = [&](int s) { return bar0 + 32 + 8 * (kScQ + s); };
     auto s_full = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 * t + x); };
     auto s_empty = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + 2 * t + x); };
-    auto l_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
-    auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + kScLs + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 8 + 2 * kScLs);
+    auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 10);
     if (tid == 0) {
-        // s_empty and l_empty: one arrival of each of the warps that read
-        for (int i = 0; i < 4 + 2 * kScQ + 8 + 2 * kScLs + 1; ++i) {
+        // s_full: the product and the log-sum-exps; s_empty and l_empty: each of the warps that read
+        for (int i = 0; i < 4 + 2 * kScQ + 8 + 3; ++i) {
             const uint32_t bar = bar0 + 8 * i;
-            tc_mbar_init(bar, bar >= s_empty(0, 0) && bar < l_full(0) ? 4 : bar >= l_empty(0) && bar < drained ? 8 : 1);
+            tc_mbar_init(bar, bar >= l_empty(0) ? (bar < drained ? 8 : 1) : bar >= s_empty(0, 0) ? 4 : bar >= s_full(0, 0) ? 2 : 1);
         }
         tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -647,13 +645,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     if (left <= 0) break;
-                    const int x = nq % kScLs;
-                    if (nq >= kScLs) ok = ok && __all_sync(~0u, tc_wait(l_empty(x), (nq / kScLs - 1) & 1, &tail.stop));
+                    const int x = nq & 1;
+                    if (nq >= 2) ok = ok && __all_sync(~0u, tc_wait(l_empty(x), ((nq >> 1) - 1) & 1, &tail.stop));
                     if (!ok) break;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) tail.ls[x][lane + 32 * e] = -kLog2e * v[u][e];
                     __syncwarp();
-                    if (lane == 0) tc_arrive(l_full(x));
+                    if (lane < 2) tc_arrive(s_full(lane, x));
                     fetch(v[u]);
                     --left;
                     ++nq;
@@ -671,27 +669,33 @@ __global__ void __launch_bounds__(kScThreads, 1)
             const int shift = it.kv_len - it.q_len, k0 = it.k0 + t * tk, j = k0 + r;
             float sum = 0.f;
             for (ScoreSteps s(it, rank, cl); s.left > 0 && ok; s.next(), ++nq) {
-                const int x = nq & 1, y = nq % kScLs;
+                const int x = nq & 1;
                 const int i0 = s.q * T, p_lo = shift + i0;
-                ok = __all_sync(~0u, tc_wait(l_full(y), (nq / kScLs) & 1, &tail.stop) &&
-                                         tc_wait(s_full(t, x), (nq >> 1) & 1, &tail.stop));
+                ok = __all_sync(~0u, tc_wait(s_full(t, x), (nq >> 1) & 1, &tail.stop));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t tS = lane_tm + 128 * x;
-                const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[y]);
+                const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[x]);
                 uint64_t acc[2] = {0, 0};
                 float v[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc_ld32(tS + 32 * q, v[q]);
-                tc_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc_tie(v[q]);
-                tc_fence_before();
-                __syncwarp();
-                if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                tc_ld32(tS, v[0]);
+                tc_ld32(tS + 32, v[1]);
                 auto masses = [&](auto seen) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q) {
+                        if ((q & 1) == 0) {   // the second half arrives under the first one's exponentials
+                            tc_wait_ld();
+                            tc_tie(v[q]);
+                            tc_tie(v[q + 1]);
+                            if (q == 0) {
+                                tc_ld32(tS + 64, v[2]);
+                                tc_ld32(tS + 96, v[3]);
+                            } else {
+                                tc_fence_before();
+                                __syncwarp();
+                                if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                            }
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const ulonglong2 lv = l2[8 * q + e / 4];
@@ -703,6 +707,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                             acc[0] = add2(acc[0], pair2(u[0], u[1]));
                             acc[1] = add2(acc[1], pair2(u[2], u[3]));
                         }
+                    }
                 };
                 if (i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks)) {
                     masses([](int) { return true; });
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     masses([&](int col) { return (unsigned)col - c0 < n; });
                 }
                 __syncwarp();
-                if ((tid & 31) == 0) tc_arrive(l_empty(y));
+                if ((tid & 31) == 0) tc_arrive(l_empty(x));
                 float s0, s1;
                 split2(add2(acc[0], acc[1]), s0, s1);
                 sum += s0 + s1;
