@@ -429,17 +429,19 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // pairs that see some of them. A cluster of CTAs shares an item's steps
 // evenly and adds its sums in rank order; with one CTA per item the CTAs
 // are persistent and the copies of the next item run under this one.
-// Warps as in the attention: two groups that each take the masses of one of the
-// two key tiles, one thread for the products, one for the copies, and a warp that
-// fetches the rows' log-sum-exps. Two logit tiles per group alternate.
-constexpr int kScThreads = kSoftmax + 96;
+// Four groups of four warps take the masses, each of one key tile in every other
+// step from a logit tile of its own, so that their waits and loads fall at
+// different times; one warp issues the products, one the copies, and one fetches
+// the rows' log-sum-exps.
+constexpr int kScMass = 512;                  // threads of the four groups
+constexpr int kScThreads = kScMass + 96;
 constexpr int kScK = 2;                       // sets of two key tiles
 constexpr int kScQ = 7 - 2 * kScK;            // query tile slots
 // what lies behind the tiles in shared memory
 struct ScoreTail {
     float ls[2][kTile];         // of a step's rows: -lse in log2 units
-    float segs[2][8], wins[2][8];   // masses of 16 keys, and of windows
-    uint64_t bars[4 + 2 * kScQ + 8 + 3];
+    float segs[2][2][8], wins[2][8];   // masses of 16 keys from each step parity, and of windows
+    uint64_t bars[4 + 2 * kScQ + 7];
     uint32_t slot;
     int stop;
 };
@@ -510,15 +512,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto k_empty = [&](int s) { return bar0 + 16 + 8 * s; };
     auto q_full = [&](int s) { return bar0 + 32 + 8 * s; };
     auto q_empty = [&](int s) { return bar0 + 32 + 8 * (kScQ + s); };
-    auto s_full = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 * t + x); };
-    auto s_empty = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + 2 * t + x); };
-    auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 10);
+    auto s_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + x); };
+    auto s_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 + x); };
+    auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 6);
     if (tid == 0) {
-        // s_full: the product and the log-sum-exps; s_empty and l_empty: each of the warps that read
-        for (int i = 0; i < 4 + 2 * kScQ + 8 + 3; ++i) {
+        // s_full: the products and the log-sum-exps; s_empty and l_empty: each of the warps that read
+        for (int i = 0; i < 4 + 2 * kScQ + 7; ++i) {
             const uint32_t bar = bar0 + 8 * i;
-            tc_mbar_init(bar, bar >= l_empty(0) ? (bar < drained ? 8 : 1) : bar >= s_empty(0, 0) ? 4 : bar >= s_full(0, 0) ? 2 : 1);
+            tc_mbar_init(bar, bar == drained ? 1 : bar >= s_empty(0) ? 8 : bar >= s_full(0) ? 2 : 1);
         }
         tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -536,8 +538,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
     const uint32_t tm = tail.slot;   // logits of group t, buffer x at column 256 t + 128 x
     bool ok = true;
 
-    if (warp == 9) {
-        if (tid == 9 * 32) {
+    if (warp == 17) {
+        if (tid == 17 * 32) {
             int nk = 0, nq = 0;   // runs of one KV head and query tiles so far
             for (int64_t item = item0; item < items && ok; item += stride) {
                 const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // the whole warp keeps step, one lane issues
         const bool lead = tc_elect();
         const uint32_t tmu = __shfl_sync(~0u, tm, 0);
@@ -587,18 +589,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     if (++set == kScK) set = 0, kp ^= 1;
                     if (!wait(k_full(set), kp)) break;
                 }
-                if (!wait(q_full(qs), qp)) break;
+                if (!wait(q_full(qs), qp) || !wait(s_empty(buf), sp)) break;   // s_empty passes at once the first time
+                tc_fence_after();
+                if (lead) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || !wait(s_empty(t, buf), sp)) break;   // passes at once for the first of each buffer
-                    tc_fence_after();
-                    if (lead) {
+                    for (int t = 0; t < 2; ++t)
                         tc_mma_tile(tmu + 256 * t + 128 * buf, sm + (2 * set + t) * kTileBytes, sq + qs * kTileBytes, kHalf);
-                        tc_commit(s_full(t, buf));
-                    }
+                    tc_commit(s_full(buf));
+                    tc_commit(q_empty(qs));
                 }
-                if (!ok) break;
-                if (lead) tc_commit(q_empty(qs));
                 head = s.next();
                 if (lead && (head || s.left == 0)) tc_commit(k_empty(set));
                 if (++qs == kScQ) qs = 0, qp ^= 1;
@@ -612,7 +611,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
         }
         __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // each lane has four of a query tile's rows; the loads run kAhead steps ahead of the stores
         constexpr int kAhead = 4;
         const int lane = tid & 31;
@@ -651,7 +650,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) tail.ls[x][lane + 32 * e] = -kLog2e * v[u][e];
                     __syncwarp();
-                    if (lane < 2) tc_arrive(s_full(lane, x));
+                    if (lane == 0) tc_arrive(s_full(x));
                     fetch(v[u]);
                     --left;
                     ++nq;
@@ -659,8 +658,9 @@ __global__ void __launch_bounds__(kScThreads, 1)
             }
         }
     } else {
-        const int t = warp >> 2, r = tid & 127;
-        const uint32_t lane_tm = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t;
+        const int t = warp >> 3, x = (warp >> 2) & 1, r = tid & 127;
+        const uint32_t tS = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t + 128 * x;
+        const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[x]);
         const float c = kLog2e * rsqrtf((float)kHeadDim);
         const uint64_t cc = pair2(c, c);
         int nq = 0;
@@ -669,39 +669,38 @@ __global__ void __launch_bounds__(kScThreads, 1)
             const int shift = it.kv_len - it.q_len, k0 = it.k0 + t * tk, j = k0 + r;
             float sum = 0.f;
             for (ScoreSteps s(it, rank, cl); s.left > 0 && ok; s.next(), ++nq) {
-                const int x = nq & 1;
+                if ((nq & 1) != x) continue;
                 const int i0 = s.q * T, p_lo = shift + i0;
-                ok = __all_sync(~0u, tc_wait(s_full(t, x), (nq >> 1) & 1, &tail.stop));
+                ok = __all_sync(~0u, tc_wait(s_full(x), (nq >> 1) & 1, &tail.stop));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t tS = lane_tm + 128 * x;
-                const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[x]);
                 uint64_t acc[2] = {0, 0};
-                float v[4][32];
+                float v[2][32];
                 tc_ld32(tS, v[0]);
                 tc_ld32(tS + 32, v[1]);
                 auto masses = [&](auto seen) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if ((q & 1) == 0) {   // the second half arrives under the first one's exponentials
+                        if ((q & 1) == 0) {
+                            if (q == 2) {
+                                tc_ld32(tS + 64, v[0]);
+                                tc_ld32(tS + 96, v[1]);
+                            }
                             tc_wait_ld();
-                            tc_tie(v[q]);
-                            tc_tie(v[q + 1]);
-                            if (q == 0) {
-                                tc_ld32(tS + 64, v[2]);
-                                tc_ld32(tS + 96, v[3]);
-                            } else {
+                            tc_tie(v[0]);
+                            tc_tie(v[1]);
+                            if (q == 2) {
                                 tc_fence_before();
                                 __syncwarp();
-                                if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                                if ((tid & 31) == 0) tc_arrive(s_empty(x));
                             }
                         }
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const ulonglong2 lv = l2[8 * q + e / 4];
                             float u[4];
-                            split2(fma2(pair2(v[q][e], v[q][e + 1]), cc, lv.x), u[0], u[1]);
-                            split2(fma2(pair2(v[q][e + 2], v[q][e + 3]), cc, lv.y), u[2], u[3]);
+                            split2(fma2(pair2(v[q & 1][e], v[q & 1][e + 1]), cc, lv.x), u[0], u[1]);
+                            split2(fma2(pair2(v[q & 1][e + 2], v[q & 1][e + 3]), cc, lv.y), u[2], u[3]);
 #pragma unroll
                             for (int z = 0; z < 4; ++z) u[z] = tc_ex2(seen(32 * q + e + z) ? u[z] : -INFINITY);
                             acc[0] = add2(acc[0], pair2(u[0], u[1]));
@@ -728,22 +727,22 @@ __global__ void __launch_bounds__(kScThreads, 1)
             if (r >= tk || j >= it.kv_len) sum = 0.f;
 #pragma unroll
             for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            if ((r & 15) == 0) tail.segs[t][r >> 4] = sum;
-            asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
+            if ((r & 15) == 0) tail.segs[t][x][r >> 4] = sum;
+            asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
             const int win = k0 / w + r;
-            if (r < tk / w) {
+            if (x == 0 && r < tk / w) {
                 float y = 0.f;
-                for (int e = 0; e < w / 16; ++e) y += tail.segs[t][r * (w / 16) + e];
+                for (int e = r * (w / 16); e < (r + 1) * (w / 16); ++e) y += tail.segs[t][0][e] + tail.segs[t][1][e];
                 tail.wins[t][r] = y;
             }
-            asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
+            asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
             if (cl > 1) {
                 __syncwarp();
                 cl_sync();
             }
-            if (rank == 0 && r < tk / w && win < n_win) {
+            if (rank == 0 && x == 0 && r < tk / w && win < n_win) {
                 float y = tail.wins[t][r];
-                for (int x = 1; x < cl; ++x) y += cl_ld1(cl_addr(smem_u32(&tail.wins[t][r]), x));
+                for (int p = 1; p < cl; ++p) y += cl_ld1(cl_addr(smem_u32(&tail.wins[t][r]), p));
                 const int u = per_head ? it.b * a.Hkv + it.h0 : it.b;
                 scores[(int64_t)u * n_win + win] = y / (per_head ? a.G : a.Hq);
             }
@@ -753,7 +752,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             }
         }
     }
-    if (cl > 1 && warp >= 8) {   // clusters take one item
+    if (cl > 1 && warp >= 16) {   // clusters take one item
         cl_sync();
         cl_sync();
     }
