@@ -29,6 +29,7 @@ class Shell(binding.TieredCache):
 
     def __init__(self, B, Hq, Hkv, w):
         self.B, self.Hq, self.Hkv, self.w, self.units, self.device = B, Hq, Hkv, w, B, 0
+        self._dev = torch.device("cuda", 0)
         self.handle = None
 
 
@@ -50,16 +51,19 @@ def test_binding_refuses_wrong_tensors(q, k):
 
 
 def test_token_strides():
-    c = Shell(2, 8, 2, 64)
+    c, one = Shell(2, 8, 2, 64), Shell(1, 8, 2, 64)
+    c._dev = one._dev = torch.device("cpu")   # the layouts alone
     fused = t(2, 5, 12, 128)
-    assert c._token_stride(fused[:, :, :8], 5, 8, "q") == 12 * 128
-    assert c._token_stride(fused[:, :, 8:10], 5, 2, "k") == 12 * 128
-    assert c._token_stride(t(2, 1, 8, 128), 1, 8, "q") == 8 * 128
-    assert c._token_stride(fused[:, 2, :8], 1, 8, "q") == 5 * 12 * 128     # one token of each sequence
-    one = Shell(1, 8, 2, 64)
-    assert one._token_stride(t(1, 1, 8, 128), 1, 8, "q") == 8 * 128
-    assert one._token_stride(t(1, 7, 8, 128)[:, ::2], 4, 8, "q") == 2 * 8 * 128
+    assert c._tokens(fused[:, :, :8], 8, "q") == (5, 12 * 128)
+    assert c._tokens(fused[:, :, 8:10], 2, "k") == (5, 12 * 128)
+    assert c._tokens(t(2, 1, 8, 128), 8, "q") == (1, 8 * 128)
+    assert c._tokens(t(2, 8, 128), 8, "q") == (1, 8 * 128)
+    assert c._tokens(fused[:, 2, :8], 8, "q") == (1, 5 * 12 * 128)     # one token of each sequence
+    assert one._tokens(t(1, 1, 8, 128), 8, "q") == (1, 8 * 128)
+    assert one._tokens(t(1, 7, 8, 128)[:, ::2], 8, "q") == (4, 2 * 8 * 128)
     for bad in (t(2, 9, 8, 128)[:, ::2], fused[:, 1:, :8], t(2, 5, 8, 256)[..., ::2],
                 t(2, 8, 5, 128).transpose(1, 2)):
         with pytest.raises(ValueError):
-            c._token_stride(bad, bad.shape[1], 8, "q")
+            c._tokens(bad, 8, "q")
+    with pytest.raises(ValueError):
+        c._dense(fused[:, :, :8], 8, "q")

@@ -190,6 +190,7 @@ class TieredCache:
         self.units = batch * num_kv_heads if per_head else batch
         self.layers = num_layers
         self.device = torch.cuda.current_device()
+        self._dev = torch.device("cuda", self.device)
         self._alloc = None
         if torch_allocator:
             dev = self.device
@@ -401,78 +402,70 @@ class TieredCache:
         return device_tensor(v.k_group_bits, (v.batch, v.num_kv_heads, 4), "|u1").cpu()
 
     # ---- from projections to the cache ------------------------------------------
-    def _heads(self, t, heads, what, dtype=torch.bfloat16):
-        """Sequences and tokens of a [B][n][heads][128] (or [B][heads][128]) tensor, checked."""
-        if t.dtype is not dtype or t.dim() not in (3, 4) or t.shape[0] != self.B or \
-                t.shape[-2] != heads or t.shape[-1] != HEAD_DIM:
-            raise ValueError(f"{what} must be {dtype} [{self.B}][n][{heads}][{HEAD_DIM}], got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if not t.is_cuda or t.device.index != self.device:
-            raise ValueError(f"{what} must be on cuda:{self.device}")
-        return t.shape[1] if t.dim() == 4 else 1
+    # These run once per layer and token, so their checks read each attribute once.
+    def _tokens(self, t, heads, what):
+        """(tokens, elements between consecutive tokens) of a bf16 [B][n][heads][128] (or, for one token,
+        [B][heads][128]) tensor on the cache's device whose tokens are evenly spaced and dense inside."""
+        sh, st, B = t.shape, t.stride(), self.B
+        if len(sh) == 3:
+            sh, st = (sh[0], 1, sh[1], sh[2]), (st[0], st[0], st[1], st[2])
+        if len(sh) != 4 or sh[0] != B or sh[2] != heads or sh[3] != HEAD_DIM or t.dtype is not torch.bfloat16 or \
+                t.device != self._dev:
+            raise ValueError(f"{what} must be bfloat16 [{B}][n][{heads}][{HEAD_DIM}] on {self._dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        n = sh[1]
+        dense = heads * HEAD_DIM
+        step = st[1] if n > 1 else st[0] if B > 1 else dense
+        if st[3] != 1 or (heads > 1 and st[2] != HEAD_DIM) or (B > 1 and st[0] != n * step):
+            raise ValueError(f"{what}: tokens must be evenly spaced, with dense heads (strides {t.stride()})")
+        return n, step
+
+    def _dense(self, t, heads, what):
+        n, step = self._tokens(t, heads, what)
+        if step != heads * HEAD_DIM:
+            raise ValueError(f"{what} must be dense (strides {t.stride()})")
+        return n
 
     def _side(self, t, shape, dtype, what):
-        """A dense tensor of the given shape and type on the cache's device, or None."""
+        """Address of a dense tensor of the given shape and type on the cache's device, or None."""
         if t is None:
             return None
-        if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda or \
-                t.device.index != self.device:
-            raise ValueError(f"{what} must be dense {dtype} {list(shape)} on cuda:{self.device}, got {t.dtype} "
-                             f"{list(t.shape)}")
+        if t.shape != shape or t.dtype is not dtype or t.device != self._dev or not t.is_contiguous():
+            raise ValueError(f"{what} must be dense {dtype} {list(shape)} on {self._dev}, got {t.dtype} "
+                             f"{list(t.shape)} on {t.device}")
         return t.data_ptr()
 
-    def _token_stride(self, t, n, heads, what):
-        """Elements between consecutive tokens of t, whose tokens must be evenly spaced and dense inside."""
-        s = t.stride()
-        if t.dim() == 4:
-            step = s[1] if n > 1 else s[0]
-            even = t.shape[0] == 1 or s[0] == n * step
-            if n == 1 and t.shape[0] == 1:
-                step = heads * HEAD_DIM
-        else:
-            step, even = (s[0] if t.shape[0] > 1 else heads * HEAD_DIM), True
-        if not even or s[-1] != 1 or (heads > 1 and s[-2] != HEAD_DIM):
-            raise ValueError(f"{what}: tokens must be evenly spaced, with dense heads (strides {s})")
-        return step
+    def _raw_stream(self, stream):
+        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device)
 
     def qk_norm_rope(self, layer, q, k, inv_freq, v=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, q_out=None, k_out=None, v_out=None, stream=None):
         """Head norms and rotation of q [B][n][Hq][128] and k [B][n][Hkv][128] (and a dense copy of v), which
         may be parts of one fused projection; positions int64 [B][n], or None: the layer's length onwards.
         [B][heads][128] tensors are one token. Returns (q, k), or (q, k, v), dense."""
-        n = self._heads(q, self.Hq, "q")
-        ins = [(q, self.Hq, "q", q_out), (k, self.Hkv, "k", k_out)]
+        side, bf = self._side, torch.bfloat16
+        n, qs = self._tokens(q, self.Hq, "q")
+        nk, ks = self._tokens(k, self.Hkv, "k")
+        nv, vs = (n, 0) if v is None else self._tokens(v, self.Hkv, "v")
+        if nk != n or nv != n:
+            raise ValueError(f"q, k and v must have the same tokens, got {n}, {nk} and {nv}")
+        like, dense = torch.empty_like, torch.contiguous_format
+        q_out = like(q, memory_format=dense) if q_out is None else q_out
+        k_out = like(k, memory_format=dense) if k_out is None else k_out
         if v is not None:
-            ins.append((v, self.Hkv, "v", v_out))
+            v_out = like(v, memory_format=dense) if v_out is None else v_out
         elif v_out is not None:
             raise ValueError("v_out without v")
-        steps, outs = [], []
-        for t, heads, what, o in ins:
-            if what != "q" and self._heads(t, heads, what) != n:
-                raise ValueError(f"{what} must have q's {n} tokens")
-            steps.append(self._token_stride(t, n, heads, what))
-            if o is None:
-                o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-            else:
-                self._side(o, tuple(t.shape), torch.bfloat16, what + "_out")
-            outs.append(o)
-        side = self._side
         rc = self.lib.qevict_qk_norm_rope(
-            self.handle, layer, q.data_ptr(), steps[0], k.data_ptr(), steps[1],
-            None if v is None else v.data_ptr(), 0 if v is None else steps[2], n,
-            side(positions, (self.B, n), torch.int64, "positions"),
-            side(q_weight, (HEAD_DIM,), torch.bfloat16, "q_weight"),
-            side(k_weight, (HEAD_DIM,), torch.bfloat16, "k_weight"), eps,
+            self.handle, layer, q.data_ptr(), qs, k.data_ptr(), ks, None if v is None else v.data_ptr(), vs, n,
+            side(positions, (self.B, n), torch.int64, "positions"), side(q_weight, (HEAD_DIM,), bf, "q_weight"),
+            side(k_weight, (HEAD_DIM,), bf, "k_weight"), eps,
             side(inv_freq, (HEAD_DIM // 2,), torch.float32, "inv_freq"), 1 if interleaved else 0,
-            outs[0].data_ptr(), outs[1].data_ptr(), None if v is None else outs[2].data_ptr(), _stream(stream))
-        self._check(rc)
-        return tuple(outs)
-
-    def _dense(self, t, heads, what):
-        n = self._heads(t, heads, what)
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be dense (strides {t.stride()})")
-        return n
+            side(q_out, q.shape, bf, "q_out"), side(k_out, k.shape, bf, "k_out"),
+            None if v is None else side(v_out, v.shape, bf, "v_out"), self._raw_stream(stream))
+        if rc:
+            self._check(rc)
+        return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
     def span_attention(self, layer, q, k, v, span=0, sinks=0, q_len=None, kv_len=None, out=None, lse=None,
                        want_lse=True, stream=None):
@@ -485,13 +478,15 @@ class TieredCache:
         if out is None:
             out = torch.empty_like(q)
         if lse is None and want_lse:
-            lse = torch.empty(self.B, self.Hq, n_q, dtype=torch.float32, device=q.device)
-        side, B = self._side, self.B
-        self._check(self.lib.qevict_span_attention(
+            lse = torch.empty(self.B, self.Hq, n_q, dtype=torch.float32, device=self._dev)
+        side, per_seq = self._side, (self.B,)
+        rc = self.lib.qevict_span_attention(
             self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), v.data_ptr(), n_kv,
-            side(q_len, (B,), torch.int32, "q_len"), side(kv_len, (B,), torch.int32, "kv_len"), span, sinks,
-            side(out, tuple(q.shape), torch.bfloat16, "out"), side(lse, (B, self.Hq, n_q), torch.float32, "lse"),
-            _stream(stream)))
+            side(q_len, per_seq, torch.int32, "q_len"), side(kv_len, per_seq, torch.int32, "kv_len"), span, sinks,
+            side(out, q.shape, torch.bfloat16, "out"), side(lse, (self.B, self.Hq, n_q), torch.float32, "lse"),
+            self._raw_stream(stream))
+        if rc:
+            self._check(rc)
         return out, lse
 
     def span_scores(self, layer, q, k, lse, span=0, sinks=0, q_len=None, kv_len=None, out=None, stream=None):
@@ -500,13 +495,15 @@ class TieredCache:
         n_q, n_kv = self._dense(q, self.Hq, "q"), self._dense(k, self.Hkv, "k")
         W = -(-n_kv // self.w)
         if out is None:
-            out = torch.empty(self.units, W, dtype=torch.float32, device=q.device)
-        side, B = self._side, self.B
-        self._check(self.lib.qevict_span_scores(
-            self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), n_kv, side(q_len, (B,), torch.int32, "q_len"),
-            side(kv_len, (B,), torch.int32, "kv_len"), span, sinks,
-            side(lse, (B, self.Hq, n_q), torch.float32, "lse"),
-            side(out, (self.units, W), torch.float32, "out"), _stream(stream)))
+            out = torch.empty(self.units, W, dtype=torch.float32, device=self._dev)
+        side, per_seq = self._side, (self.B,)
+        rc = self.lib.qevict_span_scores(
+            self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), n_kv, side(q_len, per_seq, torch.int32, "q_len"),
+            side(kv_len, per_seq, torch.int32, "kv_len"), span, sinks,
+            side(lse, (self.B, self.Hq, n_q), torch.float32, "lse"), side(out, (self.units, W), torch.float32, "out"),
+            self._raw_stream(stream))
+        if rc:
+            self._check(rc)
         return out
 
     # ---- RDKV's K-channel half -----------------------------------------------

@@ -30,9 +30,6 @@ __device__ __forceinline__ Tiles tiles_of(const SpanArgs &a, int p_lo, int p_hi)
     if (p_hi < 0) t.sink = 0;
     return t;
 }
-__device__ __forceinline__ bool visible(const SpanArgs &a, int j, int p) {
-    return j <= p && (j > p - a.span || j < a.sinks);
-}
 // whether some pair of keys [k0, k0 + 128) and positions [p_lo, p_hi] is masked
 __device__ __forceinline__ bool masked_tile(const SpanArgs &a, int k0, int p_lo, int p_hi) {
     return !(k0 + kTile - 1 <= p_lo && (k0 > p_hi - a.span || k0 + kTile <= a.sinks));
@@ -115,9 +112,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     auto k_item = [&](int j) { return SPLIT ? (j ? 2 * j - 1 : 0) : 2 * j; };
     auto v_item = [&](int j) { return SPLIT ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1; };
 
-    // 12 warps start with 168 registers a thread; the softmax groups take 224 and leave 40
+    // 12 warps start with 168 registers a thread; the softmax groups take 224 and leave 56
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (tid == 9 * 32 && n > 0) {
             tc_expect_tx(q_full, QT * rows * 256);
             for (int t = 0; t < QT; ++t)
@@ -146,68 +143,71 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const uint32_t tmu = __shfl_sync(~0u, tm, 0);
             const int nu = __shfl_sync(~0u, n, 0);
             bool ok = true;
-            auto wait = [&](uint32_t bar, int parity) {
-                ok = __all_sync(~0u, tc_wait(bar, parity, &stop));
+            auto wait = [&](uint32_t bar, int par) {
+                ok = __all_sync(~0u, tc_wait(bar, par, &stop));
                 return ok;
             };
-            auto commit = [&](uint32_t bar) {
-                if (lead) tc_commit(bar);
+            auto wait2 = [&](uint32_t bar, int par, uint32_t bar2, int par2) {
+                ok = __all_sync(~0u, tc_wait2(bar, par, bar2, par2, &stop));
+                return ok;
             };
             // The ring slots of the next key tile for S and of the next value tile; a slot's parity flips as it wraps.
-            int ks = k_item(0), kp = 0, vs = SPLIT && nu > 1 ? 2 : 1, vp = 0;
+            int ks = 0, kp = 0, vs = SPLIT && nu > 1 ? 2 : 1, vp = 0;
             auto ahead_of = [&](int &slot_, int &par, int by) {
                 slot_ += by;
                 if (slot_ >= NS) slot_ -= NS, par ^= 1;
             };
-            auto logits = [&](int t) {   // S_t = Q K^T
-                if (lead) tc_mma_tile(tmu + 128 * t, sm + (SPLIT ? 0 : t * kTileBytes), ring + ks * kTileBytes, kHalf);
-                commit(s_full(t));
+            auto logits = [&](int t, bool done) {   // S_t = Q K^T; done: the key tile's slot is free after it
+                if (lead) {
+                    tc_mma_tile(tmu + 128 * t, sm + (SPLIT ? 0 : t * kTileBytes), ring + ks * kTileBytes, kHalf);
+                    tc_commit(s_full(t));
+                    if (done) tc_commit(empty(ks));
+                }
+                __syncwarp();
             };
-            if (wait(q_full, 0) && wait(full(0), 0)) {
-                logits(0);
-                if (!SPLIT) logits(1);
-                commit(empty(0));
+            if (wait2(q_full, 0, full(0), 0)) {
+                logits(0, SPLIT);
+                if (!SPLIT) logits(1, true);
                 ahead_of(ks, kp, SPLIT ? 1 : 2);
                 if (SPLIT && nu > 1 && wait(full(ks), kp)) {
-                    logits(1);
-                    commit(empty(ks));
+                    logits(1, true);
                     ahead_of(ks, kp, 2);
                 }
             }
             for (int j = 0; j < nu && ok; ++j) {
-                if (!wait(full(vs), vp)) break;
                 const uint32_t v = tc_desc_mn(ring + vs * kTileBytes, kHalf);
                 const bool more = j + (SPLIT ? 2 : 1) < nu;
 #pragma unroll
                 for (int x = 0; x < QT; ++x) {
                     const int t = SPLIT ? j & 1 : x, par = (SPLIT ? j >> 1 : j) & 1;
+                    // the values' and the next keys' tiles are waited for beside the probabilities
+                    if (!(x == 0 ? wait2(full(vs), vp, p_full(t, 0), par) : wait(p_full(t, 0), par))) break;
+                    tc_fence_after();
+                    if (lead) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!ok || !wait(p_full(t, h), par)) break;
-                        tc_fence_after();
-                        if (lead) {
+                        for (int s = 0; s < 4; ++s)
+                            tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true),
+                                      s > 0 || j >= (SPLIT ? 2 : 1));
+                    }
+                    __syncwarp();
+                    if (!(x == 0 && more ? wait2(full(ks), kp, p_full(t, 1), par) : wait(p_full(t, 1), par))) break;
+                    tc_fence_after();
+                    if (lead) {
 #pragma unroll
-                            for (int s = 4 * h; s < 4 * h + 4; ++s)
-                                tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true),
-                                          s > 0 || j >= (SPLIT ? 2 : 1));
-                        }
+                        for (int s = 4; s < 8; ++s)
+                            tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true), 1);
+                        if (x == QT - 1) tc_commit(empty(vs));
+                        if (!more) tc_commit(o_full(t));
                     }
-                    if (!ok) break;
-                    if (x == QT - 1) commit(empty(vs));
-                    if (more) {
-                        if (x == 0 && !wait(full(ks), kp)) break;
-                        logits(t);
-                        if (x == QT - 1) commit(empty(ks));
-                    } else {
-                        commit(o_full(t));
-                    }
+                    __syncwarp();
+                    if (more) logits(t, x == QT - 1);
                 }
                 if (more) ahead_of(ks, kp, 2);
                 // split: the last value tile follows its predecessor directly
                 ahead_of(vs, vp, SPLIT && j == nu - 2 ? 1 : 2);
             }
             if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
-                commit(q_full);
+                if (lead) tc_commit(q_full);
                 const long long t0 = clock64();
                 while (!tc_try_wait(q_full, 1) && clock64() - t0 < kDefaultWaitCycles) {}
             }
@@ -240,11 +240,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const int hi = pos - k0, lo = hi - a.span, sk = a.sinks - k0;
             float x[4][32], mx[4];
             tc_ld32(tS, x[0]);
+            tc_ld32(tS + 32, x[1]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {   // the maximum of a quarter is taken while the next is on its way
-                tc_wait_ld();
-                tc_tie(x[q]);
-                if (q < 3) tc_ld32(tS + 32 * (q + 1), x[q + 1]);
+            for (int q = 0; q < 4; ++q) {   // the maximum of the first half is taken while the second is on its way
+                if ((q & 1) == 0) {
+                    tc_wait_ld();
+                    tc_tie(x[q]);
+                    tc_tie(x[q + 1]);
+                    if (q == 0) {
+                        tc_ld32(tS + 64, x[2]);
+                        tc_ld32(tS + 96, x[3]);
+                    }
+                }
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
@@ -576,30 +583,26 @@ __global__ void __launch_bounds__(kScThreads, 1)
         // the whole warp keeps step, one lane issues
         const bool lead = tc_elect();
         const uint32_t tmu = __shfl_sync(~0u, tm, 0);
-        auto wait = [&](uint32_t bar, int parity) {
-            ok = ok && __all_sync(~0u, tc_wait(bar, parity, &tail.stop));
-            return ok;
-        };
         int set = kScK - 1, kp = 1, qs = 0, qp = 0, buf = 0, sp = 1;   // slots and their parities
         for (int64_t item = item0; item < items && ok; item += stride) {
             const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
             bool head = true;
             for (ScoreSteps s(it, rank, cl); s.left > 0;) {
-                if (head) {
-                    if (++set == kScK) set = 0, kp ^= 1;
-                    if (!wait(k_full(set), kp)) break;
-                }
-                if (!wait(q_full(qs), qp) || !wait(s_empty(buf), sp)) break;   // s_empty passes at once the first time
+                if (head && ++set == kScK) set = 0, kp ^= 1;
+                // s_empty passes at once the first time
+                ok = __all_sync(~0u, tc_wait3(k_full(set), kp, q_full(qs), qp, s_empty(buf), sp, &tail.stop));
+                if (!ok) break;
                 tc_fence_after();
+                head = s.next();
                 if (lead) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         tc_mma_tile(tmu + 256 * t + 128 * buf, sm + (2 * set + t) * kTileBytes, sq + qs * kTileBytes, kHalf);
                     tc_commit(s_full(buf));
                     tc_commit(q_empty(qs));
+                    if (head || s.left == 0) tc_commit(k_empty(set));
                 }
-                head = s.next();
-                if (lead && (head || s.left == 0)) tc_commit(k_empty(set));
+                __syncwarp();
                 if (++qs == kScQ) qs = 0, qp ^= 1;
                 buf ^= 1;
                 sp ^= buf == 0;
@@ -765,6 +768,52 @@ __global__ void __launch_bounds__(kScThreads, 1)
 
 }  // namespace
 
+namespace {
+
+// How many clusters of each size the device holds at once (its SMs come in
+// groups of unlike size, so 8 CTAs fill fewer SMs than 4 or 9 do).
+constexpr int kMaxCluster = 16;
+template <class K>
+cudaError_t prepare_clusters(K kernel, int threads, int smem, int *active) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int c = 2; c <= kMaxCluster && e == cudaSuccess; ++c) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(c * 256);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = c;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&active[c], kernel, &cfg);
+    }
+    return e;
+}
+
+// CTAs per item that finish `items` items of `total` steps (the heaviest of
+// `heavy`) first, where starting a cluster's item costs `start` steps.
+int best_cluster(int64_t items, int64_t total, int64_t heavy, int num_sms, const int *active, int start) {
+    int best = 1;
+    double least = 0;
+    for (int c = 1; c <= kMaxCluster && (c == 1 || heavy >= c); ++c) {
+        const int n = c == 1 ? num_sms : active[c];
+        if (n < 1) continue;
+        const double rounds = (double)((items + n - 1) / n);
+        const double mean = rounds * (double)total / (double)items;
+        const double t = (mean > (double)heavy ? mean : (double)heavy) / c + rounds * (c == 1 ? start / 2 : start);
+        if (c == 1 || t < least) {
+            least = t;
+            best = c;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
                                   const CUtensorMap &kmap, const CUtensorMap &vmap, __nv_bfloat16 *out, float *lse,
                                   int num_sms, cudaStream_t s) {
@@ -815,22 +864,31 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
                                const CUtensorMap &kmap, const float *lse, float *scores, int w, bool per_head,
                                int num_sms, cudaStream_t s) {
-    cudaError_t e = once_per_device(0, [&] {
-        cudaError_t r =
-            cudaFuncSetAttribute(span_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScSmem);
-        if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(span_scores_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return r;
-    });
+    static int active[kOnceDevices][kMaxCluster + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev >= kOnceDevices) e = cudaErrorInvalidDevice;
+    if (e != cudaSuccess) return e;
+    e = once_per_device(0, [&] { return prepare_clusters(span_scores_kernel, kScThreads, kScSmem, active[dev]); });
     if (e != cudaSuccess) return e;
     const int keys = 2 * (kTile / w * w), T = span_tile_tokens(a.G);
     const int runs = (a.n_kv + keys - 1) / keys, n_win = (a.n_kv + w - 1) / w;
-    const int64_t items = (int64_t)runs * (per_head ? a.B * a.Hkv : a.B);
-    // steps of the longest item
-    const int64_t seen = a.sinks > 0 || a.span >= a.n_q ? a.n_q : (int64_t)a.span + keys < a.n_q ? a.span + keys : a.n_q;
-    const int64_t steps = ((seen + T - 1) / T) * (per_head ? 1 : a.Hkv);
+    const int units = per_head ? a.B * a.Hkv : a.B;
+    const int64_t items = (int64_t)runs * units;
+    // Steps of each item, at the lengths that the host knows; one CTA per item when there are many.
     int cl = 1;
-    while (cl < 8 && items * cl * 2 <= 4 * num_sms && steps >= 2 * cl) cl *= 2;
+    if (items < 8 * num_sms) {
+        int64_t heavy = 0, total = 0;
+        for (int x = 0; x < runs; ++x) {
+            const int k0 = x * keys, shift = a.n_kv - a.n_q;
+            const int lo = max(0, k0 - shift);
+            const int hi = k0 < a.sinks ? a.n_q : min(a.n_q, min(k0 + keys, a.n_kv) - 1 + a.span - shift);
+            const int64_t steps = hi <= lo ? 0 : (int64_t)((hi - 1) / T + 1 - lo / T) * (per_head ? 1 : a.Hkv);
+            heavy = steps > heavy ? steps : heavy;
+            total += steps * units;
+        }
+        cl = best_cluster(items, total, heavy, num_sms, active[dev], 6);
+    }
     int64_t grid = items * cl;
     if (cl == 1 && grid > num_sms) grid = num_sms;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;

@@ -42,6 +42,17 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile 
     return true;
 }
 
+// Two or three barriers; where all are through already, for the price of one.
+__device__ __forceinline__ bool tc_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, volatile int *stop) {
+    const bool x = tc_try_wait(a, pa), y = tc_try_wait(b, pb);
+    return (x || tc_wait(a, pa, stop)) && (y || tc_wait(b, pb, stop));
+}
+__device__ __forceinline__ bool tc_wait3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc,
+                                         volatile int *stop) {
+    const bool x = tc_try_wait(a, pa), y = tc_try_wait(b, pb), z = tc_try_wait(c, pc);
+    return (x || tc_wait(a, pa, stop)) && (y || tc_wait(b, pb, stop)) && (z || tc_wait(c, pc, stop));
+}
+
 __device__ __forceinline__ void tc_tma_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int u,
                                           uint32_t bar) {
     asm volatile(
@@ -90,11 +101,11 @@ __host__ __device__ constexpr uint32_t tc_idesc(bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// D (+)= A B over K = 16, A in shared (ss) or tensor (ts) memory. One lane issues
-// them inside a warp that is otherwise of one mind: with operands that are the
-// same in every lane they come out of uniform registers, which is what lets an
-// issue keep ahead of the 64 cycles that a 128 x 128 x 16 product takes (from a
-// branch of one thread an issue took 80 to 97 cycles).
+// D (+)= A B over K = 16, A in shared (ss) or tensor (ts) memory. The elected lane
+// issues them in a warp whose lanes otherwise keep step (they wait for the same
+// barriers and hold the same operands): the operands then come out of uniform
+// registers, and an issue keeps ahead of the 64 cycles that a 128 x 128 x 16
+// product takes (from a branch of one thread an issue took 80 to 97 cycles).
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -115,8 +126,10 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, ui
 __device__ __forceinline__ void tc_mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t half) {
     const uint32_t da = tc_desc_k(a), db = tc_desc_k(b), h = half >> 4;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) tc_mma_ss(d, da + (s >> 2) * h + (s & 3) * 2, db + (s >> 2) * h + (s & 3) * 2, tc_idesc(false), s > 0);
+    for (int s = 0; s < 8; ++s)
+        tc_mma_ss(d, da + (s >> 2) * h + (s & 3) * 2, db + (s >> 2) * h + (s & 3) * 2, tc_idesc(false), s > 0);
 }
+// all products issued so far arrive on `bar` when they have ended
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
