@@ -35,6 +35,9 @@ __device__ __forceinline__ bool masked_tile(const SpanArgs &a, int k0, int p_lo,
     return !(k0 + kTile - 1 <= p_lo && (k0 > p_hi - a.span || k0 + kTile <= a.sinks));
 }
 
+// bits 0 .. n - 1 of a word
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
 __device__ __forceinline__ int clamped(const int32_t *len, int b, int n) {
     return len ? min(max(len[b], 0), n) : n;
 }
@@ -60,32 +63,51 @@ constexpr int kAttSlots = 7;                  // 32 KB slots of shared memory: q
 constexpr int kAttSmem = kAttSlots * kTileBytes + 1024;
 constexpr float kRescale = 8.f;               // log2 growth of a row's maximum that moves its reference
 
+// One or two neighbouring query tiles of one (sequence, KV head), and the key tiles
+// [first, first + n) of theirs that this CTA takes.
+struct __align__(16) AttUnit {
+    int b, kvh, i0, n_tok, p_lo, p_hi, first, n;
+    Tiles tl;
+    int pad;
+};
+template <bool SPLIT>
+__device__ __forceinline__ AttUnit att_unit(const SpanArgs &a, int u, int q_tiles, int T, int rank, int cl) {
+    AttUnit U;
+    const int heads = a.B * a.Hkv;
+    U.b = u % heads / a.Hkv;
+    U.kvh = u % a.Hkv;
+    U.i0 = (q_tiles - 1 - u / heads) * (SPLIT ? T : 2 * T);   // the longest rows of keys first
+    const int q_len = clamped(a.q_len, U.b, a.n_q), kv_len = clamped(a.kv_len, U.b, a.n_kv);
+    U.n_tok = min(SPLIT ? T : 2 * T, q_len - U.i0);           // none: past the sequence's queries
+    U.p_lo = kv_len - q_len + U.i0;
+    U.p_hi = U.p_lo + U.n_tok - 1;
+    U.tl = tiles_of(a, U.p_lo, U.p_hi);
+    const int all = U.n_tok > 0 ? U.tl.count() : 0;
+    U.first = SPLIT ? (int)((int64_t)all * rank / cl) : 0;
+    U.n = (SPLIT ? (int)((int64_t)all * (rank + 1) / cl) : all) - U.first;
+    return U;
+}
+
 template <bool SPLIT>
 __global__ void __launch_bounds__(kAttThreads, 1)
     span_attention_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                          __nv_bfloat16 *out, float *lse, int q_tiles, int cl) {
+                          __nv_bfloat16 *out, float *lse, int q_tiles, int units, int cl) {
     constexpr int QT = SPLIT ? 1 : 2;              // query tiles of the CTA
     constexpr int NS = kAttSlots - QT;             // ring slots
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * NS + 9];
+    __shared__ uint64_t bars[2 * NS + 14];
+    __shared__ AttUnit given[2];                   // wide: units that the copy thread has worked out
     __shared__ uint32_t slot;
     __shared__ int stop;
 
     const int T = span_tile_tokens(a.G), rows = T * a.G;
-    const int unit = blockIdx.x / cl, rank = blockIdx.x - unit * cl;
-    const int heads = a.B * a.Hkv;
-    const int qt = q_tiles - 1 - unit / heads;     // the longest rows of keys first
-    const int b = unit % heads / a.Hkv, kvh = unit % a.Hkv;
-    const int i0 = qt * QT * T;
-    const int q_len = clamped(a.q_len, b, a.n_q), kv_len = clamped(a.kv_len, b, a.n_kv);
-    if (i0 >= q_len) return;                       // all CTAs of the cluster alike
-    const int n_tok = min(QT * T, q_len - i0);
-    const int p_lo = kv_len - q_len + i0, p_hi = p_lo + n_tok - 1;
-    const Tiles tl = tiles_of(a, p_lo, p_hi);
-    const int all = tl.count();
-    const int first = SPLIT ? (int)((int64_t)all * rank / cl) : 0;
-    const int n = (SPLIT ? (int)((int64_t)all * (rank + 1) / cl) : all) - first;   // key tiles of this CTA
+    const int rank = SPLIT ? blockIdx.x % cl : 0;
+    AttUnit U;
+    if (SPLIT) {   // one unit
+        U = att_unit<SPLIT>(a, blockIdx.x / cl, q_tiles, T, rank, cl);
+        if (U.n_tok <= 0) return;   // the whole cluster alike
+    }
 
     const uint32_t sm = (smem_u32(raw) + 1023) & ~1023u;
     uint8_t *gen = raw + (sm - smem_u32(raw));
@@ -97,9 +119,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     auto s_full = [&](int t) { return bar0 + 8 * (2 * NS + t); };
     auto p_full = [&](int t, int h) { return bar0 + 8 * (2 * NS + 5 + 2 * t + h); };   // h: half of the keys
     auto o_full = [&](int t) { return bar0 + 8 * (2 * NS + 2 + t); };
-    const uint32_t q_full = bar0 + 8 * (2 * NS + 4);
+    const uint32_t q_full = bar0 + 8 * (2 * NS + 4), q_empty = bar0 + 8 * (2 * NS + 9);
+    auto u_full = [&](int x) { return bar0 + 8 * (2 * NS + 10 + x); };
+    auto u_empty = [&](int x) { return bar0 + 8 * (2 * NS + 12 + x); };
     if (tid == 0) {
-        for (int i = 0; i < 2 * NS + 9; ++i) tc_mbar_init(bar0 + 8 * i, i >= 2 * NS + 5 ? 4 : 1);
+        // p_full: the group's four warps; u_empty: the product warp and both groups' warps
+        for (int i = 0; i < 2 * NS + 14; ++i)
+            tc_mbar_init(bar0 + 8 * i, i >= 2 * NS + 12 ? 9 : i >= 2 * NS + 5 && i < 2 * NS + 9 ? 4 : 1);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -108,40 +134,77 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = slot;                      // S of group t at column 128 t, O at 256 + 128 t
-    // ring order: the order in which the products use the tiles
-    auto k_item = [&](int j) { return SPLIT ? (j ? 2 * j - 1 : 0) : 2 * j; };
-    auto v_item = [&](int j) { return SPLIT ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1; };
+    // The next unit of a warp (c: how many it has had), false when there is none. Wide: the copy
+    // thread, which is tiles ahead, has worked it out, so the other warps do not stall on it.
+    auto next = [&](int c, bool &ok) {
+        if (SPLIT) return c == 0;
+        ok = __all_sync(~0u, tc_wait(u_full(c & 1), (c >> 1) & 1, &stop));
+        if (!ok) return false;
+        U = given[c & 1];
+        __syncwarp();
+        if ((tid & 31) == 0) tc_arrive(u_empty(c & 1));
+        return U.n_tok > 0;
+    };
 
     // 12 warps start with 168 registers a thread; the softmax groups take 224 and leave 56
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (tid == 9 * 32 && n > 0) {
-            tc_expect_tx(q_full, QT * rows * 256);
-            for (int t = 0; t < QT; ++t)
-                for (int h = 0; h < 2; ++h)
-                    tc_tma_4d(sm + t * kTileBytes + h * kHalf, &qmap, 64 * h, kvh * a.G, i0 + t * T, b, q_full);
-            int i = 0;
-            for (; i < 2 * n; ++i) {
-                const int s = i % NS;
-                if (i >= NS && !tc_wait(empty(s), (i / NS - 1) & 1, &stop)) break;
-                const bool isk = SPLIT ? i == 0 || (i & 1 && i < 2 * n - 1) : !(i & 1);
-                const int j = SPLIT ? (isk ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1) : i / 2;
-                tc_expect_tx(full(s), kTileBytes);
-                for (int h = 0; h < 2; ++h)
-                    tc_tma_4d(ring + s * kTileBytes + h * kHalf, isk ? &kmap : &vmap, 64 * h, kvh, tl.key(first + j), b,
-                              full(s));
-            }
-            if (i < 2 * n) {   // gave up: the copies in flight land before the CTA ends
-                for (int o = max(0, i - NS); o < i; ++o) {
-                    const long long t0 = clock64();
-                    while (!tc_try_wait(full(o % NS), (o / NS) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+        if (tid == 9 * 32) {
+            // The ring holds key and value tiles in the order in which the products use them: K0 V0 K1 V1 ..,
+            // split K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
+            int i = 0, q = 0, c = 0;
+            bool ok = true;
+            auto give = [&](const AttUnit &X) {
+                if (c >= 2 && !(ok = tc_wait(u_empty(c & 1), ((c >> 1) - 1) & 1, &stop))) return;
+                given[c & 1] = X;
+                tc_arrive(u_full(c & 1));
+                ++c;
+            };
+            // Wide CTAs are persistent: the units, longest first, are dealt out to and fro.
+            for (int k = 0; ok; ++k) {
+                const int g = gridDim.x, at = k * g + (k & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+                if (SPLIT) {
+                    if (k) break;
+                } else if (k * g >= units) {
+                    U.n_tok = 0;   // no more
+                    give(U);
+                    break;
+                } else {
+                    if (at >= units) continue;
+                    U = att_unit<SPLIT>(a, at, q_tiles, T, rank, cl);
+                    if (U.n_tok <= 0) continue;
+                    give(U);
+                    if (!ok) break;
+                }
+                if (U.n <= 0) continue;
+                if (q > 0 && !(ok = tc_wait(q_empty, (q - 1) & 1, &stop))) break;
+                tc_expect_tx(q_full, QT * rows * 256);
+                for (int t = 0; t < QT; ++t)
+                    for (int h = 0; h < 2; ++h)
+                        tc_tma_4d(sm + t * kTileBytes + h * kHalf, &qmap, 64 * h, U.kvh * a.G, U.i0 + t * T, U.b, q_full);
+                ++q;
+                for (int x = 0; x < 2 * U.n; ++x, ++i) {
+                    const int s = i % NS;
+                    if (i >= NS && !(ok = tc_wait(empty(s), (i / NS - 1) & 1, &stop))) break;
+                    const bool last = x == 2 * U.n - 1;
+                    const bool isk = SPLIT ? x == 0 || (x & 1 && !last) : !(x & 1);
+                    const int j = SPLIT ? (isk ? (x + 1) / 2 : last ? U.n - 1 : x / 2 - 1) : x / 2;
+                    tc_expect_tx(full(s), kTileBytes);
+                    for (int h = 0; h < 2; ++h)
+                        tc_tma_4d(ring + s * kTileBytes + h * kHalf, isk ? &kmap : &vmap, 64 * h, U.kvh,
+                                  U.tl.key(U.first + j), U.b, full(s));
                 }
             }
+            if (!ok) {   // gave up: the copies in flight land before the CTA ends
+                const long long t0 = clock64();
+                while (q > 0 && !tc_try_wait(q_full, (q - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+                for (int o = max(0, i - NS); o < i; ++o)
+                    while (!tc_try_wait(full(o % NS), (o / NS) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+            }
         }
-        if (warp == 8 && n > 0) {   // the whole warp keeps step, one lane issues
+        if (warp == 8) {   // the whole warp keeps step, one lane issues
             const bool lead = tc_elect();
             const uint32_t tmu = __shfl_sync(~0u, tm, 0);
-            const int nu = __shfl_sync(~0u, n, 0);
             bool ok = true;
             auto wait = [&](uint32_t bar, int par) {
                 ok = __all_sync(~0u, tc_wait(bar, par, &stop));
@@ -152,64 +215,74 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 return ok;
             };
             // The ring slots of the next key tile for S and of the next value tile; a slot's parity flips as it wraps.
-            int ks = 0, kp = 0, vs = SPLIT && nu > 1 ? 2 : 1, vp = 0;
+            int ks = 0, kp = 0, vs = 1, vp = 0, q = 0, tiles = 0;
             auto ahead_of = [&](int &slot_, int &par, int by) {
                 slot_ += by;
                 if (slot_ >= NS) slot_ -= NS, par ^= 1;
             };
-            auto logits = [&](int t, bool done) {   // S_t = Q K^T; done: the key tile's slot is free after it
+            // S_t = Q K^T; done: the key tile's slot is free after it, last: so are the query tiles
+            auto logits = [&](int t, bool done, bool last) {
                 if (lead) {
                     tc_mma_tile(tmu + 128 * t, sm + (SPLIT ? 0 : t * kTileBytes), ring + ks * kTileBytes, kHalf);
                     tc_commit(s_full(t));
                     if (done) tc_commit(empty(ks));
+                    if (done && last) tc_commit(q_empty);
                 }
                 __syncwarp();
             };
-            if (wait2(q_full, 0, full(0), 0)) {
-                logits(0, SPLIT);
-                if (!SPLIT) logits(1, true);
+            for (int c = 0; next(c, ok); ++c) {
+                const int n = __shfl_sync(~0u, U.n, 0);
+                if (n <= 0) continue;
+                if (!wait2(q_full, q & 1, full(ks), kp)) break;
+                ++q;
+                if (SPLIT && n > 1) vs = 2;
+                logits(0, SPLIT, n == 1);
+                if (!SPLIT) logits(1, true, n == 1);
                 ahead_of(ks, kp, SPLIT ? 1 : 2);
-                if (SPLIT && nu > 1 && wait(full(ks), kp)) {
-                    logits(1, true);
+                if (SPLIT && n > 1) {
+                    if (!wait(full(ks), kp)) break;
+                    logits(1, true, n == 2);
                     ahead_of(ks, kp, 2);
                 }
-            }
-            for (int j = 0; j < nu && ok; ++j) {
-                const uint32_t v = tc_desc_mn(ring + vs * kTileBytes, kHalf);
-                const bool more = j + (SPLIT ? 2 : 1) < nu;
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t v = tc_desc_mn(ring + vs * kTileBytes, kHalf);
+                    const bool more = j + (SPLIT ? 2 : 1) < n;
+                    const int par = (SPLIT ? j >> 1 : tiles + j) & 1;
 #pragma unroll
-                for (int x = 0; x < QT; ++x) {
-                    const int t = SPLIT ? j & 1 : x, par = (SPLIT ? j >> 1 : j) & 1;
-                    // the values' and the next keys' tiles are waited for beside the probabilities
-                    if (!(x == 0 ? wait2(full(vs), vp, p_full(t, 0), par) : wait(p_full(t, 0), par))) break;
-                    tc_fence_after();
-                    if (lead) {
+                    for (int x = 0; x < QT; ++x) {
+                        const int t = SPLIT ? j & 1 : x;
+                        // the values' and the next keys' tiles are waited for beside the probabilities
+                        if (!(x == 0 ? wait2(full(vs), vp, p_full(t, 0), par) : wait(p_full(t, 0), par))) break;
+                        tc_fence_after();
+                        if (lead) {
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true),
-                                      s > 0 || j >= (SPLIT ? 2 : 1));
+                            for (int s = 0; s < 4; ++s)
+                                tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true),
+                                          s > 0 || j >= (SPLIT ? 2 : 1));
+                        }
+                        __syncwarp();
+                        if (!(x == 0 && more ? wait2(full(ks), kp, p_full(t, 1), par) : wait(p_full(t, 1), par))) break;
+                        tc_fence_after();
+                        if (lead) {
+#pragma unroll
+                            for (int s = 4; s < 8; ++s)
+                                tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true), 1);
+                            if (x == QT - 1) tc_commit(empty(vs));
+                            if (!more) tc_commit(o_full(t));
+                        }
+                        __syncwarp();
+                        if (more) logits(t, x == QT - 1, j + (SPLIT ? 3 : 2) == n);
                     }
-                    __syncwarp();
-                    if (!(x == 0 && more ? wait2(full(ks), kp, p_full(t, 1), par) : wait(p_full(t, 1), par))) break;
-                    tc_fence_after();
-                    if (lead) {
-#pragma unroll
-                        for (int s = 4; s < 8; ++s)
-                            tc_mma_ts(tmu + 256 + 128 * t, tmu + 128 * t + 8 * s, v + s * 128, tc_idesc(true), 1);
-                        if (x == QT - 1) tc_commit(empty(vs));
-                        if (!more) tc_commit(o_full(t));
-                    }
-                    __syncwarp();
-                    if (more) logits(t, x == QT - 1);
+                    if (more) ahead_of(ks, kp, 2);
+                    // split: the last value tile follows its predecessor directly
+                    ahead_of(vs, vp, SPLIT && j == n - 2 ? 1 : 2);
                 }
-                if (more) ahead_of(ks, kp, 2);
-                // split: the last value tile follows its predecessor directly
-                ahead_of(vs, vp, SPLIT && j == nu - 2 ? 1 : 2);
+                if (!ok) break;
+                tiles += n;
             }
-            if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
-                if (lead) tc_commit(q_full);
+            if (!ok) {   // gave up: products in flight (microseconds at most) end before the tensor memory is freed
                 const long long t0 = clock64();
-                while (!tc_try_wait(q_full, 1) && clock64() - t0 < kDefaultWaitCycles) {}
+                while (clock64() - t0 < 1000000) {}
             }
         }
         __syncwarp();
@@ -223,206 +296,213 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint32_t lane_tm = tm + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tS = lane_tm + 128 * t, tO = lane_tm + 256 + 128 * t;
         const float c = kLog2e * rsqrtf((float)kHeadDim);
-        const int tok = (SPLIT ? 0 : t * T) + r / a.G;
-        const int pos = p_lo + tok;
-        const bool valid = r < rows && tok < n_tok;
-        const int g_lo = p_lo + (SPLIT ? 0 : t * T), g_hi = min(p_hi, g_lo + T - 1);   // this group's positions
-        float m = -INFINITY, l = 0.f;
         const uint64_t cc = pair2(c, c);
+        const int tok = (SPLIT ? 0 : t * T) + r / a.G, g = r % a.G;
         bool ok = true;
-        int done = 0;
-        for (int j = SPLIT ? t : 0; j < n; j += SPLIT ? 2 : 1, ++done) {
-            ok = __all_sync(~0u, tc_wait(s_full(t), done & 1, &stop));   // a warp stops as one
-            if (!ok) break;
-            tc_fence_after();
-            const int k0 = tl.key(first + j);
-            const bool masked = masked_tile(a, k0, g_lo, g_hi);
-            const int hi = pos - k0, lo = hi - a.span, sk = a.sinks - k0;
-            float x[4][32], mx[4];
-            tc_ld32(tS, x[0]);
-            tc_ld32(tS + 32, x[1]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {   // the maximum of the first half is taken while the second is on its way
-                if ((q & 1) == 0) {
-                    tc_wait_ld();
-                    tc_tie(x[q]);
-                    tc_tie(x[q + 1]);
-                    if (q == 0) {
-                        tc_ld32(tS + 64, x[2]);
-                        tc_ld32(tS + 96, x[3]);
-                    }
-                }
-                if (masked) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * q + e > hi || (32 * q + e <= lo && 32 * q + e >= sk)) x[q][e] = -INFINITY;
-                }
-                float y[2] = {fmaxf(x[q][0], x[q][1]), fmaxf(x[q][2], x[q][3])};
-#pragma unroll
-                for (int e = 4; e < 32; e += 4) {
-                    y[0] = max3(y[0], x[q][e], x[q][e + 1]);
-                    y[1] = max3(y[1], x[q][e + 2], x[q][e + 3]);
-                }
-                mx[q] = fmaxf(y[0], y[1]);
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // The reference follows the maximum only when it has grown by more than
-            // kRescale in the exponent: probabilities stay below 2^kRescale, and O is
-            // rarely touched between its products.
-            if (__any_sync(~0u, (top - m) * c > kRescale)) {
-                const float mn = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.f : tc_ex2((m - mn) * c);
-                m = mn;
-                l *= f;
-                if (done > 0) {   // the product before it has ended: its logits came after it
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float o[32];
-                        tc_ld32(tO + 32 * q, o);
-                        tc_wait_ld();
-                        tc_tie(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tc_st32(tO + 32 * q, o);
-                    }
-                }
-            }
-            // Values of keys that no row of the CTA sees may be anything: as zeros they stay out of the product.
-            if ((SPLIT || t == 0) && (k0 + kTile - 1 > p_hi || (k0 <= p_lo - a.span && k0 + kTile > a.sinks))) {
-                const int i = v_item(j), s = i % NS;
-                ok = __all_sync(~0u, tc_wait(full(s), (i / NS) & 1, &stop));
+        int tiles = 0, item0 = 0, outs = 0;   // logit tiles, ring items and outputs before this unit
+        for (int c_ = 0; ok && next(c_, ok); ++c_) {
+            const int b = U.b, kvh = U.kvh, i0 = U.i0, p_lo = U.p_lo, p_hi = U.p_hi, n = U.n;
+            auto v_item = [&](int j) { return item0 + (SPLIT ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1); };
+            const int pos = p_lo + tok;
+            const bool valid = r < rows && tok < U.n_tok;
+            const int g_lo = p_lo + (SPLIT ? 0 : t * T), g_hi = min(p_hi, g_lo + T - 1);   // this group's positions
+            float m = -INFINITY, l = 0.f;
+            int done = 0;
+            for (int j = SPLIT ? t : 0; j < n; j += SPLIT ? 2 : 1, ++done) {
+                ok = __all_sync(~0u, tc_wait(s_full(t), (tiles + done) & 1, &stop));   // a warp stops as one
                 if (!ok) break;
-                const int key = k0 + r;
-                if (key > p_hi || (key <= p_lo - a.span && key >= a.sinks)) {
-                    uint8_t *v = gen + (QT + s) * kTileBytes + r * 128;
+                tc_fence_after();
+                const int k0 = U.tl.key(U.first + j);
+                const bool masked = masked_tile(a, k0, g_lo, g_hi);
+                const int hi = pos - k0, lo = hi - a.span, sk = a.sinks - k0;
+                float x[4][32], mx[4];
+                tc_ld32(tS, x[0]);
+                tc_ld32(tS + 32, x[1]);
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        *reinterpret_cast<int4 *>(v + 16 * y) = make_int4(0, 0, 0, 0);
-                        *reinterpret_cast<int4 *>(v + kHalf + 16 * y) = make_int4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
-            }
-            const float mc = m == -INFINITY ? 0.f : -m * c;
-            const uint64_t mm = pair2(mc, mc);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {   // the product starts on the first half of the keys
-#pragma unroll
-                for (int q = 2 * h; q < 2 * h + 2; ++q) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float u, v;
-                        split2(fma2(pair2(x[q][2 * e], x[q][2 * e + 1]), cc, mm), u, v);
-                        u = tc_ex2(u);
-                        v = tc_ex2(v);
-                        sum[e & 1] = add2(sum[e & 1], pair2(u, v));
-                        const __nv_bfloat162 pk = __floats2bfloat162_rn(u, v);
-                        p[e] = *reinterpret_cast<const uint32_t *>(&pk);
-                    }
-                    tc_st16(tS + 16 * q, p);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if ((tid & 31) == 0) tc_arrive(p_full(t, h));
-            }
-            float s0, s1;
-            split2(add2(sum[0], sum[1]), s0, s1);
-            l += s0 + s1;
-        }
-        if (ok && done > 0) ok = __all_sync(~0u, tc_wait(o_full(t), 0, &stop));
-        tc_fence_after();
-        if (!SPLIT) {
-            const float inv = 1.f / l;
-            const bool none = l == 0.f;   // no key seen
-            const int64_t head = kvh * a.G + r % a.G;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(out + (((int64_t)b * a.n_q + i0 + tok) * a.Hq + head) * kHeadDim);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float o[32];
-                tc_ld32(tO + 32 * q, o);
-                tc_wait_ld();
-                tc_tie(o);
-                if (valid && ok) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const __nv_bfloat162 pk = __floats2bfloat162_rn(none ? 0.f : o[e + 2 * y] * inv,
-                                                                            none ? 0.f : o[e + 2 * y + 1] * inv);
-                            p[y] = *reinterpret_cast<const uint32_t *>(&pk);
+                for (int q = 0; q < 4; ++q) {   // the maximum of the first half is taken while the second is on its way
+                    if ((q & 1) == 0) {
+                        tc_wait_ld();
+                        tc_tie(x[q]);
+                        tc_tie(x[q + 1]);
+                        if (q == 0) {
+                            tc_ld32(tS + 64, x[2]);
+                            tc_ld32(tS + 96, x[3]);
                         }
-                        *reinterpret_cast<uint4 *>(dst + 16 * q + e / 2) = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                    if (masked) {   // the quarter's visible keys as bits, so that no element needs a branch
+                        const uint32_t w = below(hi + 1 - 32 * q) & (~below(lo + 1 - 32 * q) | below(sk - 32 * q));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[q][e] = (w >> e & 1) ? x[q][e] : -INFINITY;
+                    }
+                    float y[2] = {fmaxf(x[q][0], x[q][1]), fmaxf(x[q][2], x[q][3])};
+#pragma unroll
+                    for (int e = 4; e < 32; e += 4) {
+                        y[0] = max3(y[0], x[q][e], x[q][e + 1]);
+                        y[1] = max3(y[1], x[q][e + 2], x[q][e + 3]);
+                    }
+                    mx[q] = fmaxf(y[0], y[1]);
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // The reference follows the maximum only when it has grown by more than
+                // kRescale in the exponent: probabilities stay below 2^kRescale, and O is
+                // rarely touched between its products.
+                if (__any_sync(~0u, (top - m) * c > kRescale)) {
+                    const float mn = fmaxf(m, top);
+                    const float f = m == -INFINITY ? 0.f : tc_ex2((m - mn) * c);
+                    m = mn;
+                    l *= f;
+                    if (done > 0) {   // the product before it has ended: its logits came after it
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            float o[32];
+                            tc_ld32(tO + 32 * q, o);
+                            tc_wait_ld();
+                            tc_tie(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tc_st32(tO + 32 * q, o);
+                        }
+                    }
+                }
+                // Values of keys that no row of the CTA sees may be anything: as zeros they stay out of the product.
+                if ((SPLIT || t == 0) && (k0 + kTile - 1 > p_hi || (k0 <= p_lo - a.span && k0 + kTile > a.sinks))) {
+                    const int i = v_item(j), s = i % NS;
+                    ok = __all_sync(~0u, tc_wait(full(s), (i / NS) & 1, &stop));
+                    if (!ok) break;
+                    const int key = k0 + r;
+                    if (key > p_hi || (key <= p_lo - a.span && key >= a.sinks)) {
+                        uint8_t *v = gen + (QT + s) * kTileBytes + r * 128;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            *reinterpret_cast<int4 *>(v + 16 * y) = make_int4(0, 0, 0, 0);
+                            *reinterpret_cast<int4 *>(v + kHalf + 16 * y) = make_int4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : -m * c;
+                const uint64_t mm = pair2(mc, mc);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {   // the product starts on the first half of the keys
+#pragma unroll
+                    for (int q = 2 * h; q < 2 * h + 2; ++q) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float u, v;
+                            split2(fma2(pair2(x[q][2 * e], x[q][2 * e + 1]), cc, mm), u, v);
+                            u = tc_ex2(u);
+                            v = tc_ex2(v);
+                            sum[e & 1] = add2(sum[e & 1], pair2(u, v));
+                            const __nv_bfloat162 pk = __floats2bfloat162_rn(u, v);
+                            p[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                        }
+                        tc_st16(tS + 16 * q, p);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if ((tid & 31) == 0) tc_arrive(p_full(t, h));
+                }
+                float s0, s1;
+                split2(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
+            }
+            if (ok && done > 0) ok = __all_sync(~0u, tc_wait(o_full(t), outs++ & 1, &stop));
+            tc_fence_after();
+            tiles += n;
+            item0 += 2 * n;
+            if (!SPLIT) {
+                const float inv = 1.f / l;
+                const bool none = l == 0.f;   // no key seen
+                const int64_t head = kvh * a.G + g;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(out + (((int64_t)b * a.n_q + i0 + tok) * a.Hq + head) * kHeadDim);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    float o[32];
+                    tc_ld32(tO + 32 * q, o);
+                    tc_wait_ld();
+                    tc_tie(o);
+                    if (valid && ok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t p[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const __nv_bfloat162 pk = __floats2bfloat162_rn(none ? 0.f : o[e + 2 * y] * inv,
+                                                                                none ? 0.f : o[e + 2 * y + 1] * inv);
+                                p[y] = *reinterpret_cast<const uint32_t *>(&pk);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + 16 * q + e / 2) = make_uint4(p[0], p[1], p[2], p[3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (valid && ok && lse)
+                    lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + tok] =
+                        none ? -INFINITY : m * rsqrtf((float)kHeadDim) + logf(l);
+            } else {
+                // both groups' products have read the ring: it holds the partial outputs now
+                asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
+                float2 *stat = reinterpret_cast<float2 *>(gen + 5 * kTileBytes) + t * kTile;   // (max, sum) of the rows
+                stat[r] = done > 0 ? make_float2(m * c, l) : make_float2(-INFINITY, 0.f);
+                float4 *part = reinterpret_cast<float4 *>(gen + kTileBytes + t * 2 * kTileBytes) + r * 32;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float o[32];
+                    tc_ld32(tO + 32 * q, o);
+                    tc_wait_ld();
+                    tc_tie(o);
+                    if (valid && done > 0 && ok) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)   // the swizzle spreads a warp's rows over the banks
+                            part[(8 * q + e) ^ (r & 31)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    __syncwarp();
+                }
+                __syncwarp();
+                if (cl > 1) cl_sync();
+                else __syncthreads();
+                {
+                    const uint32_t st = ring + 4 * kTileBytes;
+                    for (int i = rank * kSoftmax + tid; i < U.n_tok * a.G * 32; i += cl * kSoftmax) {
+                        const int r = i >> 5, ch = i & 31;
+                        float top = -INFINITY;
+                        for (int x = 0; x < 2 * cl; ++x)
+                            top = fmaxf(top, cl_ld1(cl_addr(st + (x & 1) * kTile * 8 + r * 8, x >> 1)));
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                        float l = 0.f;
+                        for (int x = 0; x < 2 * cl; ++x) {
+                            const float2 s = cl_ld2(cl_addr(st + (x & 1) * kTile * 8 + r * 8, x >> 1));
+                            if (s.y == 0.f) continue;   // saw no key (a sum of NaN goes on)
+                            const float f = s.x == -INFINITY ? 1.f : tc_ex2(s.x - top);
+                            const float4 y = cl_ld4(cl_addr(ring + (x & 1) * 2 * kTileBytes + r * 512 + 16 * (ch ^ (r & 31)), x >> 1));
+                            l = fmaf(s.y, f, l);
+                            o.x = fmaf(y.x, f, o.x);
+                            o.y = fmaf(y.y, f, o.y);
+                            o.z = fmaf(y.z, f, o.z);
+                            o.w = fmaf(y.w, f, o.w);
+                        }
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
+                        const int64_t head = kvh * a.G + r % a.G;
+                        __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+                        *reinterpret_cast<uint2 *>(out + (((int64_t)b * a.n_q + i0 + r / a.G) * a.Hq + head) * kHeadDim + 4 * ch) =
+                            *reinterpret_cast<const uint2 *>(p);
+                        if (ch == 0 && lse)
+                            lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + r / a.G] =
+                                l == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * (1.f / kLog2e) + logf(l);
                     }
                 }
                 __syncwarp();
+                if (cl > 1) cl_sync();
             }
-            if (valid && ok && lse)
-                lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + tok] =
-                    none ? -INFINITY : m * rsqrtf((float)kHeadDim) + logf(l);
-        } else {
-            // both groups' products have read the ring: it holds the partial outputs now
-            asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
-            float2 *stat = reinterpret_cast<float2 *>(gen + 5 * kTileBytes) + t * kTile;   // (max, sum) of the rows
-            stat[r] = done > 0 ? make_float2(m * c, l) : make_float2(-INFINITY, 0.f);
-            float4 *part = reinterpret_cast<float4 *>(gen + kTileBytes + t * 2 * kTileBytes) + r * 32;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float o[32];
-                tc_ld32(tO + 32 * q, o);
-                tc_wait_ld();
-                tc_tie(o);
-                if (valid && done > 0 && ok) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)   // the swizzle spreads a warp's rows over the banks
-                        part[(8 * q + e) ^ (r & 31)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                }
-                __syncwarp();
-            }
-            __syncwarp();
-            if (cl > 1) cl_sync();
-            else __syncthreads();
-            {
-                const uint32_t st = ring + 4 * kTileBytes;
-                for (int i = rank * kSoftmax + tid; i < n_tok * a.G * 32; i += cl * kSoftmax) {
-                    const int r = i >> 5, ch = i & 31;
-                    float top = -INFINITY;
-                    for (int x = 0; x < 2 * cl; ++x)
-                        top = fmaxf(top, cl_ld1(cl_addr(st + (x & 1) * kTile * 8 + r * 8, x >> 1)));
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float l = 0.f;
-                    for (int x = 0; x < 2 * cl; ++x) {
-                        const float2 s = cl_ld2(cl_addr(st + (x & 1) * kTile * 8 + r * 8, x >> 1));
-                        if (s.y == 0.f) continue;   // saw no key (a sum of NaN goes on)
-                        const float f = s.x == -INFINITY ? 1.f : tc_ex2(s.x - top);
-                        const float4 y = cl_ld4(cl_addr(ring + (x & 1) * 2 * kTileBytes + r * 512 + 16 * (ch ^ (r & 31)), x >> 1));
-                        l = fmaf(s.y, f, l);
-                        o.x = fmaf(y.x, f, o.x);
-                        o.y = fmaf(y.y, f, o.y);
-                        o.z = fmaf(y.z, f, o.z);
-                        o.w = fmaf(y.w, f, o.w);
-                    }
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    const int64_t head = kvh * a.G + r % a.G;
-                    __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
-                    *reinterpret_cast<uint2 *>(out + (((int64_t)b * a.n_q + i0 + r / a.G) * a.Hq + head) * kHeadDim + 4 * ch) =
-                        *reinterpret_cast<const uint2 *>(p);
-                    if (ch == 0 && lse)
-                        lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + r / a.G] =
-                            l == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * (1.f / kLog2e) + logf(l);
-                }
-            }
-            __syncwarp();
-            if (cl > 1) cl_sync();
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && stop) set_status(C, QEVICT_ERR_TIMEOUT, layer, b, kvh);
+    if (tid == 0 && stop) set_status(C, QEVICT_ERR_TIMEOUT, layer, blockIdx.x, 0);
     if (warp == 0) tc_free<512>(tm);
 }
 
@@ -840,8 +920,9 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
         while (cl < 16 && tiles * cl * 2 <= num_sms && seen >= 2 * cl) cl *= 2;
     }
     const int64_t q_tiles = cl ? (a.n_q + T - 1) / T : (a.n_q + 2 * T - 1) / (2 * T);
-    const int64_t grid = q_tiles * heads * (cl ? cl : 1);
-    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const int64_t units = q_tiles * heads;
+    const int64_t grid = cl ? units * cl : units < num_sms ? units : num_sms;
+    if (units * (cl ? cl : 1) > 0x7fffffffll - num_sms) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kAttThreads);
@@ -856,9 +937,9 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
         cfg.numAttrs = 1;
     }
     return cl ? cudaLaunchKernelEx(&cfg, span_attention_kernel<true>, a, C, layer, qmap, kmap, vmap, out, lse,
-                                   (int)q_tiles, cl)
+                                   (int)q_tiles, (int)units, cl)
               : cudaLaunchKernelEx(&cfg, span_attention_kernel<false>, a, C, layer, qmap, kmap, vmap, out, lse,
-                                   (int)q_tiles, 1);
+                                   (int)q_tiles, (int)units, 1);
 }
 
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
