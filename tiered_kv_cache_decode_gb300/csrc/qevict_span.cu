@@ -524,46 +524,13 @@ constexpr int kScMass = 512;                  // threads of the four groups
 constexpr int kScThreads = kScMass + 96;
 constexpr int kScK = 2;                       // sets of two key tiles
 constexpr int kScQ = 7 - 2 * kScK;            // query tile slots
-// what lies behind the tiles in shared memory
-struct ScoreTail {
-    float ls[2][kTile];         // of a step's rows: -lse in log2 units
-    float segs[2][2][8], wins[2][8];   // masses of 16 keys from each step parity, and of windows
-    uint64_t bars[4 + 2 * kScQ + 7];
-    uint32_t slot;
-    int stop;
-};
-constexpr int kScSmem = (2 * kScK + kScQ) * kTileBytes + (int)sizeof(ScoreTail);
-static_assert(kScSmem <= 227 * 1024, "shared memory of one CTA");
-
 struct ScoreItem {
     int b, h0, nh, k0;      // sequence, KV heads, first key
     int qa, nq;             // query tiles [qa, qa + nq)
     int q_len, kv_len;
 };
-// The steps [s, end) of one CTA of an item's cluster, as KV head h and query tile q.
-struct ScoreSteps {
-    int64_t left;
-    int h, q, qa, qz;
-    __device__ __forceinline__ ScoreSteps(const ScoreItem &it, int rank, int cl) {
-        const int64_t steps = (int64_t)it.nh * it.nq, s = steps * rank / cl;
-        left = steps * (rank + 1) / cl - s;
-        qa = it.qa;
-        qz = it.qa + it.nq;
-        h = it.h0 + (it.nq ? (int)(s / it.nq) : 0);
-        q = it.qa + (it.nq ? (int)(s % it.nq) : 0);
-    }
-    // true: the next step is another KV head's
-    __device__ __forceinline__ bool next() {
-        --left;
-        if (++q < qz) return false;
-        q = qa;
-        ++h;
-        return true;
-    }
-};
-__device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int64_t item, int keys, int T,
-                                                bool per_head) {
-    // runs of the first keys, which the most queries see, come first
+// items of the first keys, which the most queries see, come first
+__device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int64_t item, int keys, int T, bool per_head) {
     ScoreItem it;
     const int units = per_head ? a.B * a.Hkv : a.B;
     const int u = (int)(item % units);
@@ -580,6 +547,45 @@ __device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int64_t item,
     it.nq = k_hi < it.k0 || hi <= lo ? 0 : (hi - 1) / T + 1 - it.qa;
     return it;
 }
+// The steps of one CTA of an item's cluster, as KV head h and query tile q.
+struct ScoreSteps {
+    int64_t left;
+    int h, q, qa, qz;
+    // true: the next step is another KV head's
+    __device__ __forceinline__ bool next() {
+        --left;
+        if (++q < qz) return false;
+        q = qa;
+        ++h;
+        return true;
+    }
+};
+struct __align__(16) ScoreWork {
+    ScoreItem it;
+    ScoreSteps s;
+};
+__device__ __forceinline__ ScoreSteps score_steps(const ScoreItem &it, int rank, int cl) {
+    ScoreSteps s;
+    const int64_t steps = (int64_t)it.nh * it.nq, at = steps * rank / cl;
+    s.left = steps * (rank + 1) / cl - at;
+    s.qa = it.qa;
+    s.qz = it.qa + it.nq;
+    s.h = it.h0 + (it.nq ? (int)(at / it.nq) : 0);
+    s.q = it.qa + (it.nq ? (int)(at % it.nq) : 0);
+    return s;
+}
+
+// what lies behind the tiles in shared memory
+struct ScoreTail {
+    float ls[2][kTile];         // of a step's rows: -lse in log2 units
+    float segs[2][2][8], wins[2][8];   // masses of 16 keys from each step parity, and of windows
+    ScoreWork given[2];         // items that the copy thread has worked out
+    uint64_t bars[4 + 2 * kScQ + 11];
+    uint32_t slot;
+    int stop, go[2];
+};
+constexpr int kScSmem = (2 * kScK + kScQ) * kTileBytes + (int)sizeof(ScoreTail);
+static_assert(kScSmem <= 227 * 1024, "shared memory of one CTA");
 
 __global__ void __launch_bounds__(kScThreads, 1)
     span_scores_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
@@ -602,12 +608,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto s_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + x); };
     auto s_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 + x); };
     auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 6);
+    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 6 + x); };
+    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 10);
     if (tid == 0) {
-        // s_full: the products and the log-sum-exps; s_empty and l_empty: each of the warps that read
-        for (int i = 0; i < 4 + 2 * kScQ + 7; ++i) {
+        // s_full: the products and the log-sum-exps; s_empty and l_empty: each of the warps that read;
+        // i_empty: every warp but the copies'
+        for (int i = 0; i < 4 + 2 * kScQ + 11; ++i) {
             const uint32_t bar = bar0 + 8 * i;
-            tc_mbar_init(bar, bar == drained ? 1 : bar >= s_empty(0) ? 8 : bar >= s_full(0) ? 2 : 1);
+            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 18 : bar >= s_empty(0) ? 8 : bar >= s_full(0) ? 2 : 1);
         }
         tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -624,29 +633,51 @@ __global__ void __launch_bounds__(kScThreads, 1)
     tc_fence_after();
     const uint32_t tm = tail.slot;   // logits of group t, buffer x at column 256 t + 128 x
     bool ok = true;
+    // The next item of a warp (c: how many it has had), false when there is none: the copy
+    // thread, which is steps ahead, has worked it out, so the other warps do not stall on it.
+    ScoreWork W;
+    float *dst = nullptr;   // mass groups: the window that the thread writes
+    auto next = [&](int c) {
+        ok = ok && __all_sync(~0u, tc_wait(i_full(c & 1), (c >> 1) & 1, &tail.stop));
+        if (!ok) return false;
+        W = tail.given[c & 1];
+        __syncwarp();
+        if ((tid & 31) == 0) tc_arrive(i_empty(c & 1));
+        return W.it.b >= 0;
+    };
 
     if (warp == 17) {
         if (tid == 17 * 32) {
-            int nk = 0, nq = 0;   // runs of one KV head and query tiles so far
-            for (int64_t item = item0; item < items && ok; item += stride) {
-                const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
-                bool head = true;
-                for (ScoreSteps s(it, rank, cl); s.left > 0; head = s.next()) {
+            int nk = 0, nq = 0, c = 0;   // runs of one KV head, query tiles and items so far
+            for (int64_t item = item0; ok; item += stride, ++c) {
+                if (item < items) {
+                    W.it = score_item(a, item, 2 * tk, T, per_head);
+                    W.s = score_steps(W.it, rank, cl);
+                } else {
+                    W.it.b = -1;   // no more
+                }
+                if (c >= 2 && !(ok = tc_wait(i_empty(c & 1), ((c >> 1) - 1) & 1, &tail.stop))) break;
+                tail.given[c & 1] = W;
+                tc_arrive(i_full(c & 1));
+                if (W.it.b < 0) break;
+                const ScoreItem &it = W.it;
+                ScoreSteps &s = W.s;
+                for (bool head = true; s.left > 0; head = s.next()) {
                     if (head) {
                         const int set = nk % kScK;
                         if (nk >= kScK && !(ok = tc_wait(k_empty(set), (nk / kScK - 1) & 1, &tail.stop))) break;
                         tc_expect_tx(k_full(set), 2 * kTileBytes);
                         for (int t = 0; t < 2; ++t)
-                            for (int c = 0; c < 2; ++c)
-                                tc_tma_4d(sm + (2 * set + t) * kTileBytes + c * kHalf, &kmap, 64 * c, s.h, it.k0 + t * tk,
+                            for (int h = 0; h < 2; ++h)
+                                tc_tma_4d(sm + (2 * set + t) * kTileBytes + h * kHalf, &kmap, 64 * h, s.h, it.k0 + t * tk,
                                           it.b, k_full(set));
                         ++nk;
                     }
                     const int q = nq % kScQ;
                     if (nq >= kScQ && !(ok = tc_wait(q_empty(q), (nq / kScQ - 1) & 1, &tail.stop))) break;
                     tc_expect_tx(q_full(q), rows * 256);
-                    for (int c = 0; c < 2; ++c)
-                        tc_tma_4d(sq + q * kTileBytes + c * kHalf, &qmap, 64 * c, s.h * a.G, s.q * T, it.b, q_full(q));
+                    for (int h = 0; h < 2; ++h)
+                        tc_tma_4d(sq + q * kTileBytes + h * kHalf, &qmap, 64 * h, s.h * a.G, s.q * T, it.b, q_full(q));
                     ++nq;
                 }
             }
@@ -664,10 +695,10 @@ __global__ void __launch_bounds__(kScThreads, 1)
         const bool lead = tc_elect();
         const uint32_t tmu = __shfl_sync(~0u, tm, 0);
         int set = kScK - 1, kp = 1, qs = 0, qp = 0, buf = 0, sp = 1;   // slots and their parities
-        for (int64_t item = item0; item < items && ok; item += stride) {
-            const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+        for (int c = 0; next(c); ++c) {
+            ScoreSteps &s = W.s;
             bool head = true;
-            for (ScoreSteps s(it, rank, cl); s.left > 0;) {
+            while (s.left > 0) {
                 if (head && ++set == kScK) set = 0, kp ^= 1;
                 // s_empty passes at once the first time
                 ok = __all_sync(~0u, tc_wait3(k_full(set), kp, q_full(qs), qp, s_empty(buf), sp, &tail.stop));
@@ -707,11 +738,11 @@ __global__ void __launch_bounds__(kScThreads, 1)
             off[e] = (int64_t)(r % a.G) * a.n_q + r / a.G;
         }
         int nq = 0;
-        for (int64_t item = item0; item < items && ok; item += stride) {
-            const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+        for (int c = 0; next(c); ++c) {
+            const ScoreItem &it = W.it;
+            ScoreSteps &s = W.s;
             const float *l0 = lse + (int64_t)it.b * a.Hq * a.n_q;
             const int64_t head = (int64_t)a.G * a.n_q;
-            ScoreSteps s(it, rank, cl);
             int64_t left = s.left;
             float v[kAhead][4];
             auto fetch = [&](float (&w)[4]) {
@@ -747,11 +778,24 @@ __global__ void __launch_bounds__(kScThreads, 1)
         const float c = kLog2e * rsqrtf((float)kHeadDim);
         const uint64_t cc = pair2(c, c);
         int nq = 0;
-        for (int64_t item = item0; item < items; item += stride) {
-            const ScoreItem it = score_item(a, item, 2 * tk, T, per_head);
+        for (int c_ = 0;; ++c_) {
+            // the first warp of a key tile decides for the eight, so that their barriers match
+            const bool first_warp = (warp & 7) == 0;
+            if (first_warp) {
+                const bool more = next(c_);
+                if ((tid & 31) == 0) tail.go[t] = more;
+            }
+            asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
+            if (!tail.go[t]) break;
+            if (!first_warp) {
+                W = tail.given[c_ & 1];
+                __syncwarp();
+                if ((tid & 31) == 0) tc_arrive(i_empty(c_ & 1));
+            }
+            const ScoreItem it = W.it;
             const int shift = it.kv_len - it.q_len, k0 = it.k0 + t * tk, j = k0 + r;
             float sum = 0.f;
-            for (ScoreSteps s(it, rank, cl); s.left > 0 && ok; s.next(), ++nq) {
+            for (ScoreSteps s = W.s; s.left > 0 && ok; s.next(), ++nq) {
                 if ((nq & 1) != x) continue;
                 const int i0 = s.q * T, p_lo = shift + i0;
                 ok = __all_sync(~0u, tc_wait(s_full(x), (nq >> 1) & 1, &tail.stop));
@@ -819,24 +863,22 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 tail.wins[t][r] = y;
             }
             asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
-            if (cl > 1) {
-                __syncwarp();
-                cl_sync();
-            }
             if (rank == 0 && x == 0 && r < tk / w && win < n_win) {
-                float y = tail.wins[t][r];
-                for (int p = 1; p < cl; ++p) y += cl_ld1(cl_addr(smem_u32(&tail.wins[t][r]), p));
-                const int u = per_head ? it.b * a.Hkv + it.h0 : it.b;
-                scores[(int64_t)u * n_win + win] = y / (per_head ? a.G : a.Hq);
-            }
-            if (cl > 1) {
-                __syncwarp();
-                cl_sync();
+                dst = scores + (int64_t)(per_head ? it.b * a.Hkv + it.h0 : it.b) * n_win + win;
+                if (cl == 1) *dst = tail.wins[t][r] / (per_head ? a.G : a.Hq);
             }
         }
     }
-    if (cl > 1 && warp >= 16) {   // clusters take one item
+    if (cl > 1) {   // clusters take one item: rank 0 adds the others' masses in order
+        __syncwarp();
         cl_sync();
+        if (dst) {
+            const uint32_t at = smem_u32(&tail.wins[warp >> 3][tid & 127]);
+            float y = 0.f;
+            for (int p = 0; p < cl; ++p) y += cl_ld1(cl_addr(at, p));
+            *dst = y / (per_head ? a.G : a.Hq);
+        }
+        __syncwarp();
         cl_sync();
     }
     __syncwarp();
