@@ -92,11 +92,12 @@ template <bool SPLIT>
 __global__ void __launch_bounds__(kAttThreads, 1)
     span_attention_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                          __nv_bfloat16 *out, float *lse, int q_tiles, int units, int cl) {
+                          __nv_bfloat16 *out, float *lse, int q_tiles, int cl) {
     constexpr int QT = SPLIT ? 1 : 2;              // query tiles of the CTA
     constexpr int NS = kAttSlots - QT;             // ring slots
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * NS + 14];
+    __shared__ uint64_t bars[2 * NS + 15];
+    __shared__ uint4 ticket;                       // wide: the answer to the copy thread's last request
     __shared__ AttUnit given[2];                   // wide: units that the copy thread has worked out
     __shared__ uint32_t slot;
     __shared__ int stop;
@@ -122,10 +123,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t q_full = bar0 + 8 * (2 * NS + 4), q_empty = bar0 + 8 * (2 * NS + 9);
     auto u_full = [&](int x) { return bar0 + 8 * (2 * NS + 10 + x); };
     auto u_empty = [&](int x) { return bar0 + 8 * (2 * NS + 12 + x); };
+    const uint32_t asked = bar0 + 8 * (2 * NS + 14);
     if (tid == 0) {
         // p_full: the group's four warps; u_empty: the product warp and both groups' warps
-        for (int i = 0; i < 2 * NS + 14; ++i)
-            tc_mbar_init(bar0 + 8 * i, i >= 2 * NS + 12 ? 9 : i >= 2 * NS + 5 && i < 2 * NS + 9 ? 4 : 1);
+        for (int i = 0; i < 2 * NS + 15; ++i)
+            tc_mbar_init(bar0 + 8 * i, i == 2 * NS + 12 || i == 2 * NS + 13 ? 9 : i >= 2 * NS + 5 && i < 2 * NS + 9 ? 4 : 1);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -160,17 +162,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 tc_arrive(u_full(c & 1));
                 ++c;
             };
-            // Wide CTAs are persistent: the units, longest first, are dealt out to and fro.
+            // A wide CTA goes on with the units of CTAs that have not started yet, longest first. It
+            // asks once the copies of the unit before are issued: the SM that is done first gets the next.
+            uint32_t at = blockIdx.x;
+            int asks = 0;
             for (int k = 0; ok; ++k) {
-                const int g = gridDim.x, at = k * g + (k & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
                 if (SPLIT) {
                     if (k) break;
-                } else if (k * g >= units) {
-                    U.n_tok = 0;   // no more
-                    give(U);
-                    break;
                 } else {
-                    if (at >= units) continue;
+                    if (k) {
+                        tc_ask(smem_u32(&ticket), asked);
+                        ok = tc_wait(asked, asks++ & 1, &stop);
+                        if (!ok) break;
+                        if (!tc_answer(smem_u32(&ticket), at)) {
+                            U.n_tok = 0;   // no more
+                            give(U);
+                            break;
+                        }
+                    }
                     U = att_unit<SPLIT>(a, at, q_tiles, T, rank, cl);
                     if (U.n_tok <= 0) continue;
                     give(U);
@@ -200,6 +209,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 while (q > 0 && !tc_try_wait(q_full, (q - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
                 for (int o = max(0, i - NS); o < i; ++o)
                     while (!tc_try_wait(full(o % NS), (o / NS) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+                while (asks > 0 && !tc_try_wait(asked, (asks - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
             }
         }
         if (warp == 8) {   // the whole warp keeps step, one lane issues
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && stop) set_status(C, QEVICT_ERR_TIMEOUT, layer, blockIdx.x, 0);
+    if (tid == 0 && stop) set_status(C, QEVICT_ERR_TIMEOUT, layer, (int)blockIdx.x, 0);
     if (warp == 0) tc_free<512>(tm);
 }
 
@@ -530,14 +540,14 @@ struct ScoreItem {
     int q_len, kv_len;
 };
 // items of the first keys, which the most queries see, come first
-__device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int64_t item, int keys, int T, bool per_head) {
+__device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int item, int keys, int T, bool per_head) {
     ScoreItem it;
     const int units = per_head ? a.B * a.Hkv : a.B;
-    const int u = (int)(item % units);
+    const int u = item % units;
     it.b = per_head ? u / a.Hkv : u;
     it.h0 = per_head ? u % a.Hkv : 0;
     it.nh = per_head ? 1 : a.Hkv;
-    it.k0 = (int)(item / units) * keys;
+    it.k0 = item / units * keys;
     it.q_len = clamped(a.q_len, it.b, a.n_q);
     it.kv_len = clamped(a.kv_len, it.b, a.n_kv);
     const int shift = it.kv_len - it.q_len, k_hi = min(it.k0 + keys, it.kv_len) - 1;
@@ -580,7 +590,8 @@ struct ScoreTail {
     float ls[2][kTile];         // of a step's rows: -lse in log2 units
     float segs[2][2][8], wins[2][8];   // masses of 16 keys from each step parity, and of windows
     ScoreWork given[2];         // items that the copy thread has worked out
-    uint64_t bars[4 + 2 * kScQ + 11];
+    uint4 ticket;               // the answer to the copy thread's last request
+    uint64_t bars[4 + 2 * kScQ + 12];
     uint32_t slot;
     int stop, go[2];
 };
@@ -590,13 +601,12 @@ static_assert(kScSmem <= 227 * 1024, "shared memory of one CTA");
 __global__ void __launch_bounds__(kScThreads, 1)
     span_scores_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
                        const __grid_constant__ CUtensorMap kmap, const float *lse, float *scores, int w, int n_win,
-                       int per_head, int64_t items, int cl) {
+                       int per_head, int cl) {
     extern __shared__ __align__(1024) uint8_t gen[];
     ScoreTail &tail = *reinterpret_cast<ScoreTail *>(gen + (2 * kScK + kScQ) * kTileBytes);
     const int T = span_tile_tokens(a.G), rows = T * a.G;
     const int tk = kTile / w * w;
     const int rank = blockIdx.x % cl;
-    const int64_t item0 = blockIdx.x / cl, stride = gridDim.x / cl;
 
     const uint32_t sm = smem_u32(gen), sq = sm + 2 * kScK * kTileBytes;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
@@ -610,11 +620,11 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
     auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 6 + x); };
     auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 10);
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 10), asked = drained + 8;
     if (tid == 0) {
         // s_full: the products and the log-sum-exps; s_empty and l_empty: each of the warps that read;
         // i_empty: every warp but the copies'
-        for (int i = 0; i < 4 + 2 * kScQ + 11; ++i) {
+        for (int i = 0; i < 4 + 2 * kScQ + 12; ++i) {
             const uint32_t bar = bar0 + 8 * i;
             tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 18 : bar >= s_empty(0) ? 8 : bar >= s_full(0) ? 2 : 1);
         }
@@ -649,12 +659,21 @@ __global__ void __launch_bounds__(kScThreads, 1)
     if (warp == 17) {
         if (tid == 17 * 32) {
             int nk = 0, nq = 0, c = 0;   // runs of one KV head, query tiles and items so far
-            for (int64_t item = item0; ok; item += stride, ++c) {
-                if (item < items) {
-                    W.it = score_item(a, item, 2 * tk, T, per_head);
+            int asks = 0;
+            uint32_t at = blockIdx.x;
+            for (; ok; ++c) {
+                bool more = c == 0;
+                if (c && cl == 1) {   // alone, the CTA goes on with the items of CTAs that have not started yet
+                    tc_ask(smem_u32(&tail.ticket), asked);
+                    ok = tc_wait(asked, asks++ & 1, &tail.stop);
+                    if (!ok) break;
+                    more = tc_answer(smem_u32(&tail.ticket), at);
+                }
+                if (more) {
+                    W.it = score_item(a, at / cl, 2 * tk, T, per_head);
                     W.s = score_steps(W.it, rank, cl);
                 } else {
-                    W.it.b = -1;   // no more
+                    W.it.b = -1;
                 }
                 if (c >= 2 && !(ok = tc_wait(i_empty(c & 1), ((c >> 1) - 1) & 1, &tail.stop))) break;
                 tail.given[c & 1] = W;
@@ -687,6 +706,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     while (!tc_try_wait(k_full(o % kScK), (o / kScK) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
                 for (int o = max(0, nq - kScQ); o < nq; ++o)
                     while (!tc_try_wait(q_full(o % kScQ), (o / kScQ) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+                while (asks > 0 && !tc_try_wait(asked, (asks - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
             }
         }
         __syncwarp();
@@ -963,8 +983,8 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
     }
     const int64_t q_tiles = cl ? (a.n_q + T - 1) / T : (a.n_q + 2 * T - 1) / (2 * T);
     const int64_t units = q_tiles * heads;
-    const int64_t grid = cl ? units * cl : units < num_sms ? units : num_sms;
-    if (units * (cl ? cl : 1) > 0x7fffffffll - num_sms) return cudaErrorInvalidConfiguration;
+    const int64_t grid = units * (cl ? cl : 1);
+    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kAttThreads);
@@ -979,9 +999,9 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
         cfg.numAttrs = 1;
     }
     return cl ? cudaLaunchKernelEx(&cfg, span_attention_kernel<true>, a, C, layer, qmap, kmap, vmap, out, lse,
-                                   (int)q_tiles, (int)units, cl)
+                                   (int)q_tiles, cl)
               : cudaLaunchKernelEx(&cfg, span_attention_kernel<false>, a, C, layer, qmap, kmap, vmap, out, lse,
-                                   (int)q_tiles, (int)units, 1);
+                                   (int)q_tiles, 1);
 }
 
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
@@ -1012,8 +1032,7 @@ cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, 
         }
         cl = best_cluster(items, total, heavy, num_sms, active[dev], 6);
     }
-    int64_t grid = items * cl;
-    if (cl == 1 && grid > num_sms) grid = num_sms;
+    const int64_t grid = items * cl;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
@@ -1028,8 +1047,7 @@ cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, 
         cfg.attrs = &at;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, span_scores_kernel, a, C, layer, qmap, kmap, lse, scores, w, n_win, per_head ? 1 : 0,
-                              items, cl);
+    return cudaLaunchKernelEx(&cfg, span_scores_kernel, a, C, layer, qmap, kmap, lse, scores, w, n_win, per_head ? 1 : 0, cl);
 }
 
 }  // namespace qevict

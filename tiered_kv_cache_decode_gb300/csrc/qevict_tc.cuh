@@ -177,6 +177,29 @@ __device__ __forceinline__ void tc_tie(float (&r)[32]) {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Dynamic scheduling: a running CTA takes over the next CTA of its grid that has not
+// started. The request's answer (16 bytes) completes on `bar`; after a false
+// answer there is nothing left to ask for.
+__device__ __forceinline__ void tc_ask(uint32_t answer, uint32_t bar) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the last answer has been read
+    tc_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ bool tc_answer(uint32_t answer, uint32_t &block) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(block)
+        : "r"(answer)
+        : "memory");
+    return ok != 0;
+}
+
 // pairs of fp32 in one register pair
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
     uint64_t r;
