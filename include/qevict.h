@@ -347,9 +347,10 @@ qevict_status qevict_k_channel_weights(qevict_cache *cache, int32_t layer, const
  * uncompressed keys, and the window scores on which qevict_prefill routes. The
  * three calls take their head counts, sequences and window size from the cache
  * (with per-head tiers too: [batch] is the number of sequences and Hq, Hkv the
- * model's heads), read nothing else of it unless said so, keep no scratch and
- * may run concurrently with one another and with decodes. The cache's device
- * must be current (INVALID_ARG otherwise).
+ * model's heads) and read nothing else of it unless said so. Like any calls,
+ * those on one layer are ordered; those on different layers may run
+ * concurrently, and none uses the decode scratch. The cache's device must be
+ * current (INVALID_ARG otherwise).
  *
  * For every token and head x of 128 channels of q and k: y = x / sqrt(mean(x^2)
  * + eps) * weight, then each pair (a, b) of channels turns by the angle t =

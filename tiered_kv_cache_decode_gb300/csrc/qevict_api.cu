@@ -425,6 +425,7 @@ qevict_status qevict_cache_create(const qevict_config *config, const qevict_allo
         const size_t o_dg = cv.take((size_t)B * 8 * 4);
         const size_t o_lb = cv.take((size_t)B * Wmax);
         const size_t o_kg = cv.take((size_t)B * Hkv * kGroups);
+        const size_t o_sp = cv.take((size_t)kSpanPartFloats * 4);
         uint8_t *base = (uint8_t *)dev_alloc(c, cv.off);
         if (!base) {
             const size_t need = cv.off;
@@ -451,6 +452,7 @@ qevict_status qevict_cache_create(const qevict_config *config, const qevict_allo
         D.diag = (int32_t *)(base + o_dg);
         D.lbits = base + o_lb;
         D.kgw = base + o_kg;
+        D.span_part = (float *)(base + o_sp);
     }
     err = prepare_decode();
     EncodeTiledFn enc = encode_tiled();
@@ -776,8 +778,8 @@ qevict_status qevict_span_scores(qevict_cache *c, int32_t layer, const void *q, 
     cudaError_t e = encode_tokens(&qm, q, a.B, n_q, a.Hq, a.G, span_tile_tokens(a.G));
     if (e == cudaSuccess) e = encode_tokens(&km, k, a.B, n_kv, a.Hkv, 1, 128);
     if (e == cudaSuccess)
-        e = launch_span_scores(a, c->cdev, layer, qm, km, lse, scores, c->cfg.window, c->hs > 1, c->num_sms,
-                               (cudaStream_t)stream);
+        e = launch_span_scores(a, c->cdev, layer, qm, km, lse, scores, c->layers[layer].dev.span_part, c->cfg.window,
+                               c->hs > 1, c->num_sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "span scores kernel");
     note_op(c, -1, stream);
     return QEVICT_OK;

@@ -19,6 +19,8 @@ constexpr int kGroup = 32;             // channels per INT2 group
 constexpr int kGroups = kHeadDim / kGroup;
 constexpr int kMaxG = 8;               // query heads per KV head
 constexpr int kMaxSplits = 32;         // decode CTAs per (sequence, KV head)
+constexpr int kMaxSpanParts = 16;      // parts into which a run of keys' window scores is split
+constexpr int kSpanPartFloats = 1 << 16;   // a layer's room for their sums
 constexpr int kMaxSpanTokens = 1 << 29; // tokens per sequence of the span calls (int sums stay in range)
 constexpr int kVTile = 16;             // tokens per transposed V-code word
 constexpr int kCtrN = 16;              // counters per sequence
@@ -106,6 +108,7 @@ struct LayerDev {
     int4 *work_c;         // [B][Wmax] prefill copy: {window, dst fp slot, 0, 0}
     int32_t *diag;        // [B][8] counts of the last completed tier move (see qevict_get_tier_move_counts)
     uint8_t *lbits;       // [B][Wmax] width of the window's ledger entry: 0 (none), 2, 4 or 8
+    float *span_part;     // [kSpanPartFloats] partial window scores of qevict_span_scores
     uint8_t *kgw;         // [B][Hkv][4] K group widths (0, 2, 4, 8) where ctr[CTR_KCH] is set
 };
 
@@ -259,10 +262,10 @@ __host__ __device__ inline int span_tile_tokens(int G) { return 128 / G; }
 cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
                                   const CUtensorMap &kmap, const CUtensorMap &vmap, __nv_bfloat16 *out, float *lse,
                                   int num_sms, cudaStream_t s);
-// scores fp32 [B][n_win], or [B * Hkv][n_win] with per_head
+// scores fp32 [B][n_win], or [B * Hkv][n_win] with per_head; part: kSpanPartFloats of the layer's own
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
-                               const CUtensorMap &kmap, const float *lse, float *scores, int w, bool per_head,
-                               int num_sms, cudaStream_t s);
+                               const CUtensorMap &kmap, const float *lse, float *scores, float *part, int w,
+                               bool per_head, int num_sms, cudaStream_t s);
 cudaError_t launch_read_lengths(const LayerDev &L, int32_t *out, cudaStream_t s);
 // kmap: k_full [sequences * n_tokens][Hkv * hs][128] bf16 as a 3-D tiled map,
 // boxes of 64 channels x 1 KV head x 16 tokens, 128-byte swizzle

@@ -523,9 +523,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // mass is a sum along its own lane, in one register, over all query tiles.
 // An item is a run of 256 keys (rounded down to whole windows) of one sequence
 // (of one KV head with per-head units); its steps are the (KV head, query tile)
-// pairs that see some of them. A cluster of CTAs shares an item's steps
-// evenly and adds its sums in rank order; with one CTA per item the CTAs
-// are persistent and the copies of the next item run under this one.
+// pairs that see some of them. Where the items are few, each is split into parts
+// of as many steps, whose sums a second kernel adds in order. CTAs go on with the
+// work of CTAs that have not started, the longest first, and the copies of the
+// next item run under this one.
 // Four groups of four warps take the masses, each of one key tile in every other
 // step from a logit tile of its own, so that their waits and loads fall at
 // different times; one warp issues the products, one the copies, and one fetches
@@ -557,7 +558,7 @@ __device__ __forceinline__ ScoreItem score_item(const SpanArgs &a, int item, int
     it.nq = k_hi < it.k0 || hi <= lo ? 0 : (hi - 1) / T + 1 - it.qa;
     return it;
 }
-// The steps of one CTA of an item's cluster, as KV head h and query tile q.
+// The steps of one part of an item, as KV head h and query tile q.
 struct ScoreSteps {
     int64_t left;
     int h, q, qa, qz;
@@ -573,11 +574,12 @@ struct ScoreSteps {
 struct __align__(16) ScoreWork {
     ScoreItem it;
     ScoreSteps s;
+    int part;
 };
-__device__ __forceinline__ ScoreSteps score_steps(const ScoreItem &it, int rank, int cl) {
+__device__ __forceinline__ ScoreSteps score_steps(const ScoreItem &it, int part, int parts) {
     ScoreSteps s;
-    const int64_t steps = (int64_t)it.nh * it.nq, at = steps * rank / cl;
-    s.left = steps * (rank + 1) / cl - at;
+    const int64_t steps = (int64_t)it.nh * it.nq, at = steps * part / parts;
+    s.left = steps * (part + 1) / parts - at;
     s.qa = it.qa;
     s.qz = it.qa + it.nq;
     s.h = it.h0 + (it.nq ? (int)(at / it.nq) : 0);
@@ -588,7 +590,7 @@ __device__ __forceinline__ ScoreSteps score_steps(const ScoreItem &it, int rank,
 // what lies behind the tiles in shared memory
 struct ScoreTail {
     float ls[2][kTile];         // of a step's rows: -lse in log2 units
-    float segs[2][2][8], wins[2][8];   // masses of 16 keys from each step parity, and of windows
+    float segs[2][2][8];        // masses of 16 keys from each step parity
     ScoreWork given[2];         // items that the copy thread has worked out
     uint4 ticket;               // the answer to the copy thread's last request
     uint64_t bars[4 + 2 * kScQ + 12];
@@ -600,13 +602,12 @@ static_assert(kScSmem <= 227 * 1024, "shared memory of one CTA");
 
 __global__ void __launch_bounds__(kScThreads, 1)
     span_scores_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
-                       const __grid_constant__ CUtensorMap kmap, const float *lse, float *scores, int w, int n_win,
-                       int per_head, int cl) {
+                       const __grid_constant__ CUtensorMap kmap, const float *lse, float *scores, float *part, int w,
+                       int n_win, int per_head, int parts) {
     extern __shared__ __align__(1024) uint8_t gen[];
     ScoreTail &tail = *reinterpret_cast<ScoreTail *>(gen + (2 * kScK + kScQ) * kTileBytes);
     const int T = span_tile_tokens(a.G), rows = T * a.G;
     const int tk = kTile / w * w;
-    const int rank = blockIdx.x % cl;
 
     const uint32_t sm = smem_u32(gen), sq = sm + 2 * kScK * kTileBytes;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
@@ -646,7 +647,6 @@ __global__ void __launch_bounds__(kScThreads, 1)
     // The next item of a warp (c: how many it has had), false when there is none: the copy
     // thread, which is steps ahead, has worked it out, so the other warps do not stall on it.
     ScoreWork W;
-    float *dst = nullptr;   // mass groups: the window that the thread writes
     auto next = [&](int c) {
         ok = ok && __all_sync(~0u, tc_wait(i_full(c & 1), (c >> 1) & 1, &tail.stop));
         if (!ok) return false;
@@ -663,15 +663,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
             uint32_t at = blockIdx.x;
             for (; ok; ++c) {
                 bool more = c == 0;
-                if (c && cl == 1) {   // alone, the CTA goes on with the items of CTAs that have not started yet
+                if (c) {   // the CTA goes on with the work of CTAs that have not started yet
                     tc_ask(smem_u32(&tail.ticket), asked);
                     ok = tc_wait(asked, asks++ & 1, &tail.stop);
                     if (!ok) break;
                     more = tc_answer(smem_u32(&tail.ticket), at);
                 }
                 if (more) {
-                    W.it = score_item(a, at / cl, 2 * tk, T, per_head);
-                    W.s = score_steps(W.it, rank, cl);
+                    W.it = score_item(a, at / parts, 2 * tk, T, per_head);
+                    W.part = at % parts;
+                    W.s = score_steps(W.it, W.part, parts);
                 } else {
                     W.it.b = -1;
                 }
@@ -877,29 +878,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
             if ((r & 15) == 0) tail.segs[t][x][r >> 4] = sum;
             asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
             const int win = k0 / w + r;
-            if (x == 0 && r < tk / w) {
-                float y = 0.f;
-                for (int e = r * (w / 16); e < (r + 1) * (w / 16); ++e) y += tail.segs[t][0][e] + tail.segs[t][1][e];
-                tail.wins[t][r] = y;
-            }
-            asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
-            if (rank == 0 && x == 0 && r < tk / w && win < n_win) {
-                dst = scores + (int64_t)(per_head ? it.b * a.Hkv + it.h0 : it.b) * n_win + win;
-                if (cl == 1) *dst = tail.wins[t][r] / (per_head ? a.G : a.Hq);
+            float mass = 0.f;
+            if (x == 0 && r < tk / w)
+                for (int e = r * (w / 16); e < (r + 1) * (w / 16); ++e) mass += tail.segs[t][0][e] + tail.segs[t][1][e];
+            if (x == 0 && r < tk / w && win < n_win) {
+                const int units = per_head ? a.B * a.Hkv : a.B, u = per_head ? it.b * a.Hkv + it.h0 : it.b;
+                if (parts == 1) scores[(int64_t)u * n_win + win] = mass / (per_head ? a.G : a.Hq);
+                else part[((int64_t)W.part * units + u) * n_win + win] = mass;
             }
         }
-    }
-    if (cl > 1) {   // clusters take one item: rank 0 adds the others' masses in order
-        __syncwarp();
-        cl_sync();
-        if (dst) {
-            const uint32_t at = smem_u32(&tail.wins[warp >> 3][tid & 127]);
-            float y = 0.f;
-            for (int p = 0; p < cl; ++p) y += cl_ld1(cl_addr(at, p));
-            *dst = y / (per_head ? a.G : a.Hq);
-        }
-        __syncwarp();
-        cl_sync();
     }
     __syncwarp();
     tc_fence_before();
@@ -908,9 +895,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
     if (warp == 0) tc_free<512>(tm);
 }
 
-}  // namespace
-
-namespace {
+// The parts' window masses in order, one window a thread.
+__global__ void __launch_bounds__(128) span_scores_sum_kernel(const float *part, float *scores, int64_t n, int parts,
+                                                              float heads) {
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (i >= n) return;
+    float y = 0.f;
+    for (int p = 0; p < parts; ++p) y += part[p * n + i];
+    scores[i] = y / heads;
+}
 
 // How many clusters of each size the device holds at once (its SMs come in
 // groups of unlike size, so 8 CTAs fill fewer SMs than 4 or 9 do).
@@ -935,19 +928,15 @@ cudaError_t prepare_clusters(K kernel, int threads, int smem, int *active) {
     return e;
 }
 
-// CTAs per item that finish `items` items of `total` steps (the heaviest of
-// `heavy`) first, where starting a cluster's item costs `start` steps.
-int best_cluster(int64_t items, int64_t total, int64_t heavy, int num_sms, const int *active, int start) {
+// CTAs per query tile that finish `tiles` tiles of `seen` key tiles each first, and in how many us.
+int best_cluster(int64_t tiles, int64_t seen, int num_sms, const int *active, double *least) {
     int best = 1;
-    double least = 0;
-    for (int c = 1; c <= kMaxCluster && (c == 1 || heavy >= c); ++c) {
+    for (int c = 1; c <= kMaxCluster && (c == 1 || seen >= 2 * c); ++c) {
         const int n = c == 1 ? num_sms : active[c];
         if (n < 1) continue;
-        const double rounds = (double)((items + n - 1) / n);
-        const double mean = rounds * (double)total / (double)items;
-        const double t = (mean > (double)heavy ? mean : (double)heavy) / c + rounds * (c == 1 ? start / 2 : start);
-        if (c == 1 || t < least) {
-            least = t;
+        const double t = (double)((tiles + n - 1) / n) * ((double)((seen + c - 1) / c) * 0.88 + (c == 1 ? 4 : 5));
+        if (c == 1 || t < *least) {
+            *least = t;
             best = c;
         }
     }
@@ -959,14 +948,15 @@ int best_cluster(int64_t items, int64_t total, int64_t heavy, int num_sms, const
 cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
                                   const CUtensorMap &kmap, const CUtensorMap &vmap, __nv_bfloat16 *out, float *lse,
                                   int num_sms, cudaStream_t s) {
-    cudaError_t e = once_per_device(0, [&] {
-        cudaError_t r = cudaFuncSetAttribute(span_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kAttSmem);
-        if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(span_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttSmem);
-        if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(span_attention_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return r;
+    static int active[kOnceDevices][kMaxCluster + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev >= kOnceDevices) e = cudaErrorInvalidDevice;
+    if (e != cudaSuccess) return e;
+    e = once_per_device(0, [&] {
+        const cudaError_t r = cudaFuncSetAttribute(span_attention_kernel<false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kAttSmem);
+        return r == cudaSuccess ? prepare_clusters(span_attention_kernel<true>, kAttThreads, kAttSmem, active[dev]) : r;
     });
     if (e != cudaSuccess) return e;
     const int T = span_tile_tokens(a.G);
@@ -974,12 +964,15 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
     // key tiles that a query tile sees at most
     const int64_t seen = ((int64_t)a.span + T < a.n_kv ? ((int64_t)a.span + T) / kTile + 2 + (a.sinks + kTile - 1) / kTile
                                                        : (a.n_kv + kTile - 1) / kTile);
+    // The wide form where its units fill the SMs. Below that, whichever ends first: a wide CTA takes
+    // about 1.45 us a key tile (two query tiles), a split one 0.88 us (one), and a unit about 4 us to
+    // start and to write (512 tokens of 16K contexts, 2 x 8 KV heads: 183 and 221 us).
     const int64_t wide = (a.n_q + 2 * T - 1) / (2 * T) * heads;
     int cl = 0;   // 0: wide
     if (wide < num_sms) {
-        const int64_t tiles = (a.n_q + T - 1) / T * heads;
-        cl = 1;
-        while (cl < 16 && tiles * cl * 2 <= num_sms && seen >= 2 * cl) cl *= 2;
+        double split = 0;
+        cl = best_cluster((a.n_q + T - 1) / T * heads, seen, num_sms, active[dev], &split);
+        if (seen * 1.45 + 4 < split) cl = 0;
     }
     const int64_t q_tiles = cl ? (a.n_q + T - 1) / T : (a.n_q + 2 * T - 1) / (2 * T);
     const int64_t units = q_tiles * heads;
@@ -1005,21 +998,19 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
 }
 
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
-                               const CUtensorMap &kmap, const float *lse, float *scores, int w, bool per_head,
-                               int num_sms, cudaStream_t s) {
-    static int active[kOnceDevices][kMaxCluster + 1];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && dev >= kOnceDevices) e = cudaErrorInvalidDevice;
-    if (e != cudaSuccess) return e;
-    e = once_per_device(0, [&] { return prepare_clusters(span_scores_kernel, kScThreads, kScSmem, active[dev]); });
+                               const CUtensorMap &kmap, const float *lse, float *scores, float *part, int w,
+                               bool per_head, int num_sms, cudaStream_t s) {
+    cudaError_t e = once_per_device(0, [&] {
+        return cudaFuncSetAttribute(span_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScSmem);
+    });
     if (e != cudaSuccess) return e;
     const int keys = 2 * (kTile / w * w), T = span_tile_tokens(a.G);
     const int runs = (a.n_kv + keys - 1) / keys, n_win = (a.n_kv + w - 1) / w;
     const int units = per_head ? a.B * a.Hkv : a.B;
-    const int64_t items = (int64_t)runs * units;
-    // Steps of each item, at the lengths that the host knows; one CTA per item when there are many.
-    int cl = 1;
+    const int64_t items = (int64_t)runs * units, wins = (int64_t)units * n_win;
+    // Parts per item: enough that the longest (at the lengths that the host knows) does not
+    // outlast an even share of the SMs, and no shorter than two steps.
+    int parts = 1;
     if (items < 8 * num_sms) {
         int64_t heavy = 0, total = 0;
         for (int x = 0; x < runs; ++x) {
@@ -1030,24 +1021,19 @@ cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, 
             heavy = steps > heavy ? steps : heavy;
             total += steps * units;
         }
-        cl = best_cluster(items, total, heavy, num_sms, active[dev], 6);
+        while (parts < kMaxSpanParts && 2 * parts * wins <= kSpanPartFloats && heavy >= 4 * parts &&
+               heavy * num_sms * 2 > total * parts)
+            parts *= 2;
     }
-    const int64_t grid = items * cl;
+    const int64_t grid = items * parts;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kScThreads);
-    cfg.dynamicSmemBytes = kScSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cl;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    if (cl > 1) {
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, span_scores_kernel, a, C, layer, qmap, kmap, lse, scores, w, n_win, per_head ? 1 : 0, cl);
+    span_scores_kernel<<<(unsigned)grid, kScThreads, kScSmem, s>>>(a, C, layer, qmap, kmap, lse, scores, part, w, n_win,
+                                                                   per_head ? 1 : 0, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || parts == 1) return e;
+    span_scores_sum_kernel<<<(unsigned)((wins + 127) / 128), 128, 0, s>>>(part, scores, wins, parts,
+                                                                          (float)(per_head ? a.G : a.Hq));
+    return cudaGetLastError();
 }
 
 }  // namespace qevict
