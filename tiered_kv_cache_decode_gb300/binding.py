@@ -450,19 +450,27 @@ class TieredCache:
         if nk != n or nv != n:
             raise ValueError(f"q, k and v must have the same tokens, got {n}, {nk} and {nv}")
         like, dense = torch.empty_like, torch.contiguous_format
-        q_out = like(q, memory_format=dense) if q_out is None else q_out
-        k_out = like(k, memory_format=dense) if k_out is None else k_out
-        if v is not None:
-            v_out = like(v, memory_format=dense) if v_out is None else v_out
-        elif v_out is not None:
-            raise ValueError("v_out without v")
+        if q_out is None:
+            q_out = like(q, memory_format=dense)
+        else:
+            side(q_out, q.shape, bf, "q_out")
+        if k_out is None:
+            k_out = like(k, memory_format=dense)
+        else:
+            side(k_out, k.shape, bf, "k_out")
+        if v is None:
+            if v_out is not None:
+                raise ValueError("v_out without v")
+        elif v_out is None:
+            v_out = like(v, memory_format=dense)
+        else:
+            side(v_out, v.shape, bf, "v_out")
         rc = self.lib.qevict_qk_norm_rope(
             self.handle, layer, q.data_ptr(), qs, k.data_ptr(), ks, None if v is None else v.data_ptr(), vs, n,
             side(positions, (self.B, n), torch.int64, "positions"), side(q_weight, (HEAD_DIM,), bf, "q_weight"),
             side(k_weight, (HEAD_DIM,), bf, "k_weight"), eps,
             side(inv_freq, (HEAD_DIM // 2,), torch.float32, "inv_freq"), 1 if interleaved else 0,
-            side(q_out, q.shape, bf, "q_out"), side(k_out, k.shape, bf, "k_out"),
-            None if v is None else side(v_out, v.shape, bf, "v_out"), self._raw_stream(stream))
+            q_out.data_ptr(), k_out.data_ptr(), None if v is None else v_out.data_ptr(), self._raw_stream(stream))
         if rc:
             self._check(rc)
         return (q_out, k_out) if v is None else (q_out, k_out, v_out)
