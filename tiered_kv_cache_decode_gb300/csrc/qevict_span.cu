@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
     const int T = span_tile_tokens(a.G), rows = T * a.G;
     const int rank = SPLIT ? blockIdx.x % cl : 0;
+    if (threadIdx.x < 3) tc_prefetch_map(threadIdx.x == 0 ? &qmap : threadIdx.x == 1 ? &kmap : &vmap);
     AttUnit U;
     if (SPLIT) {   // one unit
         U = att_unit<SPLIT>(a, blockIdx.x / cl, q_tiles, T, rank, cl);
@@ -124,18 +125,44 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     auto u_full = [&](int x) { return bar0 + 8 * (2 * NS + 10 + x); };
     auto u_empty = [&](int x) { return bar0 + 8 * (2 * NS + 12 + x); };
     const uint32_t asked = bar0 + 8 * (2 * NS + 14);
-    if (tid == 0) {
+    // The ring holds key and value tiles in the order in which the products use them: K0 V0 K1 V1 ..,
+    // split K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1). The copy thread's loads, of a unit's query tiles
+    // and of its item x as the i-th of the ring:
+    auto load_q = [&] {
+        tc_expect_tx(q_full, QT * rows * 256);
+        for (int t = 0; t < QT; ++t)
+            for (int h = 0; h < 2; ++h)
+                tc_tma_4d(sm + t * kTileBytes + h * kHalf, &qmap, 64 * h, U.kvh * a.G, U.i0 + t * T, U.b, q_full);
+    };
+    auto load_item = [&](int x, int i) {
+        const int s = i % NS;
+        const bool last = x == 2 * U.n - 1;
+        const bool isk = SPLIT ? x == 0 || (x & 1 && !last) : !(x & 1);
+        const int j = SPLIT ? (isk ? (x + 1) / 2 : last ? U.n - 1 : x / 2 - 1) : x / 2;
+        tc_expect_tx(full(s), kTileBytes);
+        for (int h = 0; h < 2; ++h)
+            tc_tma_4d(ring + s * kTileBytes + h * kHalf, isk ? &kmap : &vmap, 64 * h, U.kvh, U.tl.key(U.first + j), U.b,
+                      full(s));
+    };
+    if (tid == 9 * 32) {
         // p_full: the group's four warps; u_empty: the product warp and both groups' warps
         for (int i = 0; i < 2 * NS + 15; ++i)
             tc_mbar_init(bar0 + 8 * i, i == 2 * NS + 12 || i == 2 * NS + 13 ? 9 : i >= 2 * NS + 5 && i < 2 * NS + 9 ? 4 : 1);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (SPLIT && U.n > 0) {   // a short unit's latency counts: its first copies do not wait for the set-up
+            load_q();
+            for (int x = 0; x < min(2 * U.n, NS); ++x) load_item(x, x);
+        }
     }
+    __syncwarp();
     if (warp == 0) tc_alloc<512>(smem_u32(&slot));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = slot;                      // S of group t at column 128 t, O at 256 + 128 t
+
     // The next unit of a warp (c: how many it has had), false when there is none. Wide: the copy
     // thread, which is tiles ahead, has worked it out, so the other warps do not stall on it.
     auto next = [&](int c, bool &ok) {
@@ -152,8 +179,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (tid == 9 * 32) {
-            // The ring holds key and value tiles in the order in which the products use them: K0 V0 K1 V1 ..,
-            // split K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
             int i = 0, q = 0, c = 0;
             bool ok = true;
             auto give = [&](const AttUnit &X) {
@@ -186,22 +211,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (!ok) break;
                 }
                 if (U.n <= 0) continue;
-                if (q > 0 && !(ok = tc_wait(q_empty, (q - 1) & 1, &stop))) break;
-                tc_expect_tx(q_full, QT * rows * 256);
-                for (int t = 0; t < QT; ++t)
-                    for (int h = 0; h < 2; ++h)
-                        tc_tma_4d(sm + t * kTileBytes + h * kHalf, &qmap, 64 * h, U.kvh * a.G, U.i0 + t * T, U.b, q_full);
+                if (SPLIT) {
+                    i = min(2 * U.n, NS);   // these are on their way
+                } else {
+                    if (q > 0 && !(ok = tc_wait(q_empty, (q - 1) & 1, &stop))) break;
+                    load_q();
+                }
                 ++q;
-                for (int x = 0; x < 2 * U.n; ++x, ++i) {
-                    const int s = i % NS;
-                    if (i >= NS && !(ok = tc_wait(empty(s), (i / NS - 1) & 1, &stop))) break;
-                    const bool last = x == 2 * U.n - 1;
-                    const bool isk = SPLIT ? x == 0 || (x & 1 && !last) : !(x & 1);
-                    const int j = SPLIT ? (isk ? (x + 1) / 2 : last ? U.n - 1 : x / 2 - 1) : x / 2;
-                    tc_expect_tx(full(s), kTileBytes);
-                    for (int h = 0; h < 2; ++h)
-                        tc_tma_4d(ring + s * kTileBytes + h * kHalf, isk ? &kmap : &vmap, 64 * h, U.kvh,
-                                  U.tl.key(U.first + j), U.b, full(s));
+                for (int x = SPLIT ? i : 0; x < 2 * U.n; ++x, ++i) {
+                    if (i >= NS && !(ok = tc_wait(empty(i % NS), (i / NS - 1) & 1, &stop))) break;
+                    load_item(x, i);
                 }
             }
             if (!ok) {   // gave up: the copies in flight land before the CTA ends

@@ -62,6 +62,11 @@ __device__ __forceinline__ void tc_tma_4d(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// the descriptor of a tensor map into the cache, ahead of its first copy
+__device__ __forceinline__ void tc_prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 __device__ __forceinline__ bool tc_elect() {
     uint32_t p;
     asm volatile(
