@@ -394,8 +394,9 @@ qevict_status qevict_qk_norm_rope(qevict_cache *cache, int32_t layer, const void
  *        their product with V as bf16.
  *  lse   fp32 [batch][Hq][n_q] or NULL: log(sum(exp(q K^T / sqrt(d)))).
  * A query that sees no key (p < 0) gets out 0 and lse -inf. Rows at or past
- * q_len[b] are not written. Keys and values that no query of the call sees
- * (at or past kv_len, before the span) may hold anything, NaN included.
+ * q_len[b] are not written. What a key or value that a query does not see holds
+ * (later keys, keys before its span, rows at or past kv_len; NaN and infinities
+ * too) never reaches that query's row.
  * n_q and n_kv are in [1, 2^29]. */
 qevict_status qevict_span_attention(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
                                     const void *v, int32_t n_kv, const int32_t *q_len, const int32_t *kv_len,

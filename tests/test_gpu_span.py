@@ -206,6 +206,50 @@ def test_span_attention_values_outside_the_span_may_be_anything():
     check_attention(q, *clean, out, lse, [n_q], [n_kv], span, sinks)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,n_q,n_kv,span,sinks,bad", [
+    (1, 8, 2, 300, 300, 0, 0, (5, 130, 299)), (1, 4, 4, 700, 700, 0, 0, (0, 256, 511)), (2, 14, 2, 257, 257, 0, 0, (200,)),
+    (1, 8, 2, 400, 400, 60, 5, (2, 100, 131, 260, 390)), (1, 4, 4, 600, 600, 130, 3, (1, 3, 255, 400)),
+    (1, 16, 2, 20, 900, 0, 0, (890, 3)), (1, 8, 1, 17, 900, 50, 4, (840, 885, 2)), (1, 32, 8, 1100, 1100, 0, 0, (1000,))])
+def test_span_attention_non_finite_values_reach_only_rows_that_see_them(B, Hq, Hkv, n_q, n_kv, span, sinks, bad):
+    q, k, v = rand(1, B, n_q, Hq, D), rand(2, B, n_kv, Hkv, D), rand(3, B, n_kv, Hkv, D)
+    clean = v.clone()
+    for i, j in enumerate(bad):   # one channel of one KV head each, NaN and both infinities
+        value = (float("nan"), float("inf"), float("-inf"))[i % 3]
+        v[B - 1, j, i % Hkv, 7 * i + 3] = value
+        clean[B - 1, j, i % Hkv, 7 * i + 3] = 0.0
+    cache = cache_for(B, Hq, Hkv)
+    out, lse = cache.span_attention(0, q.cuda(), k.cuda(), v.cuda(), span=span, sinks=sinks)
+    assert cache.status() == 0, cache.last_error()
+    seen = U.visible(n_q, n_kv, span, sinks)
+    got, G = f64(out), Hq // Hkv
+    where = np.zeros(got.shape, bool)
+    for i, j in enumerate(bad):
+        rows = np.zeros(got.shape, bool)
+        for h in range(i % Hkv * G, (i % Hkv + 1) * G):
+            rows[B - 1, seen[:, j], h, 7 * i + 3] = True
+        if i % 3 == 0:
+            assert np.all(np.isnan(got[rows]))
+        else:
+            assert np.all(np.isinf(got[rows]) & ((got[rows] > 0) == (i % 3 == 1)))
+        where |= rows
+    assert np.array_equal(~np.isfinite(got), where)
+    ref, _ = U.attention(f64(q), f64(k), f64(clean), [n_q] * B, [n_kv] * B, span, sinks)
+    mag, rl = U.attention(f64(q), f64(k), np.abs(f64(clean)), [n_q] * B, [n_kv] * B, span, sinks)
+    err = np.abs(got - ref)[~where]
+    assert np.all(err <= 2.0 ** -8 * (np.abs(ref) + mag)[~where] + 1e-5)
+    assert np.all(np.abs(f64(lse) - rl) <= 1e-5 + 1e-6 * np.abs(rl))
+
+
+def test_span_attention_all_values_nan():
+    """Every value NaN, several units per SM: every row that sees a key is NaN, nothing else happens."""
+    B, Hq, Hkv, n = 2, 16, 16, 1300
+    q, k = rand(1, B, n, Hq, D), rand(2, B, n, Hkv, D)
+    v = torch.full((B, n, Hkv, D), float("nan"), dtype=torch.bfloat16)
+    cache = cache_for(B, Hq, Hkv)
+    out, _ = cache.span_attention(0, q.cuda(), k.cuda(), v.cuda(), span=200, sinks=9)
+    assert torch.all(torch.isnan(out)) and cache.status() == 0
+
+
 def test_span_attention_large_logits_and_late_maxima():
     """Logits that grow along the keys by thousands: every tile moves the maximum."""
     B, Hq, Hkv, n = 1, 4, 2, 700

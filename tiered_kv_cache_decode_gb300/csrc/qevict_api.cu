@@ -758,8 +758,8 @@ qevict_status qevict_span_attention(qevict_cache *c, int32_t layer, const void *
     if (e == cudaSuccess) e = encode_tokens(&km, k, a.B, n_kv, a.Hkv, 1, 128);
     if (e == cudaSuccess) e = encode_tokens(&vm, v, a.B, n_kv, a.Hkv, 1, 128);
     if (e == cudaSuccess)
-        e = launch_span_attention(a, c->cdev, layer, qm, km, vm, (__nv_bfloat16 *)out, lse, c->num_sms,
-                                  (cudaStream_t)stream);
+        e = launch_span_attention(a, c->cdev, layer, qm, km, vm, (const __nv_bfloat16 *)v, (__nv_bfloat16 *)out, lse,
+                                  c->num_sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "span attention kernel");
     note_op(c, -1, stream);
     return QEVICT_OK;

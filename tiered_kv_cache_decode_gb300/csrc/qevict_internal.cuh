@@ -260,8 +260,8 @@ cudaError_t launch_rope(const LayerDev &L, const RopeArgs &a, cudaStream_t s);
 // channels x 1 head x 128 tokens; 128-byte swizzle. out bf16, lse fp32 or NULL.
 __host__ __device__ inline int span_tile_tokens(int G) { return 128 / G; }
 cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
-                                  const CUtensorMap &kmap, const CUtensorMap &vmap, __nv_bfloat16 *out, float *lse,
-                                  int num_sms, cudaStream_t s);
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap, const __nv_bfloat16 *values,
+                                  __nv_bfloat16 *out, float *lse, int num_sms, cudaStream_t s);
 // scores fp32 [B][n_win], or [B * Hkv][n_win] with per_head; part: kSpanPartFloats of the layer's own
 cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
                                const CUtensorMap &kmap, const float *lse, float *scores, float *part, int w,

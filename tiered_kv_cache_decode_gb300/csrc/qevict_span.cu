@@ -63,6 +63,35 @@ constexpr int kAttSlots = 7;                  // 32 KB slots of shared memory: q
 constexpr int kAttSmem = kAttSlots * kTileBytes + 1024;
 constexpr float kRescale = 8.f;               // log2 growth of a row's maximum that moves its reference
 
+// A value row in shared memory, its halves of 64 channels kHalf bytes apart: whether no
+// element is infinite or NaN (row r starts at its own 16 bytes, so that a warp's
+// rows fall into all banks), and those elements, or all, set to 0.
+__device__ __forceinline__ bool all_finite(const uint8_t *v, int r) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(v + (y >> 3) * kHalf + 16 * ((y + r) & 7));
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                     __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+    }
+    return (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
+}
+__device__ __forceinline__ void clear_not_finite(uint8_t *v) {
+#pragma unroll 1
+    for (int y = 0; y < 64; ++y) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(v + (y >> 5) * kHalf) + (y & 31);
+        uint32_t u = *w;
+        if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+        if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
+        *w = u;
+    }
+}
+__device__ __forceinline__ void clear_row(uint8_t *v, int r) {
+#pragma unroll
+    for (int y = 0; y < 16; ++y)
+        *reinterpret_cast<int4 *>(v + (y >> 3) * kHalf + 16 * ((y + r) & 7)) = make_int4(0, 0, 0, 0);
+}
+
 // One or two neighbouring query tiles of one (sequence, KV head), and the key tiles
 // [first, first + n) of theirs that this CTA takes.
 struct __align__(16) AttUnit {
@@ -88,11 +117,38 @@ __device__ __forceinline__ AttUnit att_unit(const SpanArgs &a, int u, int q_tile
     return U;
 }
 
+// Adds to four outputs of position `pos`, from channel `ch`, the infinite and NaN values of the
+// keys that it sees in the unit's masked tiles.
+__device__ __forceinline__ void add_cleared(const SpanArgs &a, const AttUnit &U, const __nv_bfloat16 *values, int pos,
+                                            int ch, __nv_bfloat16 *o) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    bool any = false;
+#pragma unroll 1
+    for (int it = 0; it < U.tl.count(); ++it) {
+        const int k0 = U.tl.key(it);
+        if (!masked_tile(a, k0, U.p_lo, U.p_hi)) continue;
+#pragma unroll 1
+        for (int j = k0; j <= min(k0 + kTile - 1, pos); ++j) {
+            if (j <= pos - a.span && j >= a.sinks) continue;
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(
+                values + (((int64_t)U.b * a.n_kv + j) * a.Hkv + U.kvh) * kHeadDim + ch));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = __uint_as_float(e & 1 ? (e < 2 ? u.x : u.y) & 0xffff0000u : (e < 2 ? u.x : u.y) << 16);
+                if (!isfinite(y)) x[e] += y, any = true;
+            }
+        }
+    }
+    if (any)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __float2bfloat16_rn(__bfloat162float(o[e]) + x[e]);
+}
+
 template <bool SPLIT>
 __global__ void __launch_bounds__(kAttThreads, 1)
     span_attention_kernel(const SpanArgs a, const CacheDev C, int layer, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                          __nv_bfloat16 *out, float *lse, int q_tiles, int cl) {
+                          const __nv_bfloat16 *values, __nv_bfloat16 *out, float *lse, int q_tiles, int cl) {
     constexpr int QT = SPLIT ? 1 : 2;              // query tiles of the CTA
     constexpr int NS = kAttSlots - QT;             // ring slots
     extern __shared__ uint8_t raw[];
@@ -101,6 +157,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     __shared__ AttUnit given[2];                   // wide: units that the copy thread has worked out
     __shared__ uint32_t slot;
     __shared__ int stop;
+    __shared__ int poison[8];                      // by unit: a value was infinite or NaN in a masked tile
 
     const int T = span_tile_tokens(a.G), rows = T * a.G;
     const int rank = SPLIT ? blockIdx.x % cl : 0;
@@ -149,6 +206,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         for (int i = 0; i < 2 * NS + 15; ++i)
             tc_mbar_init(bar0 + 8 * i, i == 2 * NS + 12 || i == 2 * NS + 13 ? 9 : i >= 2 * NS + 5 && i < 2 * NS + 9 ? 4 : 1);
         stop = 0;
+        for (int i = 0; i < 8; ++i) poison[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (SPLIT && U.n > 0) {   // a short unit's latency counts: its first copies do not wait for the set-up
@@ -330,6 +388,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         bool ok = true;
         int tiles = 0, item0 = 0, outs = 0;   // logit tiles, ring items and outputs before this unit
         for (int c_ = 0; ok && next(c_, ok); ++c_) {
+            // the groups are less than two units apart, so a slot four ahead is out of use
+            if (tid == 0) poison[(c_ + 4) & 7] = 0;
             const int b = U.b, kvh = U.kvh, i0 = U.i0, p_lo = U.p_lo, p_hi = U.p_hi, n = U.n;
             auto v_item = [&](int j) { return item0 + (SPLIT ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1); };
             const int pos = p_lo + tok;
@@ -393,21 +453,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                     }
                 }
-                // Values of keys that no row of the CTA sees may be anything: as zeros they stay out of the product.
-                if ((SPLIT || t == 0) && (k0 + kTile - 1 > p_hi || (k0 <= p_lo - a.span && k0 + kTile > a.sinks))) {
+                // A probability of 0 does not keep an infinity or a NaN out of its product, so in a tile
+                // that some row does not see in full they are set to 0 (as are keys that no row of the
+                // CTA sees, which may be anything); rows that do see them get them back at the end.
+                if (masked) {
                     const int i = v_item(j), s = i % NS;
                     ok = __all_sync(~0u, tc_wait(full(s), (i / NS) & 1, &stop));
                     if (!ok) break;
                     const int key = k0 + r;
-                    if (key > p_hi || (key <= p_lo - a.span && key >= a.sinks)) {
-                        uint8_t *v = gen + (QT + s) * kTileBytes + r * 128;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            *reinterpret_cast<int4 *>(v + 16 * y) = make_int4(0, 0, 0, 0);
-                            *reinterpret_cast<int4 *>(v + kHalf + 16 * y) = make_int4(0, 0, 0, 0);
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    const bool dead = key > p_hi || (key <= p_lo - a.span && key >= a.sinks);
+                    uint8_t *v = gen + (QT + s) * kTileBytes + r * 128;
+                    const bool bad = !dead && !all_finite(v, r);
+                    if (dead) clear_row(v, r);
+                    if (bad) {
+                        poison[c_ & 7] = 1;
+                        clear_not_finite(v);
                     }
+                    if (dead || bad) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
                 }
                 const float mc = m == -INFINITY ? 0.f : -m * c;
                 const uint64_t mm = pair2(mc, mc);
@@ -468,6 +531,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                     __syncwarp();
                 }
+                if (poison[c_ & 7] && valid && ok) {
+#pragma unroll 1
+                    for (int ch = 0; ch < kHeadDim; ch += 4)
+                        add_cleared(a, U, values, pos, ch, reinterpret_cast<__nv_bfloat16 *>(dst) + ch);
+                }
                 if (valid && ok && lse)
                     lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + tok] =
                         none ? -INFINITY : m * rsqrtf((float)kHeadDim) + logf(l);
@@ -495,6 +563,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 else __syncthreads();
                 {
                     const uint32_t st = ring + 4 * kTileBytes;
+                    int bad = 0;
+                    for (int x = 0; x < cl; ++x) bad |= cl_ldi(cl_addr(smem_u32(&poison[0]), x));
                     for (int i = rank * kSoftmax + tid; i < U.n_tok * a.G * 32; i += cl * kSoftmax) {
                         const int r = i >> 5, ch = i & 31;
                         float top = -INFINITY;
@@ -516,8 +586,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         const float inv = l == 0.f ? 0.f : 1.f / l;
                         const int64_t head = kvh * a.G + r % a.G;
                         __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
-                        *reinterpret_cast<uint2 *>(out + (((int64_t)b * a.n_q + i0 + r / a.G) * a.Hq + head) * kHeadDim + 4 * ch) =
-                            *reinterpret_cast<const uint2 *>(p);
+                        __nv_bfloat16 *dst = out + (((int64_t)b * a.n_q + i0 + r / a.G) * a.Hq + head) * kHeadDim + 4 * ch;
+                        *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(p);
+                        if (bad) add_cleared(a, U, values, p_lo + r / a.G, 4 * ch, dst);
                         if (ch == 0 && lse)
                             lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + r / a.G] =
                                 l == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * (1.f / kLog2e) + logf(l);
@@ -965,8 +1036,8 @@ int best_cluster(int64_t tiles, int64_t seen, int num_sms, const int *active, do
 }  // namespace
 
 cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int layer, const CUtensorMap &qmap,
-                                  const CUtensorMap &kmap, const CUtensorMap &vmap, __nv_bfloat16 *out, float *lse,
-                                  int num_sms, cudaStream_t s) {
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap, const __nv_bfloat16 *values,
+                                  __nv_bfloat16 *out, float *lse, int num_sms, cudaStream_t s) {
     static int active[kOnceDevices][kMaxCluster + 1];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1010,9 +1081,9 @@ cudaError_t launch_span_attention(const SpanArgs &a, const CacheDev &C, int laye
         cfg.attrs = &at;
         cfg.numAttrs = 1;
     }
-    return cl ? cudaLaunchKernelEx(&cfg, span_attention_kernel<true>, a, C, layer, qmap, kmap, vmap, out, lse,
+    return cl ? cudaLaunchKernelEx(&cfg, span_attention_kernel<true>, a, C, layer, qmap, kmap, vmap, values, out, lse,
                                    (int)q_tiles, cl)
-              : cudaLaunchKernelEx(&cfg, span_attention_kernel<false>, a, C, layer, qmap, kmap, vmap, out, lse,
+              : cudaLaunchKernelEx(&cfg, span_attention_kernel<false>, a, C, layer, qmap, kmap, vmap, values, out, lse,
                                    (int)q_tiles, 1);
 }
 
