@@ -397,7 +397,8 @@ qevict_status qevict_qk_norm_rope(qevict_cache *cache, int32_t layer, const void
  * q_len[b] are not written. What a key or value that a query does not see holds
  * (later keys, keys before its span, rows at or past kv_len; NaN and infinities
  * too) never reaches that query's row.
- * n_q and n_kv are in [1, 2^29]. */
+ * out and lse must not overlap each other or an input (INVALID_ARG). n_q and
+ * n_kv are in [1, 2^29]. */
 qevict_status qevict_span_attention(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
                                     const void *v, int32_t n_kv, const int32_t *q_len, const int32_t *kv_len,
                                     int32_t span, int32_t sinks, void *out, float *lse, void *stream);
@@ -413,7 +414,8 @@ qevict_status qevict_span_attention(qevict_cache *cache, int32_t layer, const vo
  *  scores  fp32 [batch][ceil(n_kv / window)], device, written (0 for windows
  *          past kv_len); with per-head tiers [batch * Hkv][ceil(n_kv / window)],
  *          the mean over the G query heads of each KV head.
- * Sums are fp32 in a fixed order: every call gives the same scores. */
+ * Sums are fp32 in a fixed order: every call gives the same scores. scores must
+ * not overlap an input (INVALID_ARG). */
 qevict_status qevict_span_scores(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
                                  int32_t n_kv, const int32_t *q_len, const int32_t *kv_len, int32_t span,
                                  int32_t sinks, const float *lse, float *scores, void *stream);

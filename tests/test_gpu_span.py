@@ -278,9 +278,9 @@ def test_span_attention_non_finite_query_stays_in_its_row():
     assert torch.equal(a[0][keep.cuda()], b[0][keep.cuda()])
 
 
-def test_span_attention_streams_and_graph():
+@pytest.mark.parametrize("B,Hq,Hkv,n", [(1, 8, 2, 900), (3, 16, 8, 1500)])   # split, and several units per SM
+def test_span_attention_streams_and_graph(B, Hq, Hkv, n):
     """Two calls at once on two streams, and a captured call on new inputs, give the same bits."""
-    B, Hq, Hkv, n = 1, 8, 2, 900
     sets = [[rand(10 * s + i, B, n, h, D).cuda() for i, h in enumerate((Hq, Hkv, Hkv))] for s in range(2)]
     cache = cache_for(B, Hq, Hkv)
     ref = [cache.span_attention(0, *s) for s in sets]
@@ -347,6 +347,118 @@ def test_span_scores_padded_batch():
     ref = U.scores(f64(torch.nan_to_num(q)), f64(torch.nan_to_num(k)), f64(lse), q_len, kv_len, span, sinks, w)
     assert np.all(np.abs(f64(got) - ref) <= 1e-5 * ref + 1e-9)
     assert cache.status() == 0
+
+
+def test_span_scores_streams_layers_and_graph():
+    """Calls on two layers at once, in parts that a second kernel sums, and a captured one."""
+    B, Hq, Hkv, n, w = 1, 16, 4, 1300, 32
+    cache = binding.TieredCache(B, 2, Hq, Hkv, w, n, fp_capacity=1, ledger_capacity=1)
+    sets = [[rand(10 * s + i, B, n, h, D).cuda() for i, h in enumerate((Hq, Hkv))] for s in range(2)]
+    lse = [cache.span_attention(0, q, k, k)[1] for q, k in sets]
+    ref = [cache.span_scores(0, q, k, x) for (q, k), x in zip(sets, lse)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(10):
+        got = [cache.span_scores(i, *sets[i], lse[i], stream=st) for i, st in enumerate(streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    bufs, x, out = [t.clone() for t in sets[0]], lse[0].clone(), torch.empty_like(ref[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        g.capture_begin()
+        cache.span_scores(0, *bufs, x, out=out)
+        g.capture_end()
+    for s, l, r in zip(sets, lse, ref):
+        for t, y in zip(bufs + [x], s + [l]):
+            t.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, r)
+
+
+def test_offsets_past_32_bits():
+    """Keys, queries and outputs whose element offsets pass 2^31; only what is looked at is filled."""
+    Hq, Hkv, n, span, sinks = 8, 8, 2 ** 21 + 300, 700, 3
+    cache = cache_for(1, Hq, Hkv, w=128)
+    k, v = (torch.empty(1, n, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tail = n - 1100
+    for t, s in ((k, 2), (v, 3)):
+        t[:, :sinks] = rand(s, 1, sinks, Hkv, D).cuda()
+        t[:, tail:] = rand(s + 2, 1, n - tail, Hkv, D).cuda()
+    q = rand(1, 1, 5, Hq, D)
+    out, lse = cache.span_attention(0, q.cuda(), k, v, span=span, sinks=sinks)
+    keep = torch.cat([torch.arange(sinks), torch.arange(tail, n)]).cuda()
+    j, p = keep.cpu().numpy()[None], n - 5 + np.arange(5)[:, None]
+    seen = (j <= p) & ((j > p - span) | (j < sinks))
+    kk, vv = f64(k[:, keep]), f64(v[:, keep])
+    for h in range(Hq):
+        o, s = U.attention_head(f64(q)[0, :, h], kk[0, :, h], vv[0, :, h], seen)
+        mag, _ = U.attention_head(f64(q)[0, :, h], kk[0, :, h], np.abs(vv[0, :, h]), seen)
+        assert np.all(np.abs(f64(out)[0, :, h] - o) <= 2.0 ** -8 * (np.abs(o) + mag) + 1e-5)
+        assert np.all(np.abs(f64(lse)[0, h] - s) <= 1e-5 + 1e-6 * np.abs(s))
+    sc = cache.span_scores(0, q.cuda(), k, lse, span=span, sinks=sinks)
+    assert abs(float(sc.sum()) - 5) < 1e-4 and int((sc > 0).sum()) <= 8
+    # the last 704 keys begin in window (n - 704) // 128 = W - 7
+    assert float(sc[0, -7:].sum()) + float(sc[0, 0]) == pytest.approx(5, abs=1e-4)
+    # the same tensor as queries: n rows of n keys with a narrow span, written past 2^31 elements
+    out, lse = cache.span_attention(0, k, k, v, span=16)
+    a, b = f64(k[:, -400:]), f64(v[:, -400:])
+    ref, _ = U.attention(a, a, b, [400], [400], 16, 0)
+    mag, _ = U.attention(a, a, np.abs(b), [400], [400], 16, 0)
+    got = f64(out[:, -384:])
+    assert np.all(np.abs(got - ref[:, -384:]) <= 2.0 ** -8 * (np.abs(ref) + mag)[:, -384:] + 1e-5)
+    # and through norm and rotation
+    pos = torch.arange(n, device="cuda")[None]
+    gq, gk = cache.qk_norm_rope(0, k, v, freqs().cuda(), positions=pos)
+    for t, g in ((k, gq), (v, gk)):
+        r = U.norm_rope(f64(t[:, -4:]), None, 0, pos[:, -4:].cpu().numpy(), freqs().double().numpy())
+        assert np.all(np.abs(f64(g[:, -4:]) - r) <= 2.0 ** -8 * np.abs(r) + 2e-5)
+    assert cache.status() == 0
+
+
+def test_refusals():
+    """What the library refuses before it enqueues anything."""
+    B, Hq, Hkv, n = 2, 8, 2, 40
+    cache = cache_for(B, Hq, Hkv)
+    q, k = rand(1, B, n, Hq, D).cuda(), rand(2, B, n, Hkv, D).cuda()
+    v, inv = k.clone(), freqs().cuda()
+    out, lse = cache.span_attention(0, q, k, v)
+    kept = out.clone()
+    big = torch.zeros(q.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    shifted = big[4:4 + q.numel()].view(q.shape)      # 8-byte aligned
+    ahead = big[8:8 + q.numel()].view(q.shape)
+    behind = big[:q.numel()].view(q.shape)
+    for call, word in (
+            (lambda: cache.span_attention(5, q, k, v), "layer"),
+            (lambda: cache.span_attention(0, q, k, v, span=-1), "span"),
+            (lambda: cache.span_attention(0, q, k, v, sinks=-1), "sinks"),
+            (lambda: cache.span_attention(0, shifted, k, v), "aligned"),
+            (lambda: cache.span_attention(0, q, k, v, out=q), "overlaps"),
+            (lambda: cache.span_attention(0, ahead, k, v, out=behind), "overlaps"),
+            (lambda: cache.span_scores(0, q, k, lse, span=-3), "span"),
+            (lambda: cache.span_scores(0, q, k, lse, out=lse.view(-1)[:B].view(B, 1)), "overlaps"),
+            (lambda: cache.qk_norm_rope(0, q, k, inv, eps=-1.0), "eps"),
+            (lambda: cache.qk_norm_rope(0, q, k, inv, eps=float("nan")), "eps"),
+            (lambda: cache.qk_norm_rope(0, ahead, k, inv, q_out=behind), "overlap"),
+            (lambda: cache.qk_norm_rope(0, q, k, inv, k_out=q.view(-1)[:k.numel()].view(k.shape)), "overlap"),
+            (lambda: cache.qk_norm_rope(0, q, k, inv, v=v, k_out=v), "overlap"),
+            (lambda: cache.qk_norm_rope(0, shifted, k, inv), "aligned"),
+            (lambda: cache.qk_norm_rope(7, q, k, inv), "layer")):
+        with pytest.raises(binding.QevictError) as e:
+            call()
+        assert e.value.name == "INVALID_ARG" and word in str(e.value), str(e.value)
+    for call in (lambda: cache.span_attention(0, q, k, v[:, :3]), lambda: cache.span_attention(0, q[:, ::2], k, v),
+                 lambda: cache.span_attention(0, q[:, :0], k, v, out=out[:, :0], lse=lse[:, :, :0]),
+                 lambda: cache.span_attention(0, q, k, v, q_len=torch.zeros(B, device="cuda")),
+                 lambda: cache.span_scores(0, q, k, lse[:, :, :3]),
+                 lambda: cache.qk_norm_rope(0, q, k, inv, positions=torch.zeros(B, n, device="cuda")),
+                 lambda: cache.qk_norm_rope(0, q, k, inv[:3]), lambda: cache.qk_norm_rope(0, q, k[:, :3], inv),
+                 lambda: cache.qk_norm_rope(0, q, k, inv, v_out=v)):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.equal(out, kept) and cache.status() == 0
 
 
 # ---- the run of them -----------------------------------------------------------------

@@ -435,6 +435,16 @@ class TieredCache:
                              f"{list(t.shape)} on {t.device}")
         return t.data_ptr()
 
+    @staticmethod
+    def _new(like, stream, dtype=None, shape=None):
+        """A dense tensor like `like`, from the memory of the stream that writes it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return TieredCache._new(like, None, dtype, shape)
+        if shape is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
     def _raw_stream(self, stream):
         return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device)
 
@@ -449,20 +459,19 @@ class TieredCache:
         nv, vs = (n, 0) if v is None else self._tokens(v, self.Hkv, "v")
         if nk != n or nv != n:
             raise ValueError(f"q, k and v must have the same tokens, got {n}, {nk} and {nv}")
-        like, dense = torch.empty_like, torch.contiguous_format
         if q_out is None:
-            q_out = like(q, memory_format=dense)
+            q_out = self._new(q, stream)
         else:
             side(q_out, q.shape, bf, "q_out")
         if k_out is None:
-            k_out = like(k, memory_format=dense)
+            k_out = self._new(k, stream)
         else:
             side(k_out, k.shape, bf, "k_out")
         if v is None:
             if v_out is not None:
                 raise ValueError("v_out without v")
         elif v_out is None:
-            v_out = like(v, memory_format=dense)
+            v_out = self._new(v, stream)
         else:
             side(v_out, v.shape, bf, "v_out")
         rc = self.lib.qevict_qk_norm_rope(
@@ -484,9 +493,9 @@ class TieredCache:
         if self._dense(v, self.Hkv, "v") != n_kv:
             raise ValueError(f"v must have k's {n_kv} tokens")
         if out is None:
-            out = torch.empty_like(q)
+            out = self._new(q, stream)
         if lse is None and want_lse:
-            lse = torch.empty(self.B, self.Hq, n_q, dtype=torch.float32, device=self._dev)
+            lse = self._new(q, stream, torch.float32, (self.B, self.Hq, n_q))
         side, per_seq = self._side, (self.B,)
         rc = self.lib.qevict_span_attention(
             self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), v.data_ptr(), n_kv,
@@ -503,7 +512,7 @@ class TieredCache:
         n_q, n_kv = self._dense(q, self.Hq, "q"), self._dense(k, self.Hkv, "k")
         W = -(-n_kv // self.w)
         if out is None:
-            out = torch.empty(self.units, W, dtype=torch.float32, device=self._dev)
+            out = self._new(q, stream, torch.float32, (self.units, W))
         side, per_seq = self._side, (self.B,)
         rc = self.lib.qevict_span_scores(
             self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), n_kv, side(q_len, per_seq, torch.int32, "q_len"),

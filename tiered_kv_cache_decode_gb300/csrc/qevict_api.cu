@@ -661,12 +661,31 @@ static cudaError_t encode_tokens(CUtensorMap *map, const void *base, int seqs, i
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+struct Extent {
+    const void *p;
+    int64_t bytes;
+    const char *what;
+};
+// An output must not overlap another operand: the kernels read and write in no fixed order.
+static qevict_status check_apart(const Extent &o, const Extent *others, int n) {
+    const uintptr_t o0 = (uintptr_t)o.p, o1 = o0 + o.bytes;
+    for (int i = 0; i < n && o.p; ++i) {
+        const uintptr_t s0 = (uintptr_t)others[i].p, s1 = s0 + others[i].bytes;
+        if (others[i].p && o0 < s1 && s0 < o1)
+            return fail(QEVICT_ERR_INVALID_ARG, "%s overlaps %s", o.what, others[i].what);
+    }
+    return QEVICT_OK;
+}
+
 static qevict_status check_span(const qevict_cache *c, const void *q, int32_t n_q, const void *k, int32_t n_kv,
-                                int32_t span, int32_t sinks) {
+                                const int32_t *q_len, const int32_t *kv_len, int32_t span, int32_t sinks,
+                                const float *lse) {
     if (n_q < 1 || n_kv < 1 || n_q > kMaxSpanTokens || n_kv > kMaxSpanTokens)
         return fail(QEVICT_ERR_INVALID_ARG, "n_q (%d) and n_kv (%d) must be in [1, %d]", n_q, n_kv, kMaxSpanTokens);
     if (span < 0 || sinks < 0) return fail(QEVICT_ERR_INVALID_ARG, "span (%d) and sinks (%d) must be >= 0", span, sinks);
-    if (((uintptr_t)q | (uintptr_t)k) & 15) return fail(QEVICT_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+    if (((uintptr_t)q | (uintptr_t)k) & 15) return fail(QEVICT_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned");
+    if (((uintptr_t)q_len | (uintptr_t)kv_len | (uintptr_t)lse) & 3)
+        return fail(QEVICT_ERR_INVALID_ARG, "q_len, kv_len, lse and scores must be 4-byte aligned");
     return check_device(c);
 }
 
@@ -749,10 +768,17 @@ qevict_status qevict_span_attention(qevict_cache *c, int32_t layer, const void *
     qevict_status st = check_layer(c, layer);
     if (st) return st;
     if (!q || !k || !v || !out) return fail(QEVICT_ERR_INVALID_ARG, "q, k, v and out must not be NULL");
-    st = check_span(c, q, n_q, k, n_kv, span, sinks);
+    st = check_span(c, q, n_q, k, n_kv, q_len, kv_len, span, sinks, lse);
     if (st) return st;
-    if (((uintptr_t)v | (uintptr_t)out) & 15) return fail(QEVICT_ERR_INVALID_ARG, "v and out must be 16-byte aligned");
+    if (((uintptr_t)v | (uintptr_t)out) & 15)
+        return fail(QEVICT_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned");
     const SpanArgs a = span_args(c, n_q, n_kv, q_len, kv_len, span, sinks);
+    const int64_t rows = (int64_t)a.B * n_q * a.Hq, keys = (int64_t)a.B * n_kv * a.Hkv;
+    const Extent x[6] = {{q, rows * kHeadDim * 2, "q"},   {k, keys * kHeadDim * 2, "k"}, {v, keys * kHeadDim * 2, "v"},
+                         {q_len, (int64_t)a.B * 4, "q_len"}, {kv_len, (int64_t)a.B * 4, "kv_len"}, {lse, rows * 4, "lse"}};
+    st = check_apart({out, rows * kHeadDim * 2, "out"}, x, 6);
+    if (!st) st = check_apart(x[5], x, 5);
+    if (st) return st;
     CUtensorMap qm, km, vm;
     cudaError_t e = encode_tokens(&qm, q, a.B, n_q, a.Hq, a.G, span_tile_tokens(a.G));
     if (e == cudaSuccess) e = encode_tokens(&km, k, a.B, n_kv, a.Hkv, 1, 128);
@@ -771,9 +797,15 @@ qevict_status qevict_span_scores(qevict_cache *c, int32_t layer, const void *q, 
     qevict_status st = check_layer(c, layer);
     if (st) return st;
     if (!q || !k || !lse || !scores) return fail(QEVICT_ERR_INVALID_ARG, "q, k, lse and scores must not be NULL");
-    st = check_span(c, q, n_q, k, n_kv, span, sinks);
+    st = check_span(c, q, n_q, k, n_kv, q_len, kv_len, span, sinks, lse);
     if (st) return st;
+    if ((uintptr_t)scores & 3) return fail(QEVICT_ERR_INVALID_ARG, "q_len, kv_len, lse and scores must be 4-byte aligned");
     const SpanArgs a = span_args(c, n_q, n_kv, q_len, kv_len, span, sinks);
+    const int64_t rows = (int64_t)a.B * n_q * a.Hq;
+    const Extent x[5] = {{q, rows * kHeadDim * 2, "q"}, {k, (int64_t)a.B * n_kv * a.Hkv * kHeadDim * 2, "k"},
+                         {q_len, (int64_t)a.B * 4, "q_len"}, {kv_len, (int64_t)a.B * 4, "kv_len"}, {lse, rows * 4, "lse"}};
+    st = check_apart({scores, (int64_t)c->cfg.batch * n_windows(c, n_kv) * 4, "scores"}, x, 5);
+    if (st) return st;
     CUtensorMap qm, km;
     cudaError_t e = encode_tokens(&qm, q, a.B, n_q, a.Hq, a.G, span_tile_tokens(a.G));
     if (e == cudaSuccess) e = encode_tokens(&km, k, a.B, n_kv, a.Hkv, 1, 128);
