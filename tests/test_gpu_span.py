@@ -315,7 +315,8 @@ def test_span_attention_streams_and_graph(B, Hq, Hkv, n):
 @pytest.mark.parametrize("w", [16, 48, 64, 128])
 @pytest.mark.parametrize("B,Hq,Hkv,n_q,n_kv,span,sinks", [
     (1, 1, 1, 1, 1, 0, 0), (2, 8, 2, 64, 1000, 0, 0), (1, 28, 4, 333, 333, 0, 0), (2, 6, 3, 200, 700, 90, 5),
-    (1, 10, 2, 300, 300, 1, 0), (1, 16, 16, 17, 517, 0, 0), (1, 8, 1, 130, 2000, 300, 200)])
+    (1, 10, 2, 300, 300, 1, 0), (1, 16, 16, 17, 517, 0, 0), (1, 8, 1, 130, 2000, 300, 200),
+    (3, 14, 2, 20, 1700, 90, 5), (2, 8, 2, 1, 900, 0, 0), (1, 4, 1, 40, 3000, 50, 200), (2, 12, 4, 84, 84, 0, 0)])
 @pytest.mark.parametrize("per_head", [False, True])
 def test_span_scores_match_plain(B, Hq, Hkv, n_q, n_kv, span, sinks, w, per_head):
     cache = cache_for(B, Hq, Hkv, w=w, per_head=per_head)
@@ -331,9 +332,10 @@ def test_span_scores_match_plain(B, Hq, Hkv, n_q, n_kv, span, sinks, w, per_head
     assert torch.equal(got, again)
 
 
-def test_span_scores_padded_batch():
-    B, Hq, Hkv, n_q, n_kv, w, span, sinks = 6, 14, 2, 100, 400, 32, 90, 3
-    q_len, kv_len = [100, 0, 1, 77, 100, 5], [400, 50, 1, 399, 60, 0]
+@pytest.mark.parametrize("n_q", [100, 30])   # 30: two query tiles, the form for few queries
+def test_span_scores_padded_batch(n_q):
+    B, Hq, Hkv, n_kv, w, span, sinks = 6, 14, 2, 400, 32, 90, 3
+    q_len, kv_len = [n_q, 0, 1, n_q - 23, n_q, 5], [400, 50, 1, 399, 20, 0]
     q, k = rand(1, B, n_q, Hq, D), rand(2, B, n_kv, Hkv, D)
     for b in range(B):
         q[b, q_len[b]:] = float("nan")
@@ -349,11 +351,12 @@ def test_span_scores_padded_batch():
     assert cache.status() == 0
 
 
-def test_span_scores_streams_layers_and_graph():
+@pytest.mark.parametrize("n_q", [1300, 64])
+def test_span_scores_streams_layers_and_graph(n_q):
     """Calls on two layers at once, in parts that a second kernel sums, and a captured one."""
     B, Hq, Hkv, n, w = 1, 16, 4, 1300, 32
     cache = binding.TieredCache(B, 2, Hq, Hkv, w, n, fp_capacity=1, ledger_capacity=1)
-    sets = [[rand(10 * s + i, B, n, h, D).cuda() for i, h in enumerate((Hq, Hkv))] for s in range(2)]
+    sets = [[rand(10 * s + i, B, m, h, D).cuda() for i, (m, h) in enumerate(((n_q, Hq), (n, Hkv)))] for s in range(2)]
     lse = [cache.span_attention(0, q, k, k)[1] for q, k in sets]
     ref = [cache.span_scores(0, q, k, x) for (q, k), x in zip(sets, lse)]
     torch.cuda.synchronize()

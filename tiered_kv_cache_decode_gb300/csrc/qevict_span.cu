@@ -608,9 +608,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
 // ---- window scores --------------------------------------------------------------
 //
-// The logits are computed transposed, S^T = K Q^T: keys are the 128 lanes of
-// tensor memory and the rows of a query tile its 128 columns, so that a key's
-// mass is a sum along its own lane, in one register, over all query tiles.
+// A thread owns a row (a query of one head) of a logit tile and so has its
+// log-sum-exp in a register; it sums the row's masses over 16 keys at a time (a
+// window is a multiple of 16) into eight registers that it keeps over all query
+// tiles, and the rows meet once an item, by shuffles. Shared memory then feeds the
+// products alone: they read it at its full rate, and with the keys as the rows,
+// which needs a log-sum-exp for every column from there, a step took 1.4 times as long.
 // An item is a run of 256 keys (rounded down to whole windows) of one sequence
 // (of one KV head with per-head units); its steps are the (KV head, query tile)
 // pairs that see some of them. Where the items are few, each is split into parts
@@ -619,10 +622,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // next item run under this one.
 // Four groups of four warps take the masses, each of one key tile in every other
 // step from a logit tile of its own, so that their waits and loads fall at
-// different times; one warp issues the products, one the copies, and one fetches
-// the rows' log-sum-exps.
+// different times; one warp issues the products, one the copies.
 constexpr int kScMass = 512;                  // threads of the four groups
-constexpr int kScThreads = kScMass + 96;
+constexpr int kScThreads = kScMass + 64;
 constexpr int kScK = 2;                       // sets of two key tiles
 constexpr int kScQ = 7 - 2 * kScK;            // query tile slots
 struct ScoreItem {
@@ -679,11 +681,10 @@ __device__ __forceinline__ ScoreSteps score_steps(const ScoreItem &it, int part,
 
 // what lies behind the tiles in shared memory
 struct ScoreTail {
-    float ls[2][kTile];         // of a step's rows: -lse in log2 units
-    float segs[2][2][8];        // masses of 16 keys from each step parity
+    float segs[2][2][4][8];     // masses of 16 keys by key tile, step parity and warp
     ScoreWork given[2];         // items that the copy thread has worked out
     uint4 ticket;               // the answer to the copy thread's last request
-    uint64_t bars[4 + 2 * kScQ + 12];
+    uint64_t bars[4 + 2 * kScQ + 10];
     uint32_t slot;
     int stop, go[2];
 };
@@ -708,16 +709,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto q_empty = [&](int s) { return bar0 + 32 + 8 * (kScQ + s); };
     auto s_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + x); };
     auto s_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 + x); };
-    auto l_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
-    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 6 + x); };
-    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 10), asked = drained + 8;
+    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
+    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 6 + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 8), asked = drained + 8;
     if (tid == 0) {
-        // s_full: the products and the log-sum-exps; s_empty and l_empty: each of the warps that read;
-        // i_empty: every warp but the copies'
-        for (int i = 0; i < 4 + 2 * kScQ + 12; ++i) {
+        // s_empty: each of the warps that read; i_empty: every warp but the copies'
+        for (int i = 0; i < 4 + 2 * kScQ + 10; ++i) {
             const uint32_t bar = bar0 + 8 * i;
-            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 18 : bar >= s_empty(0) ? 8 : bar >= s_full(0) ? 2 : 1);
+            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 17 : bar >= s_empty(0) ? 8 : 1);
         }
         tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -819,7 +818,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 if (lead) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        tc_mma_tile(tmu + 256 * t + 128 * buf, sm + (2 * set + t) * kTileBytes, sq + qs * kTileBytes, kHalf);
+                        tc_mma_tile(tmu + 256 * t + 128 * buf, sq + qs * kTileBytes, sm + (2 * set + t) * kTileBytes, kHalf);
                     tc_commit(s_full(buf));
                     tc_commit(q_empty(qs));
                     if (head || s.left == 0) tc_commit(k_empty(set));
@@ -836,59 +835,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
             while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
         }
         __syncwarp();
-    } else if (warp == 18) {
-        // each lane has four of a query tile's rows; the loads run kAhead steps ahead of the stores
-        constexpr int kAhead = 4;
-        const int lane = tid & 31;
-        int tok[4];
-        int64_t off[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = lane + 32 * e;
-            tok[e] = r < rows ? r / a.G : INT_MAX / 2;
-            off[e] = (int64_t)(r % a.G) * a.n_q + r / a.G;
-        }
-        int nq = 0;
-        for (int c = 0; next(c); ++c) {
-            const ScoreItem &it = W.it;
-            ScoreSteps &s = W.s;
-            const float *l0 = lse + (int64_t)it.b * a.Hq * a.n_q;
-            const int64_t head = (int64_t)a.G * a.n_q;
-            int64_t left = s.left;
-            float v[kAhead][4];
-            auto fetch = [&](float (&w)[4]) {
-                if (s.left <= 0) return;
-                const float *p = l0 + s.h * head + s.q * T;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = tok[e] < it.q_len - s.q * T ? __ldg(p + off[e]) : INFINITY;
-                s.next();
-            };
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) fetch(v[u]);
-            while (left > 0 && ok) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (left <= 0) break;
-                    const int x = nq & 1;
-                    if (nq >= 2) ok = ok && __all_sync(~0u, tc_wait(l_empty(x), ((nq >> 1) - 1) & 1, &tail.stop));
-                    if (!ok) break;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) tail.ls[x][lane + 32 * e] = -kLog2e * v[u][e];
-                    __syncwarp();
-                    if (lane == 0) tc_arrive(s_full(x));
-                    fetch(v[u]);
-                    --left;
-                    ++nq;
-                }
-            }
-        }
     } else {
         const int t = warp >> 3, x = (warp >> 2) & 1, r = tid & 127;
         const uint32_t tS = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t + 128 * x;
-        const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(tail.ls[x]);
+        const int tok = r / a.G;
+        const int64_t off = (int64_t)(r % a.G) * a.n_q + tok;   // the row's log-sum-exp in a query tile's
         const float c = kLog2e * rsqrtf((float)kHeadDim);
         const uint64_t cc = pair2(c, c);
-        int nq = 0;
+        int nq = 0, turn = 0;   // steps so far, and the group's own
         for (int c_ = 0;; ++c_) {
             // the first warp of a key tile decides for the eight, so that their barriers match
             const bool first_warp = (warp & 7) == 0;
@@ -904,73 +858,90 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 if ((tid & 31) == 0) tc_arrive(i_empty(c_ & 1));
             }
             const ScoreItem it = W.it;
-            const int shift = it.kv_len - it.q_len, k0 = it.k0 + t * tk, j = k0 + r;
-            float sum = 0.f;
-            for (ScoreSteps s = W.s; s.left > 0 && ok; s.next(), ++nq) {
-                if ((nq & 1) != x) continue;
+            const int shift = it.kv_len - it.q_len, k0 = it.k0 + t * tk;
+            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const float *l0 = lse + (int64_t)it.b * a.Hq * a.n_q + off;
+            auto fetch = [&](const ScoreSteps &s) {   // rows that no query fills, or that see no key, take no part
+                if (s.left <= 0 || r >= rows || s.q * T + tok >= it.q_len) return -INFINITY;
+                const float y = __ldg(l0 + (int64_t)s.h * a.G * a.n_q + s.q * T);
+                return y == -INFINITY ? y : -kLog2e * y;
+            };
+            ScoreSteps s = W.s;
+            if ((nq & 1) != x && s.left > 0) s.next(), ++nq;   // the first step of the group's parity
+            float ahead = fetch(s);
+            while (s.left > 0) {
                 const int i0 = s.q * T, p_lo = shift + i0;
-                ok = __all_sync(~0u, tc_wait(s_full(x), (nq >> 1) & 1, &tail.stop));
-                if (!ok) break;
+                const float ls = ahead;
+                s.next();
+                ++nq;
+                if (s.left > 0) s.next(), ++nq;
+                ahead = fetch(s);   // of the group's next step
+                ok = ok && __all_sync(~0u, tc_wait(s_full(x), turn++ & 1, &tail.stop));
+                if (!ok) continue;
                 tc_fence_after();
-                uint64_t acc[2] = {0, 0};
+                const uint64_t mm = pair2(ls, ls);
                 float v[2][32];
                 tc_ld32(tS, v[0]);
                 tc_ld32(tS + 32, v[1]);
-                auto masses = [&](auto seen) {
+                const bool plain =
+                    i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks);
+                const int hi = i0 + tok < it.q_len ? p_lo + tok - k0 : -1, lo = p_lo + tok - k0 - a.span, sk = a.sinks - k0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if ((q & 1) == 0) {
-                            if (q == 2) {
-                                tc_ld32(tS + 64, v[0]);
-                                tc_ld32(tS + 96, v[1]);
-                            }
-                            tc_wait_ld();
-                            tc_tie(v[0]);
-                            tc_tie(v[1]);
-                            if (q == 2) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if ((tid & 31) == 0) tc_arrive(s_empty(x));
-                            }
+                for (int q = 0; q < 4; ++q) {
+                    if ((q & 1) == 0) {
+                        if (q == 2) {
+                            tc_ld32(tS + 64, v[0]);
+                            tc_ld32(tS + 96, v[1]);
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const ulonglong2 lv = l2[8 * q + e / 4];
-                            float u[4];
-                            split2(fma2(pair2(v[q & 1][e], v[q & 1][e + 1]), cc, lv.x), u[0], u[1]);
-                            split2(fma2(pair2(v[q & 1][e + 2], v[q & 1][e + 3]), cc, lv.y), u[2], u[3]);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) u[z] = tc_ex2(seen(32 * q + e + z) ? u[z] : -INFINITY);
-                            acc[0] = add2(acc[0], pair2(u[0], u[1]));
-                            acc[1] = add2(acc[1], pair2(u[2], u[3]));
+                        tc_wait_ld();
+                        tc_tie(v[0]);
+                        tc_tie(v[1]);
+                        if (q == 2) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if ((tid & 31) == 0) tc_arrive(s_empty(x));
                         }
                     }
-                };
-                if (i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks)) {
-                    masses([](int) { return true; });
-                } else {
-                    // the queries that see key j are a run of positions, so a run of columns
-                    const int first = min(max(0, j - p_lo), T);
-                    const int end = min(min(it.q_len - i0, T), j < a.sinks ? T : j + a.span - p_lo);
-                    const unsigned c0 = first * a.G, n = max(0, end - first) * a.G;
-                    masses([&](int col) { return (unsigned)col - c0 < n; });
-                }
-                __syncwarp();
-                if ((tid & 31) == 0) tc_arrive(l_empty(x));
-                float s0, s1;
-                split2(add2(acc[0], acc[1]), s0, s1);
-                sum += s0 + s1;
-            }
-            // 16 keys at a time (a window is a multiple of 16), then the windows
-            if (r >= tk || j >= it.kv_len) sum = 0.f;
+                    float(&y)[32] = v[q & 1];
+                    if (!plain) {   // the quarter's visible keys as bits
+                        const uint32_t m = below(hi + 1 - 32 * q) & (~below(lo + 1 - 32 * q) | below(sk - 32 * q));
 #pragma unroll
-            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            if ((r & 15) == 0) tail.segs[t][x][r >> 4] = sum;
+                        for (int e = 0; e < 32; ++e) y[e] = (m >> e & 1) ? y[e] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint64_t sum[2] = {0, 0};
+#pragma unroll
+                        for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+                            float u, z;
+                            split2(fma2(pair2(y[e], y[e + 1]), cc, mm), u, z);
+                            sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair2(tc_ex2(u), tc_ex2(z)));
+                        }
+                        float s0, s1;
+                        split2(add2(sum[0], sum[1]), s0, s1);
+                        acc[2 * q + g] += s0 + s1;
+                    }
+                }
+            }
+            // Eight sums over the warp's 32 rows: three exchanges halve the sums that a lane keeps,
+            // two add what is left; lane l has the sum of keys 16 (l / 4) .. + 15.
+#pragma unroll
+            for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1)
+#pragma unroll
+                for (int e = 0; e < n; ++e) {
+                    const bool up = tid & o;
+                    const float give = up ? acc[e] : acc[e + n];
+                    acc[e] = (up ? acc[e + n] : acc[e]) + __shfl_xor_sync(~0u, give, o);
+                }
+            acc[0] += __shfl_xor_sync(~0u, acc[0], 2);
+            acc[0] += __shfl_xor_sync(~0u, acc[0], 1);
+            if ((tid & 3) == 0) tail.segs[t][x][warp & 3][(tid & 31) >> 2] = acc[0];
             asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
             const int win = k0 / w + r;
             float mass = 0.f;
             if (x == 0 && r < tk / w)
-                for (int e = r * (w / 16); e < (r + 1) * (w / 16); ++e) mass += tail.segs[t][0][e] + tail.segs[t][1][e];
+                for (int e = r * (w / 16); e < (r + 1) * (w / 16); ++e)
+                    for (int y = 0; y < 8; ++y) mass += tail.segs[t][y >> 2][y & 3][e];
             if (x == 0 && r < tk / w && win < n_win) {
                 const int units = per_head ? a.B * a.Hkv : a.B, u = per_head ? it.b * a.Hkv + it.h0 : it.b;
                 if (parts == 1) scores[(int64_t)u * n_win + win] = mass / (per_head ? a.G : a.Hq);
