@@ -684,7 +684,7 @@ struct ScoreTail {
     float segs[2][2][4][8];     // masses of 16 keys by key tile, step parity and warp
     ScoreWork given[2];         // items that the copy thread has worked out
     uint4 ticket;               // the answer to the copy thread's last request
-    uint64_t bars[4 + 2 * kScQ + 10];
+    uint64_t bars[4 + 2 * kScQ + 14];
     uint32_t slot;
     int stop, go[2];
 };
@@ -707,16 +707,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto k_empty = [&](int s) { return bar0 + 16 + 8 * s; };
     auto q_full = [&](int s) { return bar0 + 32 + 8 * s; };
     auto q_empty = [&](int s) { return bar0 + 32 + 8 * (kScQ + s); };
-    auto s_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + x); };
-    auto s_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 + x); };
-    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
-    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 6 + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 8), asked = drained + 8;
+    auto s_full = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 * t + x); };
+    auto s_empty = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + 2 * t + x); };
+    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
+    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 10 + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 12), asked = drained + 8;
     if (tid == 0) {
         // s_empty: each of the warps that read; i_empty: every warp but the copies'
-        for (int i = 0; i < 4 + 2 * kScQ + 10; ++i) {
+        for (int i = 0; i < 4 + 2 * kScQ + 14; ++i) {
             const uint32_t bar = bar0 + 8 * i;
-            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 17 : bar >= s_empty(0) ? 8 : 1);
+            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 17 : bar >= s_empty(0, 0) ? 4 : 1);
         }
         tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -810,16 +810,23 @@ __global__ void __launch_bounds__(kScThreads, 1)
             bool head = true;
             while (s.left > 0) {
                 if (head && ++set == kScK) set = 0, kp ^= 1;
-                // s_empty passes at once the first time
-                ok = __all_sync(~0u, tc_wait3(k_full(set), kp, q_full(qs), qp, s_empty(buf), sp, &tail.stop));
+                const uint32_t q = sq + qs * kTileBytes, k = sm + 2 * set * kTileBytes, d = tmu + 128 * buf;
+                // s_empty passes at once the first time; the second wait runs under the first tile's products
+                ok = __all_sync(~0u, tc_wait3(k_full(set), kp, q_full(qs), qp, s_empty(0, buf), sp, &tail.stop));
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+                    tc_mma_tile(d, q, k, kHalf);
+                    tc_commit(s_full(0, buf));
+                }
+                __syncwarp();
+                ok = __all_sync(~0u, tc_wait(s_empty(1, buf), sp, &tail.stop));
                 if (!ok) break;
                 tc_fence_after();
                 head = s.next();
                 if (lead) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        tc_mma_tile(tmu + 256 * t + 128 * buf, sq + qs * kTileBytes, sm + (2 * set + t) * kTileBytes, kHalf);
-                    tc_commit(s_full(buf));
+                    tc_mma_tile(d + 256, q, k + kTileBytes, kHalf);
+                    tc_commit(s_full(1, buf));
                     tc_commit(q_empty(qs));
                     if (head || s.left == 0) tc_commit(k_empty(set));
                 }
@@ -863,23 +870,22 @@ __global__ void __launch_bounds__(kScThreads, 1)
             const float *l0 = lse + (int64_t)it.b * a.Hq * a.n_q + off;
             auto fetch = [&](const ScoreSteps &s) {   // rows that no query fills, or that see no key, take no part
                 if (s.left <= 0 || r >= rows || s.q * T + tok >= it.q_len) return -INFINITY;
-                const float y = __ldg(l0 + (int64_t)s.h * a.G * a.n_q + s.q * T);
-                return y == -INFINITY ? y : -kLog2e * y;
+                return __ldg(l0 + (int64_t)s.h * a.G * a.n_q + s.q * T);
             };
             ScoreSteps s = W.s;
             if ((nq & 1) != x && s.left > 0) s.next(), ++nq;   // the first step of the group's parity
             float ahead = fetch(s);
             while (s.left > 0) {
                 const int i0 = s.q * T, p_lo = shift + i0;
-                const float ls = ahead;
+                const float ls = ahead == -INFINITY ? ahead : -kLog2e * ahead;
                 s.next();
                 ++nq;
                 if (s.left > 0) s.next(), ++nq;
                 ahead = fetch(s);   // of the group's next step
-                ok = ok && __all_sync(~0u, tc_wait(s_full(x), turn++ & 1, &tail.stop));
+                ok = ok && __all_sync(~0u, tc_wait(s_full(t, x), turn++ & 1, &tail.stop));
                 if (!ok) continue;
                 tc_fence_after();
-                const uint64_t mm = pair2(ls, ls);
+                const uint64_t mm = pair2(ls, ls);   // (used first after a wait: the load is two steps old)
                 float v[2][32];
                 tc_ld32(tS, v[0]);
                 tc_ld32(tS + 32, v[1]);
@@ -899,7 +905,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         if (q == 2) {
                             tc_fence_before();
                             __syncwarp();
-                            if ((tid & 31) == 0) tc_arrive(s_empty(x));
+                            if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
                         }
                     }
                     float(&y)[32] = v[q & 1];
