@@ -464,6 +464,42 @@ def test_refusals():
     assert torch.equal(out, kept) and cache.status() == 0
 
 
+def test_outputs_that_are_also_side_operands_are_refused():
+    B, Hq, Hkv, n = 1, 8, 2, 4
+    cache = cache_for(B, Hq, Hkv)
+    q, k = rand(1, B, n, Hq, D).cuda(), rand(2, B, n, Hkv, D).cuda()
+    mem = torch.zeros(n * Hq * D, dtype=torch.bfloat16, device="cuda")
+    out = mem.view(B, n, Hq, D)
+    inv, pos, w = mem[:128].view(torch.float32), mem[:16].view(torch.int64).view(B, n), mem[128:256]
+    inv.copy_(freqs())
+    good = freqs().cuda()
+    for call in (lambda: cache.qk_norm_rope(0, q, k, inv, q_out=out),
+                 lambda: cache.qk_norm_rope(0, q, k, good, positions=pos, q_out=out),
+                 lambda: cache.qk_norm_rope(0, q, k, good, q_weight=w, q_out=out),
+                 lambda: cache.qk_norm_rope(0, q, k, good, k_weight=w, q_out=out)):
+        with pytest.raises(binding.QevictError) as e:
+            call()
+        assert e.value.name == "INVALID_ARG" and "overlaps" in str(e.value), str(e.value)
+    assert torch.equal(inv, good) and cache.status() == 0
+
+
+def test_spans_wider_than_32_bits_are_all_the_keys():
+    B, Hq, Hkv, n = 1, 8, 2, 300
+    cache = cache_for(B, Hq, Hkv)
+    q, k, v = rand(1, B, n, Hq, D).cuda(), rand(2, B, n, Hkv, D).cuda(), rand(3, B, n, Hkv, D).cuda()
+    out, lse = cache.span_attention(0, q, k, v)
+    scores = cache.span_scores(0, q, k, lse)
+    sunk, sunk_scores = cache.span_attention(0, q, k, v, span=7, sinks=n)[0], cache.span_scores(0, q, k, lse, span=7, sinks=n)
+    for wide in (2 ** 31 - 1, 2 ** 32 + 5):
+        a, b = cache.span_attention(0, q, k, v, span=wide)
+        assert torch.equal(a, out) and torch.equal(b, lse)
+        # (the tiles may be shared out otherwise under a short span, so it is the same call with n sinks that is equal)
+        assert torch.equal(cache.span_attention(0, q, k, v, span=7, sinks=wide)[0], sunk)
+        assert torch.equal(cache.span_scores(0, q, k, lse, span=wide), scores)
+        assert torch.equal(cache.span_scores(0, q, k, lse, span=7, sinks=wide), sunk_scores)
+    assert cache.status() == 0
+
+
 # ---- the run of them -----------------------------------------------------------------
 @pytest.mark.parametrize("budget", [0.5, 0.2])
 @pytest.mark.parametrize("per_head", [False, True])

@@ -737,6 +737,10 @@ qevict_status qevict_qk_norm_rope(qevict_cache *c, int32_t layer, const void *q,
             if (j < i && o0 < (uintptr_t)io[j].dst + a.tokens * io[j].heads * kHeadDim * 2 && (uintptr_t)io[j].dst < o1)
                 return fail(QEVICT_ERR_INVALID_ARG, "two outputs overlap");
         }
+        const Extent x[4] = {{positions, a.tokens * 8, "positions"}, {inv_freq, kHeadDim / 2 * 4, "inv_freq"},
+                             {q_weight, kHeadDim * 2, "q_weight"}, {k_weight, kHeadDim * 2, "k_weight"}};
+        st = check_apart({io[i].dst, a.tokens * io[i].heads * kHeadDim * 2, "an output"}, x, 4);
+        if (st) return st;
     }
     st = check_device(c);
     if (st) return st;

@@ -4,7 +4,6 @@
 // key j iff j <= p and (j > p - span or j < sinks).
 #include "qevict_tc.cuh"
 
-#include <limits.h>
 #include <math.h>
 
 namespace qevict {
@@ -46,17 +45,27 @@ __device__ __forceinline__ int clamped(const int32_t *len, int b, int n) {
 //
 // Rows are (token, query head of one KV head's group), token-major, 128 / G
 // tokens to a tile of 128 rows, so every head of the group shares the tile's keys.
-// Ten warps: two softmax warpgroups (a thread owns a row), one thread that
-// issues the products, one that issues the copies. Tensor memory holds a logit
+// Twelve warps: two softmax warpgroups (a thread owns a row), one warp that
+// issues the products, one thread that issues the copies. Tensor memory holds a logit
 // tile S and an output tile O (fp32, 128 x 128) per softmax group; the
 // probabilities overwrite their logits as bf16 and are the A operand of P V
 // from there, so neither S nor P leaves the SM. While one group is in its
 // softmax, the tensor cores work for the other.
 //
-// Wide: the groups take two neighbouring query tiles over the same keys.
+// Wide: the groups take two neighbouring query tiles over the same keys, and the
+// CTA goes on with units of CTAs that have not started. Bound by the products and by
+// the chain between them: a group's loads, maximum, exponentials (at 32 a cycle and
+// SM half as long as the tile's products) and stores take a little longer than the
+// other group's two products; 32 query heads on 8: a prompt of 8K 320 us
+// (1,690 TFLOP/s; the tensor pipe active 73 % of the cycles), of 32K 5.0 to 5.3 ms
+// (1,660 to 1,760; the clock falls under the power limit), with a span of 4K 1.07 ms
+// (1,540: a fifth of its tiles are masked or half seen).
 // Split: both take one query tile, every other key tile each, and the key tiles
 // are further divided over the CTAs of a cluster; the partial (max, sum, O)
-// meet in shared memory. No scratch in device memory either way.
+// meet in shared memory. No scratch in device memory either way. Single tokens
+// are bound by the keys and values: 8 sequences of 26K to 32K 146 us (6.6 TB/s);
+// 16 with a span of 4K 27 us (5.0 TB/s: the first copies and the meeting, about
+// 5 us, do not overlap the stream).
 constexpr int kSoftmax = 256;                 // threads of the two softmax groups
 constexpr int kAttThreads = kSoftmax + 128;   // and a group of four warps for copies and products
 constexpr int kAttSlots = 7;                  // 32 KB slots of shared memory: query tiles, then the key/value ring
@@ -203,8 +212,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     };
     if (tid == 9 * 32) {
         // p_full: the group's four warps; u_empty: the product warp and both groups' warps
-        for (int i = 0; i < 2 * NS + 15; ++i)
-            tc_mbar_init(bar0 + 8 * i, i == 2 * NS + 12 || i == 2 * NS + 13 ? 9 : i >= 2 * NS + 5 && i < 2 * NS + 9 ? 4 : 1);
+        for (int i = 0; i < 2 * NS + 15; ++i) {
+            const int x = i - 2 * NS;
+            tc_mbar_init(bar0 + 8 * i, x == 12 || x == 13 ? 9 : x >= 5 && x < 9 ? 4 : 1);
+        }
         stop = 0;
         for (int i = 0; i < 8; ++i) poison[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -509,7 +520,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const float inv = 1.f / l;
                 const bool none = l == 0.f;   // no key seen
                 const int64_t head = kvh * a.G + g;
-                uint32_t *dst = reinterpret_cast<uint32_t *>(out + (((int64_t)b * a.n_q + i0 + tok) * a.Hq + head) * kHeadDim);
+                uint32_t *dst =
+                    reinterpret_cast<uint32_t *>(out + (((int64_t)b * a.n_q + i0 + tok) * a.Hq + head) * kHeadDim);
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     float o[32];
@@ -554,7 +566,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (valid && done > 0 && ok) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)   // the swizzle spreads a warp's rows over the banks
-                            part[(8 * q + e) ^ (r & 31)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            part[(8 * q + e) ^ (r & 31)] =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                     __syncwarp();
                 }
@@ -576,7 +589,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             const float2 s = cl_ld2(cl_addr(st + (x & 1) * kTile * 8 + r * 8, x >> 1));
                             if (s.y == 0.f) continue;   // saw no key (a sum of NaN goes on)
                             const float f = s.x == -INFINITY ? 1.f : tc_ex2(s.x - top);
-                            const float4 y = cl_ld4(cl_addr(ring + (x & 1) * 2 * kTileBytes + r * 512 + 16 * (ch ^ (r & 31)), x >> 1));
+                            const uint32_t at = ring + (x & 1) * 2 * kTileBytes + r * 512 + 16 * (ch ^ (r & 31));
+                            const float4 y = cl_ld4(cl_addr(at, x >> 1));
                             l = fmaf(s.y, f, l);
                             o.x = fmaf(y.x, f, o.x);
                             o.y = fmaf(y.y, f, o.y);
@@ -585,8 +599,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                         const float inv = l == 0.f ? 0.f : 1.f / l;
                         const int64_t head = kvh * a.G + r % a.G;
-                        __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
-                        __nv_bfloat16 *dst = out + (((int64_t)b * a.n_q + i0 + r / a.G) * a.Hq + head) * kHeadDim + 4 * ch;
+                        __nv_bfloat162 p[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv),
+                                               __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+                        __nv_bfloat16 *dst =
+                            out + (((int64_t)b * a.n_q + i0 + r / a.G) * a.Hq + head) * kHeadDim + 4 * ch;
                         *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(p);
                         if (bad) add_cleared(a, U, values, p_lo + r / a.G, 4 * ch, dst);
                         if (ch == 0 && lse)
@@ -612,8 +628,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // log-sum-exp in a register; it sums the row's masses over 16 keys at a time (a
 // window is a multiple of 16) into eight registers that it keeps over all query
 // tiles, and the rows meet once an item, by shuffles. Shared memory then feeds the
-// products alone: they read it at its full rate, and with the keys as the rows,
-// which needs a log-sum-exp for every column from there, a step took 1.4 times as long.
+// products alone. (Keys as the rows, with a log-sum-exp for every column out of
+// shared memory, came out equal at 8K, 204 us, and slower with a span of 1K over
+// 4 x 8K, 310 and 300 us.)
 // An item is a run of 256 keys (rounded down to whole windows) of one sequence
 // (of one KV head with per-head units); its steps are the (KV head, query tile)
 // pairs that see some of them. Where the items are few, each is split into parts
@@ -622,7 +639,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // next item run under this one.
 // Four groups of four warps take the masses, each of one key tile in every other
 // step from a logit tile of its own, so that their waits and loads fall at
-// different times; one warp issues the products, one the copies.
+// different times; one warp issues the products, one the copies. (Two groups, a
+// group then reading every step: 241 us at 8K and 130 us for 64 queries of 8 x 32K.
+// Groups of half a tile's keys, which give their half back before the
+// exponentials: 238 and 127 us.)
+// 32 query heads on 8: every query of 8K 204 us (1,350 TFLOP/s), 64 queries of
+// 8 x 32K 115 us (1,200 TFLOP/s and 4.7 TB/s). Bound by the way round a logit
+// tile: product, load, release (about 1,630 cycles a step of two tiles, whose
+// products take 1,024); the exponentials, 32 a cycle and SM, take as long as the products.
 constexpr int kScMass = 512;                  // threads of the four groups
 constexpr int kScThreads = kScMass + 64;
 constexpr int kScK = 2;                       // sets of two key tiles
@@ -725,7 +749,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
     // rows of a query tile that no query fills stay zero
     for (int i = tid; i < kScQ * 2 * (kTile - rows) * 8; i += kScThreads) {
         const int x = i & 7, r = (i >> 3) % (kTile - rows), h = (i >> 3) / (kTile - rows);
-        *reinterpret_cast<int4 *>(gen + 2 * kScK * kTileBytes + h * kHalf + (rows + r) * 128 + 16 * x) = make_int4(0, 0, 0, 0);
+        uint8_t *at = gen + 2 * kScK * kTileBytes + h * kHalf + (rows + r) * 128 + 16 * x;
+        *reinterpret_cast<int4 *>(at) = make_int4(0, 0, 0, 0);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
@@ -885,13 +910,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 ok = ok && __all_sync(~0u, tc_wait(s_full(t, x), turn++ & 1, &tail.stop));
                 if (!ok) continue;
                 tc_fence_after();
-                const uint64_t mm = pair2(ls, ls);   // (used first after a wait: the load is two steps old)
+                const uint64_t mm = pair2(ls, ls);   // (used first after a wait: the load is the group's last step old)
                 float v[2][32];
                 tc_ld32(tS, v[0]);
                 tc_ld32(tS + 32, v[1]);
                 const bool plain =
                     i0 + T <= it.q_len && k0 + tk - 1 <= p_lo && (k0 > p_lo + T - 1 - a.span || k0 + tk <= a.sinks);
-                const int hi = i0 + tok < it.q_len ? p_lo + tok - k0 : -1, lo = p_lo + tok - k0 - a.span, sk = a.sinks - k0;
+                const int hi = i0 + tok < it.q_len ? p_lo + tok - k0 : -1, lo = p_lo + tok - k0 - a.span;
+                const int sk = a.sinks - k0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if ((q & 1) == 0) {
@@ -962,7 +988,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
     if (warp == 0) tc_free<512>(tm);
 }
 
-// The parts' window masses in order, one window a thread.
+// The parts' window masses in order, one window a thread: 2 to 3 us behind the items,
+// of which the launch is most (at most 256 KB to read).
 __global__ void __launch_bounds__(128) span_scores_sum_kernel(const float *part, float *scores, int64_t n, int parts,
                                                               float heads) {
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
