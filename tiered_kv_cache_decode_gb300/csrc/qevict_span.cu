@@ -56,10 +56,10 @@ __device__ __forceinline__ int clamped(const int32_t *len, int b, int n) {
 // CTA goes on with units of CTAs that have not started. Bound by the products and by
 // the chain between them: a group's loads, maximum, exponentials (at 32 a cycle and
 // SM half as long as the tile's products) and stores take a little longer than the
-// other group's two products; 32 query heads on 8: a prompt of 8K 320 us
-// (1,690 TFLOP/s; the tensor pipe active 73 % of the cycles), of 32K 5.0 to 5.3 ms
-// (1,660 to 1,760; the clock falls under the power limit), with a span of 4K 1.07 ms
-// (1,540: a fifth of its tiles are masked or half seen).
+// other group's two products; 32 query heads on 8: a prompt of 8K 322 us
+// (1,710 TFLOP/s; the tensor pipe active 73 % of the cycles), of 32K 5.0 to 5.3 ms
+// (1,660 to 1,760; the clock falls under the power limit), four of 8K with
+// a span of 4K 1.03 ms (1,600: some of its tiles are half masked).
 // Split: both take one query tile, every other key tile each, and the key tiles
 // are further divided over the CTAs of a cluster; the partial (max, sum, O)
 // meet in shared memory. No scratch in device memory either way. Single tokens
@@ -151,6 +151,30 @@ __device__ __forceinline__ void add_cleared(const SpanArgs &a, const AttUnit &U,
     if (any)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = __float2bfloat16_rn(__bfloat162float(o[e]) + x[e]);
+}
+
+// Four lanes, each with 64 bytes of a row of its own as four chunks, trade them by two
+// exchanges: afterwards lane i of the four has chunk i of each of the four rows, and a store
+// of the warp covers 8 rows x 64 bytes instead of 32 rows x 16 bytes, a quarter of the lines
+// (stores of a lane's own row and these: three prompts of 2K 88 and 79 us, 8 of 8K with
+// a span of 128 403 and 341 us; both halves of the row unrolled, so that the second loads
+// under the first: 83 and 350, the code is run once a unit and comes from far).
+__device__ __forceinline__ void trade_chunks(uint32_t (&w)[16]) {
+    const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+#pragma unroll
+    for (int m = 0; m < 16; m += 8)
+#pragma unroll
+        for (int e = m; e < m + 4; ++e) {
+            const uint32_t got = __shfl_xor_sync(~0u, b0 ? w[e] : w[e + 4], 1);
+            w[e] = b0 ? got : w[e];
+            w[e + 4] = b0 ? w[e + 4] : got;
+        }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t got = __shfl_xor_sync(~0u, b1 ? w[e] : w[e + 8], 2);
+        w[e] = b1 ? got : w[e];
+        w[e + 8] = b1 ? w[e + 8] : got;
+    }
 }
 
 template <bool SPLIT>
@@ -520,33 +544,36 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const float inv = 1.f / l;
                 const bool none = l == 0.f;   // no key seen
                 const int64_t head = kvh * a.G + g;
-                uint32_t *dst =
-                    reinterpret_cast<uint32_t *>(out + (((int64_t)b * a.n_q + i0 + tok) * a.Hq + head) * kHeadDim);
+                __nv_bfloat16 *base = out + (((int64_t)b * a.n_q + i0) * a.Hq + kvh * a.G) * kHeadDim;
+                const int row = valid ? tok * a.Hq + g : -1;   // from base; -1: not written
+                int at[4];                                     // of the lane's four
+#pragma unroll
+                for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(~0u, row, (tid & 28) + e);
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     float o[32];
                     tc_ld32(tO + 32 * q, o);
                     tc_wait_ld();
                     tc_tie(o);
-                    if (valid && ok) {
+                    uint32_t p[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t p[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const __nv_bfloat162 pk = __floats2bfloat162_rn(none ? 0.f : o[e + 2 * y] * inv,
-                                                                                none ? 0.f : o[e + 2 * y + 1] * inv);
-                                p[y] = *reinterpret_cast<const uint32_t *>(&pk);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + 16 * q + e / 2) = make_uint4(p[0], p[1], p[2], p[3]);
-                        }
+                    for (int e = 0; e < 16; ++e) {
+                        const __nv_bfloat162 pk =
+                            __floats2bfloat162_rn(none ? 0.f : o[2 * e] * inv, none ? 0.f : o[2 * e + 1] * inv);
+                        p[e] = *reinterpret_cast<const uint32_t *>(&pk);
                     }
+                    trade_chunks(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (at[e] >= 0 && ok)
+                            *reinterpret_cast<uint4 *>(base + (int64_t)at[e] * kHeadDim + 32 * q + 8 * (tid & 3)) =
+                                make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
                     __syncwarp();
                 }
                 if (poison[c_ & 7] && valid && ok) {
 #pragma unroll 1
                     for (int ch = 0; ch < kHeadDim; ch += 4)
-                        add_cleared(a, U, values, pos, ch, reinterpret_cast<__nv_bfloat16 *>(dst) + ch);
+                        add_cleared(a, U, values, pos, ch, base + (int64_t)row * kHeadDim + ch);
                 }
                 if (valid && ok && lse)
                     lse[((int64_t)b * a.Hq + head) * a.n_q + i0 + tok] =
