@@ -19,7 +19,7 @@ constexpr int kGroup = 32;             // channels per INT2 group
 constexpr int kGroups = kHeadDim / kGroup;
 constexpr int kMaxG = 8;               // query heads per KV head
 constexpr int kMaxSplits = 32;         // decode CTAs per (sequence, KV head)
-constexpr int kMaxSpanParts = 16;      // parts into which a run of keys' window scores is split
+constexpr int kMaxSpanParts = 32;      // parts into which a run of keys' window scores is split
 constexpr int kSpanPartFloats = 1 << 16;   // a layer's room for their sums
 constexpr int kMaxSpanTokens = 1 << 29; // tokens per sequence of the span calls (int sums stay in range)
 constexpr int kVTile = 16;             // tokens per transposed V-code word

@@ -1133,7 +1133,9 @@ cudaError_t launch_span_scores(const SpanArgs &a, const CacheDev &C, int layer, 
     const int units = per_head ? a.B * a.Hkv : a.B;
     const int64_t items = (int64_t)runs * units, wins = (int64_t)units * n_win;
     // Parts per item: enough that the longest (at the lengths that the host knows) does not
-    // outlast an even share of the SMs, and no shorter than two steps.
+    // outlast an even share of the SMs, and no shorter than two steps. (At most 16, 32 or 64 parts:
+    // every query of 2K 37.7, 26.6, 30.0 us, of 4K 62.8, 62.6, 68.8 us, 2 x 8K with a span of 1K
+    // and sinks 159, 164, 164 us.)
     int parts = 1;
     if (items < 8 * num_sms) {
         int64_t heavy = 0, total = 0;
