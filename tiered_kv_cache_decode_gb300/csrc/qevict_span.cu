@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // S_t = Q K^T; done: the key tile's slot is free after it, last: so are the query tiles
             auto logits = [&](int t, bool done, bool last) {
                 if (lead) {
-                    tc_mma_tile(tmu + 128 * t, sm + (SPLIT ? 0 : t * kTileBytes), ring + ks * kTileBytes, kHalf);
+                    tc_mma_tile<kTile>(tmu + 128 * t, sm + (SPLIT ? 0 : t * kTileBytes), ring + ks * kTileBytes);
                     tc_commit(s_full(t));
                     if (done) tc_commit(empty(ks));
                     if (done && last) tc_commit(q_empty);
@@ -735,7 +735,7 @@ struct ScoreTail {
     float segs[2][2][4][8];     // masses of 16 keys by key tile, step parity and warp
     ScoreWork given[2];         // items that the copy thread has worked out
     uint4 ticket;               // the answer to the copy thread's last request
-    uint64_t bars[4 + 2 * kScQ + 14];
+    uint64_t bars[4 + 2 * kScQ + 10];
     uint32_t slot;
     int stop, go[2];
 };
@@ -759,16 +759,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto k_empty = [&](int s) { return bar0 + 16 + 8 * s; };
     auto q_full = [&](int s) { return bar0 + 32 + 8 * s; };
     auto q_empty = [&](int s) { return bar0 + 32 + 8 * (kScQ + s); };
-    auto s_full = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 * t + x); };
-    auto s_empty = [&](int t, int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + 2 * t + x); };
-    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 8 + x); };
-    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 10 + x); };
-    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 12), asked = drained + 8;
+    auto s_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + x); };
+    auto s_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 2 + x); };
+    auto i_empty = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 4 + x); };
+    auto i_full = [&](int x) { return bar0 + 32 + 8 * (2 * kScQ + 6 + x); };
+    const uint32_t drained = bar0 + 32 + 8 * (2 * kScQ + 8), asked = drained + 8;
     if (tid == 0) {
         // s_empty: each of the warps that read; i_empty: every warp but the copies'
-        for (int i = 0; i < 4 + 2 * kScQ + 14; ++i) {
+        for (int i = 0; i < 4 + 2 * kScQ + 10; ++i) {
             const uint32_t bar = bar0 + 8 * i;
-            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 17 : bar >= s_empty(0, 0) ? 4 : 1);
+            tc_mbar_init(bar, bar >= i_full(0) ? 1 : bar >= i_empty(0) ? 17 : bar >= s_empty(0) ? 8 : 1);
         }
         tail.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = tail.slot;   // logits of group t, buffer x at column 256 t + 128 x
+    const uint32_t tm = tail.slot;   // logits of buffer x, key tile t at column 256 x + 128 t
     bool ok = true;
     // The next item of a warp (c: how many it has had), false when there is none: the copy
     // thread, which is steps ahead, has worked it out, so the other warps do not stall on it.
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         tc_expect_tx(k_full(set), 2 * kTileBytes);
                         for (int t = 0; t < 2; ++t)
                             for (int h = 0; h < 2; ++h)
-                                tc_tma_4d(sm + (2 * set + t) * kTileBytes + h * kHalf, &kmap, 64 * h, s.h, it.k0 + t * tk,
+                                tc_tma_4d(sm + 2 * set * kTileBytes + (2 * h + t) * kHalf, &kmap, 64 * h, s.h, it.k0 + t * tk,
                                           it.b, k_full(set));
                         ++nk;
                     }
@@ -863,23 +863,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
             bool head = true;
             while (s.left > 0) {
                 if (head && ++set == kScK) set = 0, kp ^= 1;
-                const uint32_t q = sq + qs * kTileBytes, k = sm + 2 * set * kTileBytes, d = tmu + 128 * buf;
-                // s_empty passes at once the first time; the second wait runs under the first tile's products
-                ok = __all_sync(~0u, tc_wait3(k_full(set), kp, q_full(qs), qp, s_empty(0, buf), sp, &tail.stop));
-                if (!ok) break;
-                tc_fence_after();
-                if (lead) {
-                    tc_mma_tile(d, q, k, kHalf);
-                    tc_commit(s_full(0, buf));
-                }
-                __syncwarp();
-                ok = __all_sync(~0u, tc_wait(s_empty(1, buf), sp, &tail.stop));
+                const uint32_t q = sq + qs * kTileBytes, k = sm + 2 * set * kTileBytes;
+                // s_empty passes at once the first time
+                ok = __all_sync(~0u, tc_wait3(k_full(set), kp, q_full(qs), qp, s_empty(buf), sp, &tail.stop));
                 if (!ok) break;
                 tc_fence_after();
                 head = s.next();
                 if (lead) {
-                    tc_mma_tile(d + 256, q, k + kTileBytes, kHalf);
-                    tc_commit(s_full(1, buf));
+                    tc_mma_tile<2 * kTile>(tmu + 256 * buf, q, k);
+                    tc_commit(s_full(buf));
                     tc_commit(q_empty(qs));
                     if (head || s.left == 0) tc_commit(k_empty(set));
                 }
@@ -897,7 +889,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
         __syncwarp();
     } else {
         const int t = warp >> 3, x = (warp >> 2) & 1, r = tid & 127;
-        const uint32_t tS = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * t + 128 * x;
+        const uint32_t tS = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * x + 128 * t;
         const int tok = r / a.G;
         const int64_t off = (int64_t)(r % a.G) * a.n_q + tok;   // the row's log-sum-exp in a query tile's
         const float c = kLog2e * rsqrtf((float)kHeadDim);
@@ -935,7 +927,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 ++nq;
                 if (s.left > 0) s.next(), ++nq;
                 ahead = fetch(s);   // of the group's next step
-                ok = ok && __all_sync(~0u, tc_wait(s_full(t, x), turn++ & 1, &tail.stop));
+                ok = ok && __all_sync(~0u, tc_wait(s_full(x), turn++ & 1, &tail.stop));
                 if (!ok) continue;
                 tc_fence_after();
                 const uint64_t mm = pair2(ls, ls);   // (used first after a wait: the load is the group's last step old)
@@ -959,7 +951,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         if (q == 2) {
                             tc_fence_before();
                             __syncwarp();
-                            if ((tid & 31) == 0) tc_arrive(s_empty(t, x));
+                            if ((tid & 31) == 0) tc_arrive(s_empty(x));
                         }
                     }
                     float(&y)[32] = v[q & 1];

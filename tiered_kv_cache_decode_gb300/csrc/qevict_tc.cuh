@@ -101,9 +101,9 @@ __device__ __forceinline__ uint32_t tc_desc_k(uint32_t addr) { return (1u << 16)
 __device__ __forceinline__ uint32_t tc_desc_mn(uint32_t addr, uint32_t lead) {
     return ((lead >> 4) << 16) | ((addr & 0x3ffff) >> 4);
 }
-// Instruction descriptor: bf16 x bf16 -> fp32, M = 128, N = 128; B MN-major or K-major.
-__host__ __device__ constexpr uint32_t tc_idesc(bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor: bf16 x bf16 -> fp32, M = 128; B MN-major or K-major.
+__host__ __device__ constexpr uint32_t tc_idesc(bool b_mn, uint32_t n = 128) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // D (+)= A B over K = 16, A in shared (ss) or tensor (ts) memory. The elected lane
@@ -127,12 +127,13 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, ui
         "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi)
         : "memory");
 }
-// a 128 x 128 x 128 product of two tiles in shared memory, halves of 64 channels `half` bytes apart
-__device__ __forceinline__ void tc_mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t half) {
-    const uint32_t da = tc_desc_k(a), db = tc_desc_k(b), h = half >> 4;
+// a 128 x N x 128 product of two tiles in shared memory, halves of 64 channels 128 and N rows apart
+template <int N>
+__device__ __forceinline__ void tc_mma_tile(uint32_t d, uint32_t a, uint32_t b) {
+    const uint32_t da = tc_desc_k(a), db = tc_desc_k(b), ha = 128 * 128 / 16, hb = N * 128 / 16;
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-        tc_mma_ss(d, da + (s >> 2) * h + (s & 3) * 2, db + (s >> 2) * h + (s & 3) * 2, tc_idesc(false), s > 0);
+        tc_mma_ss(d, da + (s >> 2) * ha + (s & 3) * 2, db + (s >> 2) * hb + (s & 3) * 2, tc_idesc(false, N), s > 0);
 }
 // all products issued so far arrive on `bar` when they have ended
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
