@@ -656,8 +656,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // window is a multiple of 16) into eight registers that it keeps over all query
 // tiles, and the rows meet once an item, by shuffles. Shared memory then feeds the
 // products alone. (Keys as the rows, with a log-sum-exp for every column out of
-// shared memory, came out equal at 8K, 204 us, and slower with a span of 1K over
-// 4 x 8K, 310 and 300 us.)
+// shared memory, came out equal at 8K and slower with a span of 1K over 4 x 8K, 310
+// and 300 us.)
 // An item is a run of 256 keys (rounded down to whole windows) of one sequence
 // (of one KV head with per-head units); its steps are the (KV head, query tile)
 // pairs that see some of them. Where the items are few, each is split into parts
@@ -665,15 +665,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // work of CTAs that have not started, the longest first, and the copies of the
 // next item run under this one.
 // Four groups of four warps take the masses, each of one key tile in every other
-// step from a logit tile of its own, so that their waits and loads fall at
-// different times; one warp issues the products, one the copies. (Two groups, a
+// step, so that their waits and loads fall at different times; one warp issues the
+// products, both key tiles' in one of 256 columns, one the copies. (Two groups, a
 // group then reading every step: 241 us at 8K and 130 us for 64 queries of 8 x 32K.
-// Groups of half a tile's keys, which give their half back before the
-// exponentials: 238 and 127 us.)
-// 32 query heads on 8: every query of 8K 204 us (1,350 TFLOP/s), 64 queries of
-// 8 x 32K 115 us (1,200 TFLOP/s and 4.7 TB/s). Bound by the way round a logit
-// tile: product, load, release (about 1,630 cycles a step of two tiles, whose
-// products take 1,024); the exponentials, 32 a cycle and SM, take as long as the products.
+// Groups of half a tile's keys, which give their half back before the exponentials:
+// 238 and 127 us. A product of its own for each tile: 203 and 117 us.)
+// 32 query heads on 8: every query of 8K 200 us (1,375 TFLOP/s), 64 queries of
+// 8 x 32K 116 us (1,180 TFLOP/s and 4.65 TB/s). Bound by the way round a logit
+// buffer: product, load, half of the exponentials, release (about 1,600 cycles a step,
+// the products of which take 1,024, as its exponentials do at 32 a cycle and SM).
 constexpr int kScMass = 512;                  // threads of the four groups
 constexpr int kScThreads = kScMass + 64;
 constexpr int kScK = 2;                       // sets of two key tiles
