@@ -489,7 +489,8 @@ def test_spans_wider_than_32_bits_are_all_the_keys():
     q, k, v = rand(1, B, n, Hq, D).cuda(), rand(2, B, n, Hkv, D).cuda(), rand(3, B, n, Hkv, D).cuda()
     out, lse = cache.span_attention(0, q, k, v)
     scores = cache.span_scores(0, q, k, lse)
-    sunk, sunk_scores = cache.span_attention(0, q, k, v, span=7, sinks=n)[0], cache.span_scores(0, q, k, lse, span=7, sinks=n)
+    sunk = cache.span_attention(0, q, k, v, span=7, sinks=n)[0]
+    sunk_scores = cache.span_scores(0, q, k, lse, span=7, sinks=n)
     for wide in (2 ** 31 - 1, 2 ** 32 + 5):
         a, b = cache.span_attention(0, q, k, v, span=wide)
         assert torch.equal(a, out) and torch.equal(b, lse)
@@ -497,6 +498,10 @@ def test_spans_wider_than_32_bits_are_all_the_keys():
         assert torch.equal(cache.span_attention(0, q, k, v, span=7, sinks=wide)[0], sunk)
         assert torch.equal(cache.span_scores(0, q, k, lse, span=wide), scores)
         assert torch.equal(cache.span_scores(0, q, k, lse, span=7, sinks=wide), sunk_scores)
+    for kw in (dict(span=-2 ** 32), dict(sinks=-2 ** 32)):   # refused, not cut to 32 bits
+        for call in (lambda: cache.span_attention(0, q, k, v, **kw), lambda: cache.span_scores(0, q, k, lse, **kw)):
+            with pytest.raises(binding.QevictError):
+                call()
     assert cache.status() == 0
 
 
