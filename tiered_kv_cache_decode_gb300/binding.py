@@ -517,8 +517,8 @@ class TieredCache:
         rc = self.lib.qevict_span_scores(
             self.handle, layer, q.data_ptr(), n_q, k.data_ptr(), n_kv, side(q_len, per_seq, torch.int32, "q_len"),
             side(kv_len, per_seq, torch.int32, "kv_len"), max(-1, min(span, n_kv)),
-            max(-1, min(sinks, n_kv)), side(lse, (self.B, self.Hq, n_q), torch.float32, "lse"), side(out, (self.units, W), torch.float32, "out"),
-            self._raw_stream(stream))
+            max(-1, min(sinks, n_kv)), side(lse, (self.B, self.Hq, n_q), torch.float32, "lse"),
+            side(out, (self.units, W), torch.float32, "out"), self._raw_stream(stream))
         if rc:
             self._check(rc)
         return out
