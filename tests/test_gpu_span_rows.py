@@ -1,0 +1,71 @@
+"""What a row of the span attention and a window of the span scores depend on: the keys that it sees, and
+nothing else. Results are compared bit by bit with those of other calls, or with the definition where
+infinities and zeros decide.
+
+The form that attention takes follows from its sizes (units of two query tiles, at least one per SM: wide;
+fewer: split over clusters), so the sizes here name theirs.
+"""
+import numpy as np
+import pytest
+import torch
+
+import span_util as U
+from tiered_kv_cache_decode_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from tiered_kv_cache_decode_gb300 import build
+    build.build()
+    binding.load()
+
+
+def cache_for(B, Hq, Hkv, w=64, **kw):
+    return binding.TieredCache(B, 1, Hq, Hkv, w, 4096, fp_capacity=1, ledger_capacity=1, **kw)
+
+
+def rand(seed, *shape, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).bfloat16()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def bits(t):
+    return t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
+@pytest.mark.parametrize("B,H,n,key,span", [
+    (2, 16, 1300, 394, 300),    # wide: the key's tile is masked for the second query tile of unit 512..767 alone
+    (3, 16, 1100, 395, 333),
+    (1, 4, 900, 394, 200)])     # split
+def test_infinite_values_of_probability_zero(B, H, n, key, span):
+    """A key whose probability rounds to 0 holds infinities and a NaN: the rows that see it take them, whichever
+    of a tile's two query tiles masks some of its keys."""
+    q, k, v = rand(1, B, n, H, D), rand(2, B, n, H, D), rand(3, B, n, H, D)
+    q[..., 0] = 8.0
+    k[:, key, :, 0] = -400.0     # a logit near -283: its probability is below every fp32 number
+    clean = v.clone()
+    for ch, value in ((5, float("inf")), (77, float("-inf")), (100, float("nan"))):
+        v[:, key, :, ch] = value
+        clean[:, key, :, ch] = 0.0
+    cache = cache_for(B, H, H)
+    dev = [x.cuda() for x in (q, k, v)]
+    out, lse = cache.span_attention(0, *dev, span=span)
+    assert cache.status() == 0, cache.last_error()
+    got, seen = f64(out), U.visible(n, n, span, 0)[:, key]
+    assert np.all(got[:, seen, :, 5] == np.inf) and np.all(got[:, seen, :, 77] == -np.inf)
+    assert np.all(np.isnan(got[:, seen, :, 100]))
+    rest = np.ones(got.shape, bool)
+    rest[:, seen, :, 5] = rest[:, seen, :, 77] = rest[:, seen, :, 100] = False
+    plain, lse_plain = cache.span_attention(0, dev[0], dev[1], clean.cuda(), span=span)
+    assert np.array_equal(got[rest], f64(plain)[rest]) and torch.equal(lse, lse_plain)
+    for _ in range(10):
+        again, _ = cache.span_attention(0, *dev, span=span)
+        assert torch.equal(bits(again), bits(out))

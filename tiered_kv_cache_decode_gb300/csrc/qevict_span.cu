@@ -489,9 +489,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                 }
                 // A probability of 0 does not keep an infinity or a NaN out of its product, so in a tile
-                // that some row does not see in full they are set to 0 (as are keys that no row of the
-                // CTA sees, which may be anything); rows that do see them get them back at the end.
-                if (masked) {
+                // that some row of the unit does not see in full they are set to 0 (as are keys that no
+                // row of it sees, which may be anything); rows that do see them get them back at the
+                // end. Wide: the first group does it, for both: no product reads the tile before that
+                // group's probabilities have arrived, and none of the second group's is issued before
+                // them, so nothing is written under a product.
+                if ((SPLIT || t == 0) && masked_tile(a, k0, p_lo, p_hi)) {
                     const int i = v_item(j), s = i % NS;
                     ok = __all_sync(~0u, tc_wait(full(s), (i / NS) & 1, &stop));
                     if (!ok) break;
