@@ -69,3 +69,36 @@ def test_infinite_values_of_probability_zero(B, H, n, key, span):
     for _ in range(10):
         again, _ = cache.span_attention(0, *dev, span=span)
         assert torch.equal(bits(again), bits(out))
+
+
+def repeats(n, H, Hkv, w, per_head, n_q=None, B=4, span=0):
+    """Window scores of B copies of one sequence: every copy, and every call, adds in the same order."""
+    q, k = rand(1, 1, n_q or n, H, D).expand(B, -1, -1, -1).contiguous().cuda(), \
+        rand(2, 1, n, Hkv, D).expand(B, -1, -1, -1).contiguous().cuda()
+    cache = cache_for(B, H, Hkv, w=w, per_head=per_head)
+    lse = cache.span_attention(0, q, k, k, span=span)[1][:1].expand(B, -1, -1).contiguous()
+    one, other = (cache.span_scores(0, q, k, lse, span=span).clone() for _ in range(2))
+    by_copy = one.view(B, -1)
+    assert torch.equal(by_copy, by_copy[:1].expand(B, -1))
+    assert torch.equal(one, other)
+    side = torch.cuda.Stream()
+    busy = torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):     # beside other work, which moves the CTAs' starts
+        with torch.cuda.stream(side):
+            busy = torch.tanh(busy @ busy)
+        assert torch.equal(cache.span_scores(0, q, k, lse, span=span), one)
+    assert cache.status() == 0, cache.last_error()
+
+
+@pytest.mark.parametrize("n,H,Hkv,w,per_head,n_q,span", [
+    (2047, 28, 4, 64, False, None, 0), (2047, 28, 4, 64, True, None, 0), (4095, 24, 8, 32, False, None, 0),
+    (2048, 8, 8, 64, True, None, 0), (3001, 14, 2, 16, True, 77, 0), (2500, 16, 4, 48, False, None, 300),
+    (1300, 16, 4, 32, False, None, 0), (1000, 5, 1, 128, False, 333, 0)])
+def test_window_scores_repeat(n, H, Hkv, w, per_head, n_q, span):
+    repeats(n, H, Hkv, w, per_head, n_q, span=span)
+
+
+@pytest.mark.parametrize("n,H,Hkv,per_head", [(2047, 28, 4, False), (2047, 28, 4, True), (8191, 28, 4, False)])
+def test_window_scores_of_one_sequence_repeat(n, H, Hkv, per_head):
+    repeats(n, H, Hkv, 64, per_head, B=1)

@@ -735,7 +735,7 @@ __device__ __forceinline__ ScoreSteps score_steps(const ScoreItem &it, int part,
 
 // what lies behind the tiles in shared memory
 struct ScoreTail {
-    float segs[2][2][4][8];     // masses of 16 keys by key tile, step parity and warp
+    float segs[2][2][4][8];     // masses of 16 keys by key tile, parity of the item's steps, and warp
     ScoreWork given[2];         // items that the copy thread has worked out
     uint4 ticket;               // the answer to the copy thread's last request
     uint64_t bars[4 + 2 * kScQ + 10];
@@ -921,7 +921,10 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 return __ldg(l0 + (int64_t)s.h * a.G * a.n_q + s.q * T);
             };
             ScoreSteps s = W.s;
-            if ((nq & 1) != x && s.left > 0) s.next(), ++nq;   // the first step of the group's parity
+            // The CTA's steps alternate between the groups, so which of them has the item's even steps
+            // depends on the items before it; their sums are added as even and odd, not by group.
+            const int odd = (nq & 1) ^ x;
+            if (odd && s.left > 0) s.next(), ++nq;   // the first step of the group's parity
             float ahead = fetch(s);
             while (s.left > 0) {
                 const int i0 = s.q * T, p_lo = shift + i0;
@@ -990,7 +993,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 }
             acc[0] += __shfl_xor_sync(~0u, acc[0], 2);
             acc[0] += __shfl_xor_sync(~0u, acc[0], 1);
-            if ((tid & 3) == 0) tail.segs[t][x][warp & 3][(tid & 31) >> 2] = acc[0];
+            if ((tid & 3) == 0) tail.segs[t][odd][warp & 3][(tid & 31) >> 2] = acc[0];
             asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
             const int win = k0 / w + r;
             float mass = 0.f;
