@@ -102,3 +102,104 @@ def test_window_scores_repeat(n, H, Hkv, w, per_head, n_q, span):
 @pytest.mark.parametrize("n,H,Hkv,per_head", [(2047, 28, 4, False), (2047, 28, 4, True), (8191, 28, 4, False)])
 def test_window_scores_of_one_sequence_repeat(n, H, Hkv, per_head):
     repeats(n, H, Hkv, 64, per_head, B=1)
+
+
+def same(a, b, rows=None):
+    """Equal bits of two attention results (out [B][n][H][128], lse [B][H][n]), of some rows [n][H] of all."""
+    for x, y, r in ((a[0], b[0], rows), (a[1], b[1], None if rows is None else rows.T)):
+        x, y = bits(x), bits(y)
+        if r is not None:
+            x, y = x[:, r], y[:, r]
+        if not torch.equal(x, y):
+            return False
+    return True
+
+
+FORMS = [  # B, Hq, Hkv, n, span, sinks
+    (3, 16, 8, 1500, 0, 0), (2, 28, 4, 700, 0, 0), (2, 28, 4, 700, 150, 5), (3, 16, 16, 1100, 300, 0),   # wide
+    (1, 8, 2, 900, 0, 0), (1, 12, 2, 333, 70, 3), (1, 3, 1, 500, 0, 0)]                                    # split
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n,span,sinks", FORMS)
+def test_rows_do_not_depend_on_what_they_do_not_see(B, Hq, Hkv, n, span, sinks):
+    """Large finite queries of other rows, later keys and keys before the span change no bit of a row."""
+    cache = cache_for(B, Hq, Hkv)
+    q, k, v = rand(1, B, n, Hq, D).cuda(), rand(2, B, n, Hkv, D).cuda(), rand(3, B, n, Hkv, D).cuda()
+
+    def call(q=q, k=k, v=v):
+        return cache.span_attention(0, q, k, v, span=span, sinks=sinks)
+
+    base = call()
+    every = torch.ones(n, Hq, dtype=torch.bool, device="cuda")
+    for i in (n // 3, n - 2):
+        louder = q.clone()
+        louder[:, i, Hq // 2] *= 64
+        rows = every.clone()
+        rows[i, Hq // 2] = False
+        assert same(base, call(q=louder), rows), f"query {i}"
+    for p in (n // 2 + 3, n - 3):
+        k2, v2 = k.clone(), v.clone()
+        k2[:, p + 1:] *= 64
+        v2[:, p + 1:] *= 64
+        rows = every.clone()
+        rows[p + 1:] = False
+        assert same(base, call(k=k2, v=v2), rows), f"keys after {p}"
+    if span:
+        p = n // 2 + 3
+        k2, v2 = k.clone(), v.clone()
+        k2[:, sinks:p - span + 1] *= 64
+        v2[:, sinks:p - span + 1] *= 64
+        rows = every.clone()
+        rows[:p] = False
+        assert same(base, call(k=k2, v=v2), rows), f"keys before the span of {p}"
+    assert cache.status() == 0, cache.last_error()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n,span,sinks", FORMS)
+def test_padding_does_not_reach_the_rows(B, Hq, Hkv, n, span, sinks):
+    """Queries and keys past a sequence's ends: zeros or large numbers, the same bits."""
+    cache = cache_for(B, Hq, Hkv)
+    q, k, v = rand(1, B, n, Hq, D), rand(2, B, n, Hkv, D), rand(3, B, n, Hkv, D)
+    kv = [n - 5 - 37 * b for b in range(B)]
+    nq = [x - 11 for x in kv]
+    lens = dict(q_len=torch.tensor(nq, dtype=torch.int32).cuda(), kv_len=torch.tensor(kv, dtype=torch.int32).cuda())
+    got, mass = [], []
+    for scale in (0.0, 64.0):
+        a, b, c = q.clone(), k.clone(), v.clone()
+        for x, m in ((a, nq), (b, kv), (c, kv)):
+            for s in range(B):
+                x[s, m[s]:] *= scale
+        a, b, c = a.cuda(), b.cuda(), c.cuda()
+        out = torch.zeros(B, n, Hq, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(B, Hq, n, device="cuda")
+        got.append(cache.span_attention(0, a, b, c, span=span, sinks=sinks, out=out, lse=lse, **lens))
+        lse = lse.clone()
+        for s in range(B):
+            lse[s, :, nq[s]:] = -scale
+        mass.append(cache.span_scores(0, a, b, lse, span=span, sinks=sinks, **lens))
+    assert same(*got) and torch.equal(bits(mass[0]), bits(mass[1]))
+    assert cache.status() == 0, cache.last_error()
+
+
+@pytest.mark.parametrize("G", [3, 5, 6, 7])
+@pytest.mark.parametrize("B,Hkv,n", [(4, 8, 500), (2, 2, 150)])   # wide, split
+def test_calls_leave_nothing_behind(G, B, Hkv, n):
+    """Where a KV head's group does not divide a tile's 128 rows, rows that no query fills: copies of one
+    sequence, and calls after calls on other data, give the same bits."""
+    q, k, v = rand(1, 1, n, G * Hkv, D).expand(B, -1, -1, -1).contiguous().cuda(), \
+        rand(2, 1, n, Hkv, D).expand(B, -1, -1, -1).contiguous().cuda(), \
+        rand(3, 1, n, Hkv, D).expand(B, -1, -1, -1).contiguous().cuda()
+    cache, loud = cache_for(B, G * Hkv, Hkv), cache_for(4, 16, 16)
+    x = rand(4, 4, 700, 16, D, scale=40.0).cuda()
+    out, lse = cache.span_attention(0, q, k, v)
+    scores = cache.span_scores(0, q, k, lse)
+    for b in range(1, B):
+        assert torch.equal(bits(out[b]), bits(out[0])) and torch.equal(lse[b], lse[0])
+        assert torch.equal(scores[b], scores[0])
+    for i in range(6):
+        y = x * (1 - 2 * (i & 1))
+        _, l = loud.span_attention(0, y, x, x)
+        loud.span_scores(0, y, x, l)
+        assert same((out, lse), cache.span_attention(0, q, k, v)), i
+        assert torch.equal(scores, cache.span_scores(0, q, k, lse)), i
+    assert cache.status() == 0, cache.last_error()

@@ -469,11 +469,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // The reference follows the maximum only when it has grown by more than
                 // kRescale in the exponent: probabilities stay below 2^kRescale, and O is
-                // rarely touched between its products.
-                if (__any_sync(~0u, (top - m) * c > kRescale)) {
-                    const float mn = fmaxf(m, top);
-                    const float f = m == -INFINITY ? 0.f : tc_ex2((m - mn) * c);
-                    m = mn;
+                // rarely touched between its products. A warp moves together, but each row's
+                // reference by its own logits alone (a factor of 1 changes no bit): rows share
+                // a warp with later queries, with rows that no query fills and whose part of the
+                // query tile holds anything, and with rows past the sequence's end.
+                const bool move = valid && (top - m) * c > kRescale;
+                if (__any_sync(~0u, move)) {
+                    const float f = !move ? 1.f : m == -INFINITY ? 0.f : tc_ex2((m - top) * c);
+                    if (move) m = top;
                     l *= f;
                     if (done > 0) {   // the product before it has ended: its logits came after it
 #pragma unroll 1
