@@ -203,3 +203,24 @@ def test_calls_leave_nothing_behind(G, B, Hkv, n):
         assert same((out, lse), cache.span_attention(0, q, k, v)), i
         assert torch.equal(scores, cache.span_scores(0, q, k, lse)), i
     assert cache.status() == 0, cache.last_error()
+
+
+@pytest.mark.parametrize("G", [3, 5, 6, 7, 4])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_window_of_infinite_keys_scores_zero(G, per_head):
+    """Keys whose every logit is -inf have no mass, also beside the rows of a query tile that no query fills."""
+    B, Hkv, n, w = 1, 2, 400, 64
+    q, k = rand(1, B, n, G * Hkv, D), rand(2, B, n, Hkv, D)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    clean = k.clone()
+    k[:, 64:128, :, 3] = float("-inf")
+    clean[:, 64:128, :, 3] = -1e4     # a logit of -400 at the least: mass 0 in fp32 too
+    cache = cache_for(B, G * Hkv, Hkv, w=w, per_head=per_head)
+    _, lse = cache.span_attention(0, q.cuda(), k.cuda(), clean.cuda())
+    # the first queries of the run see other keys besides: 64 on
+    got = cache.span_scores(0, q.cuda(), k.cuda(), lse)
+    assert torch.all(got[:, 1] == 0.0) and torch.all(torch.isfinite(got))
+    assert torch.equal(got, cache.span_scores(0, q.cuda(), clean.cuda(), lse))
+    ref = U.scores(f64(q), f64(clean), f64(lse), [n], [n], 0, 0, w, per_head)
+    assert np.all(np.abs(f64(got) - ref) <= 1e-5 * ref + 1e-9)
+    assert cache.status() == 0, cache.last_error()

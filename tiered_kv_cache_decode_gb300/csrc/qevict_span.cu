@@ -985,6 +985,11 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     }
                 }
             }
+            // Rows of a query tile that no query fills are zeros and have the weight 0, but a zero times
+            // an infinite key is NaN.
+            if (r >= rows)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = 0.f;
             // Eight sums over the warp's 32 rows: three exchanges halve the sums that a lane keeps,
             // two add what is left; lane l has the sum of keys 16 (l / 4) .. + 15.
 #pragma unroll
