@@ -355,14 +355,16 @@ qevict_status qevict_k_channel_weights(qevict_cache *cache, int32_t layer, const
  * For every token and head x of 128 channels of q and k: y = x / sqrt(mean(x^2)
  * + eps) * weight, then each pair (a, b) of channels turns by the angle t =
  * position * inv_freq[pair] into (a cos t - b sin t, b cos t + a sin t). fp32
- * throughout (the angle is reduced exactly), rounded to bf16 once. v is copied.
+ * throughout, rounded to bf16 once; the angle is reduced in integers, within
+ * about 2^-64 turns per position, and rounded to fp32 after that. v is copied.
  *  q, k, v     bf16 [batch][n_tokens] tokens of [Hq] or [Hkv][head_dim], device;
  *              consecutive tokens lie q_stride (k_stride, v_stride) elements
  *              apart: a multiple of 8, at least the heads' own length (so the
  *              three can be parts of one fused projection). v may be NULL.
- *  positions   int64 [batch][n_tokens], device, any value (accurate to fp32
- *              below 2^37), or NULL: the layer's length on the device as the
- *              call runs, onwards (graph replays advance with it).
+ *  positions   int64 [batch][n_tokens], device, any value (at 2^37 the angle
+ *              is off by 2^-27 turns, 4.7e-8 rad), or NULL: the layer's length on
+ *              the device as the call runs, onwards (graph replays advance with
+ *              it).
  *  q_weight, k_weight  bf16 [head_dim], device, or NULL: no norm of q (of k).
  *  eps         finite, >= 0.
  *  inv_freq    fp32 [head_dim / 2], device, finite: radians per position.

@@ -13,9 +13,9 @@ constexpr int kRopeRows = 16;     // heads of one token per warp
 
 // inv_freq / (2 pi) turns per position as a fraction of 2^64, in integers: with
 // inv_freq = m 2^(E - 150), m * round(2^66 / (2 pi)) * 2^(E - 152) mod 2^64. The
-// product with a 64-bit position then wraps at whole turns exactly, so a far
-// position loses nothing (the fraction's own error, 2^-64 turns per position,
-// is below fp32's at any position under 2^37).
+// product with a 64-bit position then wraps at whole turns exactly; what is left
+// of an error is the fraction's own, about 2^-64 turns per position (2^-27
+// turns, 4.7e-8 rad, at position 2^37).
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
     const uint32_t u = __float_as_uint(f);
     const int E = max(1, (int)((u >> 23) & 0xff));
@@ -79,10 +79,11 @@ __global__ void __launch_bounds__(32) rope_kernel(const RopeArgs a, const int32_
                                         : (int64_t)ctr[(tok / a.n_tokens) * ctr_stride + CTR_LEN] + tok % a.n_tokens;
         const float2 f = *reinterpret_cast<const float2 *>(a.inv_freq + 2 * lane);
         float c0, s0, c1, s1;
-        const int32_t t0 = (int32_t)(((uint64_t)pos * turn_fraction(f.x)) >> 32);
-        const int32_t t1 = (int32_t)(((uint64_t)pos * turn_fraction(f.y)) >> 32);
-        sincospif((float)t0 * 0x1p-31f, &s0, &c0);
-        sincospif((float)t1 * 0x1p-31f, &s1, &c1);
+        const int64_t t0 = (int64_t)((uint64_t)pos * turn_fraction(f.x));
+        const int64_t t1 = (int64_t)((uint64_t)pos * turn_fraction(f.y));
+        // all 64 bits, so that a small angle keeps fp32's relative accuracy
+        sincospif((float)t0 * 0x1p-63f, &s0, &c0);
+        sincospif((float)t1 * 0x1p-63f, &s1, &c1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // half-split: pairs 8 l + 2 j, + 1; interleaved: pairs 4 l + .. of the low half, 32 + 4 l + .. of the high
