@@ -400,7 +400,11 @@ qevict_status qevict_qk_norm_rope(qevict_cache *cache, int32_t layer, const void
  * (later keys, keys before its span, rows at or past kv_len; NaN and infinities
  * too) never reaches that query's row.
  * out and lse must not overlap each other or an input (INVALID_ARG). n_q and
- * n_kv are in [1, 2^29]. */
+ * n_kv are in [1, 2^29].
+ * Waits inside the kernel are for its own copies and products and have a limit
+ * of about two seconds, which qevict_set_wait_limit does not change; one that
+ * runs out sets QEVICT_ERR_TIMEOUT in the status word, and out and lse are then
+ * not valid. The kernel ends in any case. */
 qevict_status qevict_span_attention(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
                                     const void *v, int32_t n_kv, const int32_t *q_len, const int32_t *kv_len,
                                     int32_t span, int32_t sinks, void *out, float *lse, void *stream);
@@ -417,7 +421,8 @@ qevict_status qevict_span_attention(qevict_cache *cache, int32_t layer, const vo
  *          past kv_len); with per-head tiers [batch * Hkv][ceil(n_kv / window)],
  *          the mean over the G query heads of each KV head.
  * Sums are fp32 in a fixed order: every call gives the same scores. scores must
- * not overlap an input (INVALID_ARG). */
+ * not overlap an input (INVALID_ARG). Waits as in qevict_span_attention: after a
+ * TIMEOUT the scores are not valid. */
 qevict_status qevict_span_scores(qevict_cache *cache, int32_t layer, const void *q, int32_t n_q, const void *k,
                                  int32_t n_kv, const int32_t *q_len, const int32_t *kv_len, int32_t span,
                                  int32_t sinks, const float *lse, float *scores, void *stream);

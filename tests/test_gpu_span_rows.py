@@ -224,3 +224,30 @@ def test_window_of_infinite_keys_scores_zero(G, per_head):
     ref = U.scores(f64(q), f64(clean), f64(lse), [n], [n], 0, 0, w, per_head)
     assert np.all(np.abs(f64(got) - ref) <= 1e-5 * ref + 1e-9)
     assert cache.status() == 0, cache.last_error()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n_q,n_kv", [
+    (1, 4, 2, 1, 1), (1, 4, 2, 1, 200), (1, 4, 2, 1, 300), (2, 8, 8, 3, 4000), (1, 7, 1, 40, 900),    # split
+    (4, 16, 16, 600, 600), (3, 28, 4, 1000, 1000), (8, 8, 8, 2048, 2048)])                            # wide
+@pytest.mark.parametrize("lengths", ["all", "none", "no keys", "some"])
+def test_calls_end_with_their_last_copies_and_products(B, Hq, Hkv, n_q, n_kv, lengths):
+    """Before a CTA ends it waits for the copies and products that are under way, with a limit of about two
+    seconds; one that waits for something that never comes would take those."""
+    q, k = torch.randn(B, n_q, Hq, D).bfloat16().cuda(), torch.randn(B, n_kv, Hkv, D).bfloat16().cuda()
+    some = [0 if b % 2 else 1 + b for b in range(B)]
+    lens = {"all": {}, "none": dict(q_len=[0] * B), "no keys": dict(kv_len=[0] * B),
+            "some": dict(q_len=[min(n_q, s * 37) for s in some], kv_len=[min(n_kv, s * 150) for s in some])}[lengths]
+    lens = {x: torch.tensor(y, dtype=torch.int32).cuda() for x, y in lens.items()}
+    cache = cache_for(B, Hq, Hkv)
+    out, lse = torch.zeros_like(q), torch.zeros(B, Hq, n_q, device="cuda")
+    scores = torch.zeros(B, -(-n_kv // 64), device="cuda")
+    for _ in range(2):
+        at = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+        at[0].record()
+        cache.span_attention(0, q, k, k, out=out, lse=lse, **lens)
+        at[1].record()
+        cache.span_scores(0, q, k, lse, out=scores, **lens)
+        at[2].record()
+        torch.cuda.synchronize()
+    assert at[0].elapsed_time(at[1]) < 250 and at[1].elapsed_time(at[2]) < 250
+    assert cache.status() == 0, cache.last_error()

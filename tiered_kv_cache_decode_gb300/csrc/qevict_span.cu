@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     constexpr int QT = SPLIT ? 1 : 2;              // query tiles of the CTA
     constexpr int NS = kAttSlots - QT;             // ring slots
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * NS + 15];
+    __shared__ uint64_t bars[2 * NS + 16];
     __shared__ uint4 ticket;                       // wide: the answer to the copy thread's last request
     __shared__ AttUnit given[2];                   // wide: units that the copy thread has worked out
     __shared__ uint32_t slot;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t q_full = bar0 + 8 * (2 * NS + 4), q_empty = bar0 + 8 * (2 * NS + 9);
     auto u_full = [&](int x) { return bar0 + 8 * (2 * NS + 10 + x); };
     auto u_empty = [&](int x) { return bar0 + 8 * (2 * NS + 12 + x); };
-    const uint32_t asked = bar0 + 8 * (2 * NS + 14);
+    const uint32_t asked = bar0 + 8 * (2 * NS + 14), drained = asked + 8;
     // The ring holds key and value tiles in the order in which the products use them: K0 V0 K1 V1 ..,
     // split K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1). The copy thread's loads, of a unit's query tiles
     // and of its item x as the i-th of the ring:
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     };
     if (tid == 9 * 32) {
         // p_full: the group's four warps; u_empty: the product warp and both groups' warps
-        for (int i = 0; i < 2 * NS + 15; ++i) {
+        for (int i = 0; i < 2 * NS + 16; ++i) {
             const int x = i - 2 * NS;
             tc_mbar_init(bar0 + 8 * i, x == 12 || x == 13 ? 9 : x >= 5 && x < 9 ? 4 : 1);
         }
@@ -316,13 +316,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     load_item(x, i);
                 }
             }
-            if (!ok) {   // gave up: the copies in flight land before the CTA ends
-                const long long t0 = clock64();
-                while (q > 0 && !tc_try_wait(q_full, (q - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
-                for (int o = max(0, i - NS); o < i; ++o)
-                    while (!tc_try_wait(full(o % NS), (o / NS) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
-                while (asks > 0 && !tc_try_wait(asked, (asks - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
-            }
+            // The copies in flight land before the CTA ends, whichever role gave up, now or later.
+            const long long t0 = clock64();
+            while (q > 0 && !tc_try_wait(q_full, (q - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+            for (int o = max(0, i - NS); o < i; ++o)
+                while (!tc_try_wait(full(o % NS), (o / NS) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+            while (asks > 0 && !tc_try_wait(asked, (asks - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
         }
         if (warp == 8) {   // the whole warp keeps step, one lane issues
             const bool lead = tc_elect();
@@ -402,10 +401,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (!ok) break;
                 tiles += n;
             }
-            if (!ok) {   // gave up: products in flight (microseconds at most) end before the tensor memory is freed
-                const long long t0 = clock64();
-                while (clock64() - t0 < 1000000) {}
-            }
+            // The products in flight end before the tensor memory is freed, whichever role gave up.
+            if (lead) tc_commit(drained);
+            __syncwarp();
+            const long long t0 = clock64();
+            while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
         }
         __syncwarp();
         if (SPLIT) {
@@ -850,14 +850,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     ++nq;
                 }
             }
-            if (!ok) {   // gave up: the copies in flight land before the CTA ends
-                const long long t0 = clock64();
-                for (int o = max(0, nk - kScK); o < nk; ++o)
-                    while (!tc_try_wait(k_full(o % kScK), (o / kScK) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
-                for (int o = max(0, nq - kScQ); o < nq; ++o)
-                    while (!tc_try_wait(q_full(o % kScQ), (o / kScQ) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
-                while (asks > 0 && !tc_try_wait(asked, (asks - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
-            }
+            // The copies in flight land before the CTA ends, whichever role gave up, now or later.
+            const long long t0 = clock64();
+            for (int o = max(0, nk - kScK); o < nk; ++o)
+                while (!tc_try_wait(k_full(o % kScK), (o / kScK) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+            for (int o = max(0, nq - kScQ); o < nq; ++o)
+                while (!tc_try_wait(q_full(o % kScQ), (o / kScQ) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
+            while (asks > 0 && !tc_try_wait(asked, (asks - 1) & 1) && clock64() - t0 < kDefaultWaitCycles) {}
         }
         __syncwarp();
     } else if (warp == 16) {
@@ -888,11 +887,11 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 sp ^= buf == 0;
             }
         }
-        if (!ok) {   // gave up: the products in flight end before the tensor memory is freed
-            if (lead) tc_commit(drained);
-            const long long t0 = clock64();
-            while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
-        }
+        // The products in flight end before the tensor memory is freed, whichever role gave up.
+        if (lead) tc_commit(drained);
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!tc_try_wait(drained, 0) && clock64() - t0 < kDefaultWaitCycles) {}
         __syncwarp();
     } else {
         const int t = warp >> 3, x = (warp >> 2) & 1, r = tid & 127;
