@@ -446,7 +446,7 @@ class TieredCache:
         return torch.empty(shape, dtype=dtype, device=like.device)
 
     def _raw_stream(self, stream):
-        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device)
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
 
     def qk_norm_rope(self, layer, q, k, inv_freq, v=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, q_out=None, k_out=None, v_out=None, stream=None):
