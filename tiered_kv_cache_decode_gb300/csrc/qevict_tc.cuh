@@ -111,6 +111,13 @@ __host__ __device__ constexpr uint32_t tc_idesc(bool b_mn, uint32_t n = 128) {
 // barriers and hold the same operands): the operands then come out of uniform
 // registers, and an issue keeps ahead of the 64 cycles that a 128 x 128 x 16
 // product takes (from a branch of one thread an issue took 80 to 97 cycles).
+// Keeping step is also a condition of correctness. All lanes of the issuing warp wait
+// for the same barriers (each polls, then a vote over the whole warp); the issue is
+// a plain branch on the flag that tc_elect gave, with nothing between the wait and it
+// that only some lanes run; a __syncwarp follows it. The operands lie in registers that
+// the warp shares: forms in which lanes could run ahead (the elected lane polling for the
+// others; lanes polling unlike barriers, the instruction itself predicated) ended in an
+// illegal memory access.
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
