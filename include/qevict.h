@@ -398,7 +398,10 @@ qevict_status qevict_qk_norm_rope(qevict_cache *cache, int32_t layer, const void
  * A query that sees no key (p < 0) gets out 0 and lse -inf. Rows at or past
  * q_len[b] are not written. What a key or value that a query does not see holds
  * (later keys, keys before its span, rows at or past kv_len; NaN and infinities
- * too) never reaches that query's row.
+ * too) never reaches that query's row: calls that differ in nothing that a row
+ * sees, nor in the lengths, give it the same bits. A visible value that is
+ * infinite or NaN makes its channel so (an infinity whose probability rounds to
+ * 0: itself or NaN, the same in every call).
  * out and lse must not overlap each other or an input (INVALID_ARG). n_q and
  * n_kv are in [1, 2^29].
  * Waits inside the kernel are for its own copies and products and have a limit

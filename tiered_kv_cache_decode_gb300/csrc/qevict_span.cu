@@ -56,16 +56,21 @@ __device__ __forceinline__ int clamped(const int32_t *len, int b, int n) {
 // CTA goes on with units of CTAs that have not started. Bound by the products and by
 // the chain between them: a group's loads, maximum, exponentials (at 32 a cycle and
 // SM half as long as the tile's products) and stores take a little longer than the
-// other group's two products; 32 query heads on 8: a prompt of 8K 322 us
-// (1,710 TFLOP/s; the tensor pipe active 73 % of the cycles), of 32K 5.0 to 5.3 ms
-// (1,660 to 1,760; the clock falls under the power limit), four of 8K with
-// a span of 4K 1.03 ms (1,600: some of its tiles are half masked).
+// other group's two products; 32 query heads on 8: a prompt of 8K 326 us
+// (1,690 TFLOP/s; the tensor pipe active 74 % of the cycles), of 32K 5.05 to 5.35 ms
+// (1,645 to 1,740; the clock falls under the power limit), four of 8K with
+// a span of 4K 1.04 ms (1,585: some of its tiles are half masked).
 // Split: both take one query tile, every other key tile each, and the key tiles
 // are further divided over the CTAs of a cluster; the partial (max, sum, O)
 // meet in shared memory. No scratch in device memory either way. Single tokens
 // are bound by the keys and values: 8 sequences of 26K to 32K 146 us (6.6 TB/s);
 // 16 with a span of 4K 27 us (5.0 TB/s: the first copies and the meeting, about
 // 5 us, do not overlap the stream).
+//
+// Probabilities are rounded to bf16 for P V: a product takes both operands in one
+// type, and a second one for what the rounding leaves off would double P V, half of the
+// tensor work here. Each is off by half a step, 2^-8 of itself, at most; their sum is taken
+// before it, in fp32. Exponentials are the hardware's, off by 2^-22.
 constexpr int kSoftmax = 256;                 // threads of the two softmax groups
 constexpr int kAttThreads = kSoftmax + 128;   // and a group of four warps for copies and products
 constexpr int kAttSlots = 7;                  // 32 KB slots of shared memory: query tiles, then the key/value ring
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // group then reading every step: 241 us at 8K and 130 us for 64 queries of 8 x 32K.
 // Groups of half a tile's keys, which give their half back before the exponentials:
 // 238 and 127 us. A product of its own for each tile: 203 and 117 us.)
-// 32 query heads on 8: every query of 8K 200 us (1,375 TFLOP/s), 64 queries of
+// 32 query heads on 8: every query of 8K 199 us (1,380 TFLOP/s), 64 queries of
 // 8 x 32K 116 us (1,180 TFLOP/s and 4.65 TB/s). Bound by the way round a logit
 // buffer: product, load, half of the exponentials, release (about 1,600 cycles a step,
 // the products of which take 1,024, as its exponentials do at 32 a cycle and SM).
