@@ -658,6 +658,150 @@ qevict_status qevict_decode_attention_static_scratch(qevict_cache *cache, int32_
                                                      float *out, float *mass, int32_t accumulate_scores,
                                                      void *stream);
 
+/* ---- the cache in 8 bits ---------------------------------------------------
+ * Every token of ragged sequences kept, in 8 bits: beside the tiered cache (one
+ * length, windows in tiers) and attention over uncompressed keys, for layers
+ * whose tokens are not routed, and for token-level eviction by accumulated
+ * attention (QEvict "Cumulatieve Scoring" with tokens in the windows' place).
+ *
+ * A block is 64 tokens of one KV head. A full block holds its keys as codes c
+ * and one fp32 scale s, its values likewise: s = fl32(max|x| / 127) and c =
+ * fl32(x / s) rounded to the nearest integer, ties to even (INT8), or s =
+ * fl32(max|x| / 448) and c = fl32(x / s) rounded to e4m3 likewise; s = 0: codes
+ * 0. It stands for fl32(c s). It is quantised once, when its last token comes;
+ * the tokens of a block that is not full are bf16 as given.
+ *
+ * Lengths are the caller's: each call takes the positions it works on from the
+ * caller's device memory (so a replayed graph follows them), and the layers of
+ * a model can share them. A sequence may be set back by passing a smaller start
+ * or length: exact down to the first token of the last full block (its rows,
+ * too, are kept as bf16), as for drafted tokens that are rejected, but not behind
+ * an eviction.
+ *
+ * Conventions, errors and status word are those of the other calls. Calls on one
+ * layer are ordered; attention calls of one handle share its scratch, so they
+ * must not overlap one another, also not in replayed graphs (two handles may).
+ * The handle's device must be current (INVALID_ARG otherwise). */
+#define QEVICT_BLOCK_TOKENS 64
+#define QEVICT_BLOCK_MAX_QUERIES 8
+enum { QEVICT_BLOCK_INT8 = 0, QEVICT_BLOCK_E4M3 = 1 };
+
+/*  num_q_heads   a multiple of num_kv_heads, at most 8 per KV head.
+ *  head_dim      must be 128.
+ *  capacity      tokens per sequence, in [1, 2^24]; rounded up to a multiple of
+ *                64 (qevict_block_capacity gives it back).
+ *  format        QEVICT_BLOCK_INT8 or QEVICT_BLOCK_E4M3.
+ *  score_queries 0 to 8: the most queries per sequence of an attention call that
+ *                asks for weights (4 bytes of scratch per query, query head and
+ *                token of the batch, one array for all layers). */
+typedef struct qevict_block_config {
+    int32_t batch;
+    int32_t num_layers;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t capacity;
+    int32_t format;
+    int32_t score_queries;
+} qevict_block_config;
+
+typedef struct qevict_block_cache qevict_block_cache;
+
+/* Allocate (through `allocator`, or cudaMalloc) on the current device, clear on
+ * `stream`, synchronise it. Errors as qevict_cache_create. Per layer and token of
+ * capacity 256 bytes per KV head, and 64 KiB per (sequence, KV head). */
+qevict_status qevict_block_create(const qevict_block_config *config, const qevict_allocator *allocator, void *stream,
+                                  qevict_block_cache **out);
+
+/* Synchronise the device's work on the handle's creation stream, free everything. */
+qevict_status qevict_block_destroy(qevict_block_cache *cache);
+
+/* The capacity in tokens (a multiple of 64), or -1 for NULL. */
+int32_t qevict_block_capacity(const qevict_block_cache *cache);
+
+/* Tokens into the cache: token i < n_new[b] of sequence b at position start[b] + i.
+ *  k, v     bf16 [batch][n] tokens of [Hkv][128], device, 16-byte aligned;
+ *           consecutive tokens lie k_stride (v_stride) elements apart: a multiple
+ *           of 8, at least the heads' own length.
+ *  start    int32 [batch], device, or NULL: 0. n_new likewise, or NULL: n; clamped
+ *           to [0, n].
+ *  weights  fp32 [batch][Hkv][capacity], device, or NULL: 0 is written for the
+ *           new tokens.
+ * What a sequence holds before start[b] has to be there; what it held from there
+ * on is replaced. On the device: a negative start sets INVALID_ARG, and the
+ * sequence is left as it was; positions past the capacity set CAPACITY, and their
+ * tokens are dropped; a value that is infinite or NaN sets DEVICE, and is stored as
+ * 0 (so nothing in the cache is either). */
+qevict_status qevict_block_append(qevict_block_cache *cache, int32_t layer, const void *k, int64_t k_stride,
+                                  const void *v, int64_t v_stride, int32_t n, const int32_t *start,
+                                  const int32_t *n_new, float *weights, void *stream);
+
+/* Attention of the last n_q positions over the cache: query i of sequence b sits
+ * at p = kv_len[b] - n_q + i and sees the tokens j <= p.
+ *  q        bf16 [batch][n_q][Hq][128], device, 16-byte aligned, n_q in [1, 8] (longer
+ *           ones: qevict_block_read and qevict_span_attention).
+ *  kv_len   int32 [batch], device; clamped to [0, capacity].
+ *  out      bf16 [batch][n_q][Hq][128], 16-byte aligned: softmax(q K^T / sqrt(128)) V
+ *           over what the cache stands for. fp32 sums; probabilities enter their
+ *           product with the codes as fp16 (relative to the largest of their block
+ *           so far), with bf16 rows as two bf16 parts.
+ *  lse      fp32 [batch][Hq][n_q] or NULL: log(sum(exp(q K^T / sqrt(128)))).
+ *  weights  fp32 [batch][Hkv][capacity] or NULL: token j < kv_len[b] gets the sum
+ *           over the queries of the mean over the head's Hq / Hkv query heads of
+ *           its probabilities, added (accumulate nonzero) or written; others are
+ *           left as they were. Needs score_queries >= n_q (INVALID_ARG).
+ * A query that sees no token gets out 0, lse -inf, and gives no weight. Sums run in a
+ * fixed order: every call gives the same bits. out, lse and weights must not
+ * overlap one another or an input (INVALID_ARG). Waits are for the kernel's own
+ * copies, as in qevict_span_attention. */
+qevict_status qevict_block_attention(qevict_block_cache *cache, int32_t layer, const void *q, int32_t n_q,
+                                     const int32_t *kv_len, void *out, float *lse, float *weights,
+                                     int32_t accumulate, void *stream);
+
+/* What the cache stands for, as bf16 (fl32(c s) rounded once; rows of the open block
+ * as they are): row i of sequence b is the token at position first[b] + i.
+ *  kv_len   int32 [batch], device; rows at positions outside [0, kv_len[b]) are left
+ *           as they were.
+ *  first    int32 [batch], device, or NULL: 0.
+ *  k, v     bf16 [batch][n][Hkv][128], device, 16-byte aligned, written; either may
+ *           not overlap the other or an input. */
+qevict_status qevict_block_read(qevict_block_cache *cache, int32_t layer, const int32_t *kv_len, const int32_t *first,
+                                int32_t n, void *k, void *v, void *stream);
+
+/* Eviction by accumulated weight. Of the c = 64 floor(kv_len / 64) tokens in full
+ * blocks of a (sequence, KV head): all stay where c <= keep; else the last `recent`
+ * of them and the keep - recent others of the largest weight (NaN below every
+ * number; equal weights: the lower position), in order of position, requantised in
+ * blocks of 64 from what they stand for. The tokens of the open block stay behind
+ * them. Each KV head keeps tokens of its own.
+ *  to, to_layer  where they go: the cache and layer itself (in place; where nothing
+ *           leaves, nothing is touched), or another layer or handle of the same
+ *           batch, heads and format, whose layer is overwritten.
+ *  keep     a multiple of 64, at least 64; keep + 64 at most the destination's
+ *           capacity. recent in [0, keep].
+ *  weights  fp32 [batch][Hkv][capacity], device.
+ *  weights_out  fp32 [batch][Hkv][capacity of the destination], or NULL: the weights
+ *           of the tokens that stay, in their new places; places behind them are
+ *           left as they were. May be `weights` itself where the capacities agree.
+ *  new_len  int32 [batch], device, written: min(c, keep) + kv_len - c.
+ *  kept     int32 [batch][Hkv][keep], device, written: the old positions of the tokens
+ *           in full blocks, then -1.
+ * Outputs must not overlap one another or an input but weights (INVALID_ARG). */
+qevict_status qevict_block_evict(qevict_block_cache *cache, int32_t layer, const int32_t *kv_len, int32_t keep,
+                                 int32_t recent, const float *weights, qevict_block_cache *to, int32_t to_layer,
+                                 float *weights_out, int32_t *new_len, int32_t *kept, void *stream);
+
+/* A layer's full blocks, for inspection: codes uint8 [batch][Hkv][capacity / 64][K, V]
+ * [64 tokens][128], the 16-byte chunks of a token t's row at chunk ^ (t & 7), an INT8 code
+ * with 128 added; scales fp32 [batch][Hkv][capacity / 64][K, V]. Device pointers of the
+ * handle. Host call, no stream work. */
+qevict_status qevict_block_view(const qevict_block_cache *cache, int32_t layer, const void **codes,
+                                const float **scales);
+
+/* As qevict_get_status and qevict_clear_status. */
+qevict_status qevict_block_get_status(qevict_block_cache *cache, void *stream);
+qevict_status qevict_block_clear_status(qevict_block_cache *cache, void *stream);
+
 /* Thread-local text of the last host-side error of this thread. */
 const char *qevict_last_error(void);
 

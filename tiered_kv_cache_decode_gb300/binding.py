@@ -32,6 +32,9 @@ EXPORTS = ["qevict_pool_capacity", "qevict_cache_create", "qevict_cache_destroy"
            "qevict_get_tier_move_counts", "qevict_future_missed_mass", "qevict_route_global", "qevict_route_logsparse", "qevict_route_rd",
            "qevict_route_rd_mixed", "qevict_k_channel_weights", "qevict_route_rd_kv",
            "qevict_qk_norm_rope", "qevict_span_attention", "qevict_span_scores",
+           "qevict_block_create", "qevict_block_destroy", "qevict_block_capacity", "qevict_block_append",
+           "qevict_block_attention", "qevict_block_read", "qevict_block_evict", "qevict_block_view",
+           "qevict_block_get_status", "qevict_block_clear_status",
            "qevict_length",
            "qevict_last_error"]
 
@@ -81,6 +84,14 @@ class Stats(ctypes.Structure):
                 ("ledger_reuses", ctypes.c_uint64), ("device_bytes", ctypes.c_int64)]
 
 
+class BlockConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "num_layers", "num_q_heads", "num_kv_heads", "head_dim",
+                                              "capacity", "format", "score_queries")]
+
+
+BLOCK_TOKENS = 64
+BLOCK_FORMATS = {"int8": 0, "e4m3": 1}
+
 _lib = None
 
 
@@ -128,6 +139,16 @@ def load() -> ctypes.CDLL:
         "qevict_span_attention": [P, I32, P, I32, P, P, I32, P, P, I32, I32, P, P, P],
         "qevict_span_scores": [P, I32, P, I32, P, I32, P, P, I32, I32, P, P, P],
         "qevict_future_missed_mass": [P, I32, P, P, I64, P, P],
+        "qevict_block_create": [ctypes.POINTER(BlockConfig), ctypes.POINTER(Allocator), P, ctypes.POINTER(P)],
+        "qevict_block_destroy": [P],
+        "qevict_block_capacity": [P],
+        "qevict_block_append": [P, I32, P, I64, P, I64, I32, P, P, P, P],
+        "qevict_block_attention": [P, I32, P, I32, P, P, P, P, I32, P],
+        "qevict_block_read": [P, I32, P, P, I32, P, P, P],
+        "qevict_block_evict": [P, I32, P, I32, I32, P, P, I32, P, P, P, P],
+        "qevict_block_view": [P, I32, ctypes.POINTER(P), ctypes.POINTER(P)],
+        "qevict_block_get_status": [P, P],
+        "qevict_block_clear_status": [P, P],
         "qevict_length": [P, I32],
         "qevict_last_error": [],
     }
@@ -172,7 +193,82 @@ def device_tensor(ptr: int, shape, typestr: str) -> torch.Tensor:
     return torch.as_tensor(_DeviceArray(ptr, shape, typestr), device="cuda")
 
 
-class TieredCache:
+class _Handle:
+    """What the caches' classes share: their handle on the library and the checks of their calls' tensors."""
+
+    def _check(self, rc):
+        if rc != 0:
+            raise QevictError(rc, self.lib.qevict_last_error().decode())
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _torch_allocator(self):
+        """Allocator callbacks that draw on torch's caching allocator (kept alive by the handle)."""
+        dev = self.device
+
+        def _a(size, stream, ctx):
+            try:
+                return torch.cuda.caching_allocator_alloc(int(size), dev, stream or 0)
+            except Exception:
+                return None
+
+        def _f(ptr, stream, ctx):
+            torch.cuda.caching_allocator_delete(ptr)
+
+        return Allocator(ALLOC_FN(_a), FREE_FN(_f), None)
+
+    # These run once per layer and token, so their checks read each attribute once.
+    def _tokens(self, t, heads, what):
+        """(tokens, elements between consecutive tokens) of a bf16 [B][n][heads][128] (or, for one token,
+        [B][heads][128]) tensor on the cache's device whose tokens are evenly spaced and dense inside."""
+        sh, st, B = t.shape, t.stride(), self.B
+        if len(sh) == 3:
+            sh, st = (sh[0], 1, sh[1], sh[2]), (st[0], st[0], st[1], st[2])
+        if len(sh) != 4 or sh[0] != B or sh[2] != heads or sh[3] != HEAD_DIM or t.dtype is not torch.bfloat16 or \
+                t.device != self._dev:
+            raise ValueError(f"{what} must be bfloat16 [{B}][n][{heads}][{HEAD_DIM}] on {self._dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        n = sh[1]
+        dense = heads * HEAD_DIM
+        step = st[1] if n > 1 else st[0] if B > 1 else dense
+        if st[3] != 1 or (heads > 1 and st[2] != HEAD_DIM) or (B > 1 and st[0] != n * step):
+            raise ValueError(f"{what}: tokens must be evenly spaced, with dense heads (strides {t.stride()})")
+        return n, step
+
+    def _dense(self, t, heads, what):
+        n, step = self._tokens(t, heads, what)
+        if step != heads * HEAD_DIM:
+            raise ValueError(f"{what} must be dense (strides {t.stride()})")
+        return n
+
+    def _side(self, t, shape, dtype, what):
+        """Address of a dense tensor of the given shape and type on the cache's device, or None."""
+        if t is None:
+            return None
+        if t.shape != shape or t.dtype is not dtype or t.device != self._dev or not t.is_contiguous():
+            raise ValueError(f"{what} must be dense {dtype} {list(shape)} on {self._dev}, got {t.dtype} "
+                             f"{list(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    @staticmethod
+    def _new(like, stream, dtype=None, shape=None, make=torch.empty):
+        """A dense tensor like `like`, from the memory of the stream that writes it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return _Handle._new(like, None, dtype, shape, make)
+        if shape is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return make(shape, dtype=dtype, device=like.device)
+
+    def _raw_stream(self, stream):
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
+
+class TieredCache(_Handle):
     """A multi-layer tiered KV cache living on the current CUDA device."""
 
     def __init__(self, batch, num_layers, num_q_heads, num_kv_heads, window, max_context,
@@ -191,20 +287,7 @@ class TieredCache:
         self.layers = num_layers
         self.device = torch.cuda.current_device()
         self._dev = torch.device("cuda", self.device)
-        self._alloc = None
-        if torch_allocator:
-            dev = self.device
-
-            def _a(size, stream, ctx):
-                try:
-                    return torch.cuda.caching_allocator_alloc(int(size), dev, stream or 0)
-                except Exception:
-                    return None
-
-            def _f(ptr, stream, ctx):
-                torch.cuda.caching_allocator_delete(ptr)
-
-            self._alloc = Allocator(ALLOC_FN(_a), FREE_FN(_f), None)
+        self._alloc = self._torch_allocator() if torch_allocator else None
         self.handle = ctypes.c_void_p()
         rc = self.lib.qevict_cache_create(ctypes.byref(self.cfg),
                                           ctypes.byref(self._alloc) if self._alloc else None,
@@ -212,20 +295,10 @@ class TieredCache:
         self._check(rc)
 
     # ---- plumbing ----------------------------------------------------------
-    def _check(self, rc):
-        if rc != 0:
-            raise QevictError(rc, self.lib.qevict_last_error().decode())
-
     def close(self):
         if self.handle:
             self._check(self.lib.qevict_cache_destroy(self.handle))
             self.handle = ctypes.c_void_p()
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
 
     def set_launch_overlap(self, enable=True):
         self._check(self.lib.qevict_set_launch_overlap(self.handle, 1 if enable else 0))
@@ -402,52 +475,6 @@ class TieredCache:
         return device_tensor(v.k_group_bits, (v.batch, v.num_kv_heads, 4), "|u1").cpu()
 
     # ---- from projections to the cache ------------------------------------------
-    # These run once per layer and token, so their checks read each attribute once.
-    def _tokens(self, t, heads, what):
-        """(tokens, elements between consecutive tokens) of a bf16 [B][n][heads][128] (or, for one token,
-        [B][heads][128]) tensor on the cache's device whose tokens are evenly spaced and dense inside."""
-        sh, st, B = t.shape, t.stride(), self.B
-        if len(sh) == 3:
-            sh, st = (sh[0], 1, sh[1], sh[2]), (st[0], st[0], st[1], st[2])
-        if len(sh) != 4 or sh[0] != B or sh[2] != heads or sh[3] != HEAD_DIM or t.dtype is not torch.bfloat16 or \
-                t.device != self._dev:
-            raise ValueError(f"{what} must be bfloat16 [{B}][n][{heads}][{HEAD_DIM}] on {self._dev}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        n = sh[1]
-        dense = heads * HEAD_DIM
-        step = st[1] if n > 1 else st[0] if B > 1 else dense
-        if st[3] != 1 or (heads > 1 and st[2] != HEAD_DIM) or (B > 1 and st[0] != n * step):
-            raise ValueError(f"{what}: tokens must be evenly spaced, with dense heads (strides {t.stride()})")
-        return n, step
-
-    def _dense(self, t, heads, what):
-        n, step = self._tokens(t, heads, what)
-        if step != heads * HEAD_DIM:
-            raise ValueError(f"{what} must be dense (strides {t.stride()})")
-        return n
-
-    def _side(self, t, shape, dtype, what):
-        """Address of a dense tensor of the given shape and type on the cache's device, or None."""
-        if t is None:
-            return None
-        if t.shape != shape or t.dtype is not dtype or t.device != self._dev or not t.is_contiguous():
-            raise ValueError(f"{what} must be dense {dtype} {list(shape)} on {self._dev}, got {t.dtype} "
-                             f"{list(t.shape)} on {t.device}")
-        return t.data_ptr()
-
-    @staticmethod
-    def _new(like, stream, dtype=None, shape=None):
-        """A dense tensor like `like`, from the memory of the stream that writes it."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return TieredCache._new(like, None, dtype, shape)
-        if shape is None:
-            return torch.empty_like(like, memory_format=torch.contiguous_format)
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-    def _raw_stream(self, stream):
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
-
     def qk_norm_rope(self, layer, q, k, inv_freq, v=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, q_out=None, k_out=None, v_out=None, stream=None):
         """Head norms and rotation of q [B][n][Hq][128] and k [B][n][Hkv][128] (and a dense copy of v), which
@@ -540,6 +567,134 @@ class TieredCache:
         """uint8 [units][W]: width of each window's ledger entry (0 none, 2, 4, 8), host copy."""
         v = self.view(layer)
         return device_tensor(v.ledger_bits, (v.batch, v.max_windows), "|u1")[:, :v.num_windows].cpu()
+
+
+class BlockCache(_Handle):
+    """Every token of ragged sequences in 8 bits, with a scale for each block of 64 tokens and KV head, on the
+    current CUDA device. Lengths and weights are the caller's tensors: int32 [B], fp32 [B][Hkv][capacity]."""
+
+    def __init__(self, batch, num_layers, num_q_heads, num_kv_heads, capacity, fmt="int8", score_queries=1,
+                 head_dim=HEAD_DIM, torch_allocator=True):
+        """fmt: "int8" or "e4m3". score_queries: the most queries of an attend() that asks for weights."""
+        self.lib = load()
+        if fmt not in BLOCK_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(BLOCK_FORMATS)}, got {fmt!r}")
+        self.cfg = BlockConfig(batch, num_layers, num_q_heads, num_kv_heads, head_dim, capacity, BLOCK_FORMATS[fmt],
+                               score_queries)
+        self.B, self.Hq, self.Hkv, self.fmt, self.layers = batch, num_q_heads, num_kv_heads, fmt, num_layers
+        self.handle = ctypes.c_void_p()
+        self.device = torch.cuda.current_device()
+        self._dev = torch.device("cuda", self.device)
+        self._alloc = self._torch_allocator() if torch_allocator else None
+        self._check(self.lib.qevict_block_create(ctypes.byref(self.cfg),
+                                                 ctypes.byref(self._alloc) if self._alloc else None, _stream(),
+                                                 ctypes.byref(self.handle)))
+        self.capacity = int(self.lib.qevict_block_capacity(self.handle))
+        self._per_seq, self._per_token = (batch,), (batch, num_kv_heads, self.capacity)
+
+    def close(self):
+        if self.handle:
+            self._check(self.lib.qevict_block_destroy(self.handle))
+            self.handle = ctypes.c_void_p()
+
+    def append(self, layer, k, v, start=None, n_new=None, weights=None, stream=None):
+        """Tokens k, v [B][n][Hkv][128] (or [B][Hkv][128], one each; parts of a fused projection too) into positions
+        start[b] .. start[b] + n_new[b] - 1 (None: 0 and n); their weights, where given, become 0."""
+        n, ks = self._tokens(k, self.Hkv, "k")
+        nv, vs = self._tokens(v, self.Hkv, "v")
+        if nv != n:
+            raise ValueError(f"v must have k's {n} tokens, got {nv}")
+        side, i32 = self._side, torch.int32
+        rc = self.lib.qevict_block_append(
+            self.handle, layer, k.data_ptr(), ks, v.data_ptr(), vs, n, side(start, self._per_seq, i32, "start"),
+            side(n_new, self._per_seq, i32, "n_new"), side(weights, self._per_token, torch.float32, "weights"),
+            self._raw_stream(stream))
+        if rc:
+            self._check(rc)
+
+    def attend(self, layer, q, kv_len, out=None, lse=None, want_lse=True, weights=None, accumulate=True, stream=None):
+        """Attention of q [B][n_q][Hq][128] (or [B][Hq][128]), the last positions of kv_len [B] tokens, n_q <= 8.
+        Returns (out bf16, lse fp32 [B][Hq][n_q] or None). weights: each token's probabilities, summed over the
+        queries and averaged over the query heads of its KV head, are added (or written)."""
+        n_q = self._dense(q, self.Hq, "q")
+        if out is None:
+            out = self._new(q, stream)
+        if lse is None and want_lse:
+            lse = self._new(q, stream, torch.float32, (self.B, self.Hq, n_q))
+        side, f32 = self._side, torch.float32
+        rc = self.lib.qevict_block_attention(
+            self.handle, layer, q.data_ptr(), n_q, side(kv_len, self._per_seq, torch.int32, "kv_len"),
+            side(out, q.shape, torch.bfloat16, "out"), side(lse, (self.B, self.Hq, n_q), f32, "lse"),
+            side(weights, self._per_token, f32, "weights"), 1 if accumulate else 0, self._raw_stream(stream))
+        if rc:
+            self._check(rc)
+        return out, lse
+
+    def read(self, layer, kv_len, n, first=None, k_out=None, v_out=None, stream=None):
+        """(k, v) bf16 [B][n][Hkv][128]: what the cache holds at positions first[b] .. (None: 0 ..). Rows at positions
+        outside [0, kv_len[b]) are left as they were (0 in tensors made here)."""
+        shape, bf = (self.B, n, self.Hkv, HEAD_DIM), torch.bfloat16
+        side, i32 = self._side, torch.int32
+        at = side(kv_len, self._per_seq, i32, "kv_len")
+        if at is None:
+            raise ValueError("kv_len must be given")
+        if k_out is None:
+            k_out = self._new(kv_len, stream, bf, shape, torch.zeros)
+        if v_out is None:
+            v_out = self._new(kv_len, stream, bf, shape, torch.zeros)
+        rc = self.lib.qevict_block_read(self.handle, layer, at, side(first, self._per_seq, i32, "first"), n,
+                                        side(k_out, shape, bf, "k_out"), side(v_out, shape, bf, "v_out"),
+                                        self._raw_stream(stream))
+        if rc:
+            self._check(rc)
+        return k_out, v_out
+
+    def evict(self, layer, kv_len, keep, recent, weights, into=None, into_layer=0, new_len=None, kept=None,
+              weights_out=None, stream=None):
+        """Keep, of each (sequence, KV head)'s tokens in full blocks, the last `recent` and those of the largest
+        weights, `keep` (a multiple of 64) in all; in place, weights with them, or into layer `into_layer` of another
+        BlockCache. Returns (new_len int32 [B], kept int32 [B][Hkv][keep]: the old positions, then -1)."""
+        to = self if into is None else into
+        if into is None:
+            into_layer = layer
+            if weights_out is None:
+                weights_out = weights
+        side, i32, f32 = self._side, torch.int32, torch.float32
+        at, w = side(kv_len, self._per_seq, i32, "kv_len"), side(weights, self._per_token, f32, "weights")
+        if at is None or w is None:
+            raise ValueError("kv_len and weights must be given")
+        if new_len is None:
+            new_len = self._new(kv_len, stream, i32, self._per_seq)
+        if kept is None:
+            kept = self._new(kv_len, stream, i32, (self.B, self.Hkv, max(keep, 0)))
+        rc = self.lib.qevict_block_evict(
+            self.handle, layer, at, keep, recent, w, to.handle, into_layer,
+            side(weights_out, to._per_token, f32, "weights_out"), side(new_len, self._per_seq, i32, "new_len"),
+            side(kept, (self.B, self.Hkv, keep), i32, "kept"), self._raw_stream(stream))
+        if rc:
+            self._check(rc)
+        return new_len, kept
+
+    def blocks(self, layer):
+        """Host copies of a layer's full blocks: codes [B][Hkv][capacity / 64][K, V][64][128], int8 or float8_e4m3fn,
+        and scales fp32 [B][Hkv][capacity / 64][K, V]."""
+        c, s = ctypes.c_void_p(), ctypes.c_void_p()
+        self._check(self.lib.qevict_block_view(self.handle, layer, ctypes.byref(c), ctypes.byref(s)))
+        nb = self.capacity // BLOCK_TOKENS
+        raw = device_tensor(c.value, (self.B, self.Hkv, nb, 2, BLOCK_TOKENS, HEAD_DIM // 16, 16), "|u1").cpu()
+        t = torch.arange(BLOCK_TOKENS)[:, None]
+        raw = raw[:, :, :, :, t, torch.arange(HEAD_DIM // 16) ^ (t & 7)].flatten(-2)
+        codes = (raw.to(torch.int16) - 128).to(torch.int8) if self.fmt == "int8" else raw.view(torch.float8_e4m3fn)
+        return codes, device_tensor(s.value, (self.B, self.Hkv, nb, 2), "<f4").cpu()
+
+    def status(self, stream=None) -> int:
+        return int(self.lib.qevict_block_get_status(self.handle, _stream(stream)))
+
+    def last_error(self) -> str:
+        return self.lib.qevict_last_error().decode()
+
+    def clear_status(self, stream=None):
+        self._check(self.lib.qevict_block_clear_status(self.handle, _stream(stream)))
 
 
 def decode_kch_slot(raw: torch.Tensor, Hkv: int, w: int, bits: int, kgw):

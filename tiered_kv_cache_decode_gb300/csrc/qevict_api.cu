@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/qevict.h: configuration checks,
 // slot-pool sizing from the byte budget, device allocations, host-side error
 // reporting and the launch sequence of every call.
+#include "qevict_host.h"
 #include "qevict_internal.cuh"
 
 #include <math.h>
@@ -14,8 +15,10 @@
 using namespace qevict;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace qevict {
 
 qevict_status fail(qevict_status st, const char *fmt, ...) {
     char buf[512];
@@ -30,6 +33,10 @@ qevict_status fail(qevict_status st, const char *fmt, ...) {
 qevict_status cuda_fail(cudaError_t e, const char *what) {
     return fail(QEVICT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+}  // namespace qevict
+
+namespace {
 
 struct LayerHost {
     LayerDev dev{};
@@ -659,22 +666,6 @@ static cudaError_t encode_tokens(CUtensorMap *map, const void *base, int seqs, i
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-struct Extent {
-    const void *p;
-    int64_t bytes;
-    const char *what;
-};
-// An output must not overlap another operand: the kernels read and write in no fixed order.
-static qevict_status check_apart(const Extent &o, const Extent *others, int n) {
-    const uintptr_t o0 = (uintptr_t)o.p, o1 = o0 + o.bytes;
-    for (int i = 0; i < n && o.p; ++i) {
-        const uintptr_t s0 = (uintptr_t)others[i].p, s1 = s0 + others[i].bytes;
-        if (others[i].p && o0 < s1 && s0 < o1)
-            return fail(QEVICT_ERR_INVALID_ARG, "%s overlaps %s", o.what, others[i].what);
-    }
-    return QEVICT_OK;
 }
 
 static qevict_status check_span(const qevict_cache *c, const void *q, int32_t n_q, const void *k, int32_t n_kv,

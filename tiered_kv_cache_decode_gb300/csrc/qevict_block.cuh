@@ -1,0 +1,170 @@
+// The cache in 8 bits: its layout, the quantiser of a block and the launch entry
+// points of qevict_block.cu and qevict_block_attend.cu.
+#pragma once
+
+#include "qevict_div.cuh"
+#include "qevict_internal.cuh"
+
+namespace qevict {
+
+constexpr int kBlk = QEVICT_BLOCK_TOKENS;      // tokens that share a scale
+constexpr int kBlkBytes = 2 * kBlk * kHeadDim; // a block's codes of K, then of V
+constexpr int kOpenHalf = 32;                  // tokens of half an open block: as many bytes as a block's codes
+constexpr int kMaxBlkQueries = 8;
+constexpr int kMaxBlkCtas = 192;               // CTAs of an attention launch (152 SMs, one each)
+
+// A layer's memory. "pair" = sequence * Hkv + KV head.
+//  codes  [pair][NB][K, V][64 tokens][128 channels], a byte each. The eight
+//         16-byte chunks of a token's row lie at chunk ^ (token & 7), so that
+//         eight lanes that read one chunk of eight tokens, or two neighbouring
+//         tokens' alternate chunks, meet no shared-memory bank twice.
+//  scale  [pair][NB] (K, V)
+//  open   [pair][block & 1][token >> 5][K, V][32 tokens][128] bf16: the rows of the
+//         block that is not full, and of the one before it.
+struct BlockDev {
+    uint8_t *codes;
+    float2 *scale;
+    uint8_t *open;
+    int B, Hq, Hkv, G, NB, capacity, layer;
+    int32_t *status;   // [4] as CacheDev::status
+};
+
+__host__ __device__ inline int64_t blk_code_off(const BlockDev &D, int64_t pair, int block) {
+    return (pair * D.NB + block) * kBlkBytes;
+}
+// byte of chunk c (16 channels) of token t of a block's K codes (V: kBlkBytes / 2 further)
+__host__ __device__ inline int blk_chunk(int t, int c) { return t * kHeadDim + ((c ^ (t & 7)) << 4); }
+__host__ __device__ inline int64_t blk_open_off(int64_t pair, int block, int t) {
+    return ((pair * 2 + (block & 1)) * 2 + (t >> 5)) * kBlkBytes;
+}
+// byte of chunk c (8 channels) of token t & 31 of half an open block's K rows. Chunks c and
+// c + 8 of a row, 128 bytes apart, differ in bit 1 of their place, for the same reason.
+__host__ __device__ inline int blk_open_chunk(int t, int c) {
+    return (t & 31) * (2 * kHeadDim) + (((c & 8) | ((c & 7) ^ (t & 7) ^ ((c >> 3) << 1))) << 4);
+}
+
+struct BlockAppendArgs {
+    const __nv_bfloat16 *k, *v;      // token i of sequence b: (b * n + i) * stride elements on
+    int64_t k_stride, v_stride;
+    const int32_t *start, *n_new;    // [B] or NULL: 0, n
+    int n;
+    float *weights;                  // [pair][capacity] or NULL
+};
+struct BlockReadArgs {
+    const int32_t *kv_len, *first;   // [B]; first NULL: 0
+    int n;
+    __nv_bfloat16 *k, *v;            // [B][n][Hkv][128]
+};
+struct BlockEvictArgs {
+    const int32_t *kv_len;
+    int keep, recent;
+    const float *weights;            // [pair][capacity]
+    float *weights_out;              // [pair][the other cache's capacity] or NULL
+    int32_t *new_len, *kept;         // [B], [pair][keep]
+};
+struct BlockAttendArgs {
+    const __nv_bfloat16 *q;          // [B][n_q][Hq][128]
+    const int32_t *kv_len;
+    int n_q;
+    __nv_bfloat16 *out;
+    float *lse;                      // [B][Hq][n_q] or NULL
+    float *weights;                  // [pair][capacity] or NULL
+    int accumulate;
+    // scratch of the handle
+    float *part;
+    float *logits;                   // [pair][NB][rows][64] where weights are wanted
+    float *row_lse;                  // [pair][rows], log2 domain
+    uint32_t *count;                 // [pair], 0 between launches
+};
+
+cudaError_t launch_block_append(const BlockDev &D, int fmt, const BlockAppendArgs &a, cudaStream_t s);
+cudaError_t launch_block_read(const BlockDev &D, int fmt, const BlockReadArgs &a, cudaStream_t s);
+cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, const BlockEvictArgs &a, cudaStream_t s);
+cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArgs &a, int num_sms, cudaStream_t s);
+// floats of `part` and of `row_lse` that a handle's calls need
+int64_t blk_part_floats(int B, int Hkv, int G, int NB);
+
+__device__ __forceinline__ void blk_status(const BlockDev &D, int code, int b, int info) {
+    if (atomicCAS(D.status, 0, code) == 0) {
+        D.status[1] = D.layer;
+        D.status[2] = b;
+        D.status[3] = info;
+    }
+}
+
+__device__ __forceinline__ int blk_len(const BlockDev &D, const int32_t *len, int b) {
+    return min(max(len[b], 0), D.capacity);
+}
+
+// Two neighbouring codes (the low half of w) as two halves, exactly: an int8 code is held
+// with 128 added, and 1024 + u is the half 0x6400 | u.
+template <int FMT>
+__device__ __forceinline__ __half2 blk_half2(uint32_t w) {
+    if constexpr (FMT == QEVICT_BLOCK_INT8) {
+        const uint32_t x = __byte_perm(w, 0x64646464u, 0x5140);
+        return __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6480)));
+    } else {
+        uint32_t x;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(x) : "r"(w));
+        return *reinterpret_cast<const __half2 *>(&x);
+    }
+}
+
+// The codes of a block's scale. s = fl32(amax / Q); code = round(fl32(x / s)), to the
+// nearest, ties to even. The quotient comes from the reciprocal and two FMAs, which
+// round it as the division does while nothing underflows; below 2^-60 (values of no
+// model) the division itself is used, and the quotient clamped (s is then rounded to few
+// bits). amax is finite.
+struct BlockScale {
+    float s, r;   // r = 0: divide
+};
+template <int FMT>
+__device__ __forceinline__ BlockScale blk_scale(float amax) {
+    BlockScale q;
+    q.s = __fdiv_rn(amax, FMT == QEVICT_BLOCK_INT8 ? 127.f : 448.f);
+    q.r = q.s >= 0x1p-60f ? __frcp_rn(q.s) : 0.f;
+    return q;
+}
+__device__ __forceinline__ float blk_quotient(float x, const BlockScale &q, float top) {
+    if (q.r != 0.f) return div_by_recip(x, q.s, q.r);
+    return q.s > 0.f ? fminf(fmaxf(__fdiv_rn(x, q.s), -top), top) : 0.f;
+}
+// eight codes
+template <int FMT>
+__device__ __forceinline__ uint2 blk_codes(const float *x, const BlockScale &q) {
+    uint2 r;
+    uint32_t *w = &r.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i, ++w) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = blk_quotient(x[4 * i + j], q, FMT == QEVICT_BLOCK_INT8 ? 127.f : 448.f);
+        if constexpr (FMT == QEVICT_BLOCK_INT8) {
+            uint32_t u[4];   // 1.5 * 2^23 + 128 + y: rounded to an integer, code + 128 in the low byte
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(__fadd_rn(y[j], 12583040.f));
+            *w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+        } else {
+            asm("{\n\t.reg .b16 l, h;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+                "mov.b32 %0, {l, h};\n\t}"
+                : "=r"(*w)
+                : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+        }
+    }
+    return r;
+}
+// eight values, fl32(code * s)
+template <int FMT>
+__device__ __forceinline__ void blk_values(uint2 c, float s, float *x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? c.x : c.y;
+        const float2 f = __half22float2(blk_half2<FMT>((i & 1) ? w >> 16 : w));
+        x[2 * i] = __fmul_rn(f.x, s);
+        x[2 * i + 1] = __fmul_rn(f.y, s);
+    }
+}
+
+}  // namespace qevict
