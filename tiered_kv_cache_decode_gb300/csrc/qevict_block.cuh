@@ -96,18 +96,20 @@ __device__ __forceinline__ int blk_len(const BlockDev &D, const int32_t *len, in
     return min(max(len[b], 0), D.capacity);
 }
 
-// Two neighbouring codes (the low half of w) as two halves, exactly: an int8 code is held
-// with 128 added, and 1024 + u is the half 0x6400 | u.
-template <int FMT>
+// Two neighbouring codes (the low or high half of w) as two halves, exactly: an int8 code is
+// held with 128 added, and 1024 + u is the half 0x6400 | u.
+template <int FMT, bool HIGH = false>
 __device__ __forceinline__ __half2 blk_half2(uint32_t w) {
+    uint32_t x;
     if constexpr (FMT == QEVICT_BLOCK_INT8) {
-        const uint32_t x = __byte_perm(w, 0x64646464u, 0x5140);
+        x = __byte_perm(w, 0x64646464u, HIGH ? 0x5342 : 0x5140);
         return __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6480)));
+    } else if constexpr (HIGH) {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(x) : "r"(w));
     } else {
-        uint32_t x;
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(x) : "r"(w));
-        return *reinterpret_cast<const __half2 *>(&x);
     }
+    return *reinterpret_cast<const __half2 *>(&x);
 }
 
 // The codes of a block's scale. s = fl32(amax / Q); code = round(fl32(x / s)), to the
@@ -161,7 +163,7 @@ __device__ __forceinline__ void blk_values(uint2 c, float s, float *x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w = i < 2 ? c.x : c.y;
-        const float2 f = __half22float2(blk_half2<FMT>((i & 1) ? w >> 16 : w));
+        const float2 f = __half22float2((i & 1) ? blk_half2<FMT, true>(w) : blk_half2<FMT>(w));
         x[2 * i] = __fmul_rn(f.x, s);
         x[2 * i + 1] = __fmul_rn(f.y, s);
     }

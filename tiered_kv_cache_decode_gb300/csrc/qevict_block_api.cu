@@ -59,6 +59,8 @@ qevict_status check_config(const qevict_block_config &f) {
         return fail(QEVICT_ERR_INVALID_ARG, "score_queries must be in [0, %d]", kMaxBlkQueries);
     if ((int64_t)f.batch * f.num_kv_heads > 1 << 20)
         return fail(QEVICT_ERR_INVALID_ARG, "batch x num_kv_heads must be at most 2^20");
+    if ((int64_t)f.batch * f.num_kv_heads * ((f.capacity + kBlk - 1) / kBlk + 2) >= 1 << 30)
+        return fail(QEVICT_ERR_INVALID_ARG, "batch x num_kv_heads x blocks must be below 2^30");
     return QEVICT_OK;
 }
 
