@@ -74,15 +74,13 @@ struct BlockAttendArgs {
     float *part;
     float *logits;                   // [pair][NB][rows][64] where weights are wanted
     float *row_lse;                  // [pair][rows], log2 domain
-    uint32_t *count;                 // [pair], 0 between launches
 };
 
 cudaError_t launch_block_append(const BlockDev &D, int fmt, const BlockAppendArgs &a, cudaStream_t s);
 cudaError_t launch_block_read(const BlockDev &D, int fmt, const BlockReadArgs &a, cudaStream_t s);
 cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, const BlockEvictArgs &a, cudaStream_t s);
 cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArgs &a, int num_sms, cudaStream_t s);
-// floats of `part` and of `row_lse` that a handle's calls need
-int64_t blk_part_floats(int B, int Hkv, int G, int NB);
+int64_t blk_part_floats(int G);   // of `part`, for the calls of a handle with G query heads per KV head
 
 __device__ __forceinline__ void blk_status(const BlockDev &D, int code, int b, int info) {
     if (atomicCAS(D.status, 0, code) == 0) {

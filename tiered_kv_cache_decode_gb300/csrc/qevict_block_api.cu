@@ -15,7 +15,6 @@ struct qevict_block_cache {
     int device = 0, num_sms = 1, G = 1, NB = 0, capacity = 0;
     int32_t *status = nullptr;
     float *part = nullptr, *logits = nullptr, *row_lse = nullptr;
-    uint32_t *count = nullptr;
     std::vector<BlockDev> layers;
     std::vector<void *> memory;
 };
@@ -114,9 +113,8 @@ qevict_status qevict_block_create(const qevict_block_config *config, const qevic
     c->capacity = c->NB * kBlk;
     const size_t pairs = (size_t)f.batch * f.num_kv_heads;
     // every allocation first, so that a failing allocator leaves nothing behind
-    const size_t o_lse = 256, o_count = o_lse + up256(pairs * kMaxBlkQueries * c->G * 4);
-    const size_t o_part = o_count + up256(pairs * 4);
-    const size_t base_bytes = o_part + (size_t)blk_part_floats(f.batch, f.num_kv_heads, c->G, c->NB) * 4;
+    const size_t o_lse = 256, o_part = o_lse + up256(pairs * kMaxBlkQueries * c->G * 4);
+    const size_t base_bytes = o_part + (size_t)blk_part_floats(c->G) * 4;
     const size_t logit_bytes = pairs * c->capacity * c->G * f.score_queries * 4;
     const size_t o_scale = up256(pairs * c->NB * (size_t)kBlkBytes), o_open = o_scale + up256(pairs * c->NB * 8);
     const size_t layer_bytes = o_open + pairs * 4 * (size_t)kBlkBytes;
@@ -153,7 +151,6 @@ qevict_status qevict_block_create(const qevict_block_config *config, const qevic
     }
     c->status = (int32_t *)base;
     c->row_lse = (float *)(base + o_lse);
-    c->count = (uint32_t *)(base + o_count);
     c->part = (float *)(base + o_part);
     e = cudaMemsetAsync(base, 0, o_part, c->stream);
     for (const BlockDev &D : c->layers)
@@ -240,7 +237,6 @@ qevict_status qevict_block_attention(qevict_block_cache *c, int32_t layer, const
     a.part = c->part;
     a.logits = c->logits;
     a.row_lse = c->row_lse;
-    a.count = c->count;
     const cudaError_t e = launch_block_attend(c->layers[layer], c->cfg.format, a, c->num_sms, (cudaStream_t)stream);
     return e == cudaSuccess ? QEVICT_OK : cuda_fail(e, "block attention kernel");
 }
