@@ -25,7 +25,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kHalf = kBlkBytes / 2;               // what one copy brings: K or V of a unit
-constexpr int kSlots = 24;                         // of kHalf bytes, 3 for each warp
+// Of kHalf bytes, 2 for each warp: 128 KiB on their way to an SM. With 3 for each the memory system serves the SMs less
+// evenly (the slowest took 17 % longer than the median for as many bytes: 4 x 128K 175 us against 158), with 1 it idles (190).
+constexpr int kSlots = 16;
 constexpr int kRec = kHeadDim + 4;                 // floats of a row of a partial result: output, maximum, sum
 constexpr int kSmemBytes = kSlots * kHalf + 2 * kSlots * 8 + 16;
 
@@ -93,10 +95,14 @@ struct Unit {
     }
 };
 
+// The cache is read once a call: its lines leave the L2 first (the logits of a call with weights, and the parts, stay
+// in: 8 x 32K with weights 102 -> 100 us).
 __device__ __forceinline__ void copy_half(uint32_t dst, const uint8_t *src, uint32_t bar) {
+    uint64_t first_out;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first_out));
     tc_expect_tx(bar, kHalf);
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(kHalf), "r"(bar)
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
+                     "r"(dst), "l"(src), "r"(kHalf), "r"(bar), "l"(first_out)
                  : "memory");
 }
 template <bool BF>
@@ -195,18 +201,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
     const int streams = kWarps / groups, stream = warp % streams, group = warp / streams;
     const int slots = kSlots / streams, slot0 = stream * slots;
     const int R = a.n_q * D.G, room = 8 * NT * groups;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            tc_mbar_init(full + 8 * i, 1);
-            tc_mbar_init(empty + 8 * i, groups);
-        }
+    if (tid < kSlots) {
+        tc_mbar_init(full + 8 * tid, 1);
+        tc_mbar_init(empty + 8 * tid, groups);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *stop = 0;
     }
-    __syncthreads();
+    if (tid == 0) *stop = 0;
     // this ring's run of the row of units
     const int total = count_units(D, a.kv_len, 0, nullptr);
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int runs = min((int)gridDim.x * streams, total), run = stream * gridDim.x + blockIdx.x;
     if (run >= runs) return;
     const int begin = (int)((int64_t)total * run / runs), end = (int)((int64_t)total * (run + 1) / runs);
@@ -233,8 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
     int slot = 0, use = 0;   // of the next half to read
     bool ok = true;
     auto wait_half = [&]() {
-        ok = ok && tc_wait(full + 8 * (slot0 + slot), use & 1, stop);
-        __syncwarp();
+        ok = __all_sync(~0u, ok && tc_wait(full + 8 * (slot0 + slot), use & 1, stop));
         return ring + (slot0 + slot) * kHalf;
     };
     auto done_half = [&]() {
@@ -243,7 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
         if (++slot == slots) slot = 0, ++use;
         if (group != 0 || left == 0 || !ok) return;
         const int s = slot0 + cslot;   // the slot just read; every warp of the ring has read it
-        if (groups > 1 && !(ok = tc_wait(empty + 8 * s, (cuse - 1) & 1, stop))) return;
+        if (groups > 1) {
+            ok = __all_sync(~0u, tc_wait(empty + 8 * s, (cuse - 1) & 1, stop));   // a warp gives up as one
+            if (!ok) return;
+        }
         if (lane == 0) copy_half(ring + s * kHalf, cu.source(D) + chalf * kHalf, full + 8 * s);
         chalf ^= 1;
         if (--left > 0 && chalf == 0) cu.next(D, a.kv_len);
@@ -485,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
         }
         if (at < end) w.next(D, a.kv_len, u1 - u0);
     }
-    ok = !__any_sync(~0u, !ok);
     if (!ok && lane == 0) blk_status(D, QEVICT_ERR_TIMEOUT, 0, blockIdx.x);
     // after a wait that ran out: copies still on their way are waited for before the CTA ends
     if (!ok && group == 0) {
@@ -499,14 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
 }
 
 // Behind the attention: the first pairs x rows CTAs add up the parts of the pairs that lie in several runs, one row
-// each; the others turn the logits that the attention left into the tokens' weights, 1,024 tokens of a pair each.
-__global__ void __launch_bounds__(kThreads) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room) {
+// each; the others turn the logits that the attention left into the tokens' weights, `tile` blocks of a pair each.
+__global__ void __launch_bounds__(kThreads) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room, int tile) {
     __shared__ float red[kWarps][kRec];
     __shared__ float lse[kMaxBlkQueries * kMaxG];   // of the pair's rows, log2 domain
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.n_q * D.G;
     const int64_t pairs = (int64_t)D.B * D.Hkv;
     const bool join = blockIdx.x < pairs * R;
-    const int tiles = (D.NB + 15) / 16;
+    const int tiles = (D.NB + tile - 1) / tile;
     const int64_t x = join ? blockIdx.x : blockIdx.x - pairs * R, pair = join ? x / R : x / tiles;
     const int b = (int)(pair / D.Hkv), h = (int)(pair % D.Hkv), len = blk_len(D, a.kv_len, b), n = units_of(len);
     int before;
@@ -527,40 +532,60 @@ __global__ void __launch_bounds__(kThreads) block_join_kernel(const BlockDev D, 
             return;
         }
         if (c0 == c1) return;   // its run has written the result
-        // every warp: the maximum of all parts; warp w adds up the parts w, w + 8, ...
-        float m = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c, row)[kHeadDim]);
-        for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
-        const float ref = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
+        // warp w adds up the parts w, w + 8, ..., four at a time, relative to their running maximum
+        float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0 + warp; c <= c1; c += kWarps) {
-            const float *p = part(c, row);
-            const float2 ml = *reinterpret_cast<const float2 *>(p + kHeadDim);
-            const float4 y = *(reinterpret_cast<const float4 *>(p) + lane);
-            const float f = tc_ex2(ml.x - ref);   // 0 for a part whose keys the row does not see
-            l = fmaf(ml.y, f, l);
-            o.x = fmaf(y.x, f, o.x);
-            o.y = fmaf(y.y, f, o.y);
-            o.z = fmaf(y.z, f, o.z);
-            o.w = fmaf(y.w, f, o.w);
+        for (int c = c0 + warp; c <= c1; c += 4 * kWarps) {
+            float2 ml[4];
+            float4 y[4];
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = c + e * kWarps <= c1;
+                const float *p = part(in ? c + e * kWarps : c, row);
+                ml[e] = *reinterpret_cast<const float2 *>(p + kHeadDim);
+                y[e] = *(reinterpret_cast<const float4 *>(p) + lane);
+                if (!in) ml[e].x = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, ml[e].x);
+            const float ref = top == -INFINITY ? 0.f : top, f0 = tc_ex2(m - ref);
+            m = top;
+            l *= f0;
+            o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (c + e * kWarps > c1) break;
+                const float f = tc_ex2(ml[e].x - ref);   // 0 for a part whose keys the row does not see
+                l = fmaf(ml[e].y, f, l);
+                o.x = fmaf(y[e].x, f, o.x);
+                o.y = fmaf(y[e].y, f, o.y);
+                o.z = fmaf(y[e].z, f, o.z);
+                o.w = fmaf(y[e].w, f, o.w);
+            }
         }
         *(reinterpret_cast<float4 *>(red[warp]) + lane) = o;
-        if (lane == 0) red[warp][kHeadDim] = l;
+        if (lane == 0) {
+            red[warp][kHeadDim] = m;
+            red[warp][kHeadDim + 1] = l;
+        }
         __syncthreads();
         if (tid >= kHeadDim) return;
+        m = red[0][kHeadDim];
+        for (int e = 1; e < kWarps; ++e) m = fmaxf(m, red[e][kHeadDim]);
+        const float ref = m == -INFINITY ? 0.f : m;
         l = 0.f;
         float s = 0.f;
         for (int e = 0; e < kWarps; ++e) {
-            l += red[e][kHeadDim];
-            s += red[e][tid];
+            const float f = tc_ex2(red[e][kHeadDim] - ref);
+            l = fmaf(red[e][kHeadDim + 1], f, l);
+            s = fmaf(red[e][tid], f, s);
         }
         out[tid] = __float2bfloat16_rn(l == 0.f ? 0.f : s * (1.f / l));
         if (tid == 0 && out_lse) *out_lse = row_lse(m, l) * 0.6931471805599453f;
         return;
     }
-    const int j0 = (int)(x % tiles) * 16;
+    const int j0 = (int)(x % tiles) * tile;
     if (j0 * kBlk >= len) return;
     for (int row = warp; row < R; row += kWarps) {
         float m = -INFINITY, l = 0.f;
@@ -576,23 +601,34 @@ __global__ void __launch_bounds__(kThreads) block_join_kernel(const BlockDev D, 
         if (lane == 0) lse[row] = row_lse(m, l);
     }
     __syncthreads();
-    // four tokens to a thread
-    const int j = j0 + (tid >> 4), t = 4 * (tid & 15), pos = j * kBlk + t;
-    if (pos >= len) return;
-    const float4 *g = reinterpret_cast<const float4 *>(a.logits + (pair * D.NB + j) * R * kBlk + t);
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    // four tokens to a thread at a time
+    const int t = 4 * (tid & 15);
+#pragma unroll 2
+    for (int j = j0 + (tid >> 4); j < j0 + tile; j += kThreads / 16) {
+        const int pos = j * kBlk + t;
+        if (pos >= len) return;
+        const float4 *g = reinterpret_cast<const float4 *>(a.logits + (pair * D.NB + j) * R * kBlk + t);
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int row = 0; row < R; ++row) {
-        const float4 y = g[row * (kBlk / 4)];
-        const int last = len - a.n_q + row / D.G;
-        const float z[4] = {y.x, y.y, y.z, y.w};
+        for (int row = 0; row < R; ++row) {
+            const float4 y = __ldcs(g + row * (kBlk / 4));
+            const int last = len - a.n_q + row / D.G;
+            const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] += pos + e <= last ? tc_ex2(z[e] - lse[row]) : 0.f;
+            for (int e = 0; e < 4; ++e) w[e] += pos + e <= last ? tc_ex2(z[e] - lse[row]) : 0.f;
+        }
+        float *o = a.weights + pair * D.capacity + pos;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] /= D.G;
+        if (pos + 4 <= len && !(reinterpret_cast<uintptr_t>(o) & 15)) {
+            float4 *o4 = reinterpret_cast<float4 *>(o);
+            const float4 y = a.accumulate ? *o4 : make_float4(0.f, 0.f, 0.f, 0.f);
+            *o4 = make_float4(y.x + w[0], y.y + w[1], y.z + w[2], y.w + w[3]);
+        } else {
+            for (int e = 0; e < 4; ++e)
+                if (pos + e < len) o[e] = a.accumulate ? o[e] + w[e] : w[e];
+        }
     }
-    float *o = a.weights + pair * D.capacity + pos;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (pos + e < len) o[e] = a.accumulate ? o[e] + w[e] / D.G : w[e] / D.G;
 }
 
 }  // namespace
@@ -618,7 +654,10 @@ cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArg
     const cudaError_t e = fmt == I ? (nt == 1 ? launch_attend<I, 1>(D, a, grid, groups, s) : launch_attend<I, 2>(D, a, grid, groups, s))
                                    : (nt == 1 ? launch_attend<E, 1>(D, a, grid, groups, s) : launch_attend<E, 2>(D, a, grid, groups, s));
     if (e != cudaSuccess) return e;
-    const int64_t pairs = (int64_t)D.B * D.Hkv, ctas = pairs * R + (a.weights ? pairs * ((D.NB + 15) / 16) : 0);
+    // blocks whose weights a CTA writes: 16 at a time, as many as leave about six CTAs to an SM
+    const int64_t pairs = (int64_t)D.B * D.Hkv, each = pairs * D.NB / (6 * num_sms);
+    const int tile = each < 16 ? 16 : each > 64 ? 64 : (int)(each + 15) & ~15;
+    const int64_t ctas = pairs * R + (a.weights ? pairs * ((D.NB + tile - 1) / tile) : 0);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     // its launch overlaps the attention; it waits for that kernel's end before it reads what it left
     cudaLaunchConfig_t cfg{};
@@ -630,7 +669,7 @@ cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArg
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_join_kernel, D, a, grid * (kWarps / groups), 8 * nt * groups);
+    return cudaLaunchKernelEx(&cfg, block_join_kernel, D, a, grid * (kWarps / groups), 8 * nt * groups, tile);
 }
 
 }  // namespace qevict
