@@ -688,7 +688,7 @@ enum { QEVICT_BLOCK_INT8 = 0, QEVICT_BLOCK_E4M3 = 1 };
 
 /*  num_q_heads   a multiple of num_kv_heads, at most 8 per KV head.
  *  head_dim      must be 128.
- *  capacity      tokens per sequence, in [1, 2^24]; rounded up to a multiple of
+ *  capacity      tokens per sequence, in [1, 2^21]; rounded up to a multiple of
  *                64 (qevict_block_capacity gives it back).
  *  format        QEVICT_BLOCK_INT8 or QEVICT_BLOCK_E4M3.
  *  score_queries 0 to 8: the most queries per sequence of an attention call that
@@ -720,7 +720,7 @@ qevict_status qevict_block_destroy(qevict_block_cache *cache);
 int32_t qevict_block_capacity(const qevict_block_cache *cache);
 
 /* Tokens into the cache: token i < n_new[b] of sequence b at position start[b] + i.
- *  k, v     bf16 [batch][n] tokens of [Hkv][128], device, 16-byte aligned;
+ *  k, v     bf16 [batch][n] tokens of [Hkv][128], device, 16-byte aligned; n in [1, 2^21];
  *           consecutive tokens lie k_stride (v_stride) elements apart: a multiple
  *           of 8, at least the heads' own length.
  *  start    int32 [batch], device, or NULL: 0. n_new likewise, or NULL: n; clamped
@@ -763,6 +763,7 @@ qevict_status qevict_block_attention(qevict_block_cache *cache, int32_t layer, c
  *  kv_len   int32 [batch], device; rows at positions outside [0, kv_len[b]) are left
  *           as they were.
  *  first    int32 [batch], device, or NULL: 0.
+ *  n        rows, in [1, 2^21].
  *  k, v     bf16 [batch][n][Hkv][128], device, 16-byte aligned, written; either may
  *           not overlap the other or an input. */
 qevict_status qevict_block_read(qevict_block_cache *cache, int32_t layer, const int32_t *kv_len, const int32_t *first,
@@ -779,7 +780,7 @@ qevict_status qevict_block_read(qevict_block_cache *cache, int32_t layer, const 
  *           batch, heads and format, whose layer is overwritten.
  *  keep     a multiple of 64, at least 64; keep + 64 at most the destination's
  *           capacity. recent in [0, keep].
- *  weights  fp32 [batch][Hkv][capacity], device.
+ *  weights  fp32 [batch][Hkv][capacity], device, 16-byte aligned.
  *  weights_out  fp32 [batch][Hkv][capacity of the destination], or NULL: the weights
  *           of the tokens that stay, in their new places; places behind them are
  *           left as they were. May be `weights` itself where the capacities agree.

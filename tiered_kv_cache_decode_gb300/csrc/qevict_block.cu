@@ -29,185 +29,186 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 __device__ __forceinline__ uint4 finite8(const uint4 &x) {
     return make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
 }
-__device__ __forceinline__ void unpack8(const uint4 &x, float *y) {
+__device__ __forceinline__ void unpack8(const uint4 &x, uint64_t *y) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = __uint_as_float(w[i] << 16);
-        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) y[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-// the largest of two words over the CTA; `sm` has room for 2 x 8, and a call ends with all threads past its reads
-__device__ __forceinline__ uint2 cta_max(uint2 m, uint2 *sm) {
-    m.x = __reduce_max_sync(~0u, m.x);
-    m.y = __reduce_max_sync(~0u, m.y);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
-    __syncthreads();
-    uint2 r = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-        r.x = max(r.x, sm[i].x);
-        r.y = max(r.y, sm[i].y);
-    }
-    __syncthreads();
-    return r;
-}
-
-// One CTA takes one block of one (sequence, KV head): CTAs of the heads of a block are
-// neighbours, so that they read whole tokens between them. Thread: channels 8 c .. 8 c + 7
-// of rows r + 16 i.
+// The largest word over the CTA, a non-negative fp32 number's bits, and the scale that follows from it, which the first
+// warp computes for all. A call begins behind what the CTA's threads have read before.
+struct ScaleRoom {
+    uint32_t m[kThreads / 32], top;
+    BlockScale q;
+};
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) block_append_kernel(const BlockDev D, const BlockAppendArgs a, int nbx) {
-    __shared__ uint2 sm[kThreads / 32];
-    const int64_t u = blockIdx.x;
-    const int h = (int)(u % D.Hkv), jx = (int)(u / D.Hkv % nbx), b = (int)(u / D.Hkv / nbx);
-    const int64_t pair = (int64_t)b * D.Hkv + h;
-    const int tid = threadIdx.x, c = tid & 15, r = tid >> 4;
+__device__ __forceinline__ uint32_t cta_scale(uint32_t m, ScaleRoom &sm, BlockScale &q) {
+    m = __reduce_max_sync(~0u, m);
+    if ((threadIdx.x & 31) == 0) sm.m[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = __reduce_max_sync(~0u, threadIdx.x < kThreads / 32 ? sm.m[threadIdx.x] : 0u);
+        if (threadIdx.x == 0) {
+            sm.top = m;
+            sm.q = blk_scale<FMT>(__uint_as_float(m));
+        }
+    }
+    __syncthreads();
+    q = sm.q;
+    return sm.top;
+}
+// what a CTA works on: the keys (0) or values (1) of block number j of KV head h of sequence b. Neighbouring CTAs have
+// the heads of a block, so that they read whole tokens between them.
+struct Place {
+    int kv, h, j, b;
+    int64_t pair;
+    __device__ __forceinline__ explicit Place(const BlockDev &D)
+        : kv(blockIdx.x & 1), h(blockIdx.x >> 1), j(blockIdx.y), b(blockIdx.z), pair((int64_t)b * D.Hkv + h) {}
+};
+inline dim3 places(const BlockDev &D, int blocks) { return dim3(2u * D.Hkv, (unsigned)blocks, (unsigned)D.B); }
+
+// One CTA takes the keys or the values of one block of one (sequence, KV head). Thread: channels 8 c .. 8 c + 7 of rows
+// r + 16 i. Memory-bound: every row is read once and its codes written once (keys and values in CTAs of their own: 8
+// CTAs to an SM, 128 KiB of loads in flight).
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) block_append_kernel(const BlockDev D, const BlockAppendArgs a) {
+    __shared__ ScaleRoom sm;
+    const Place x(D);
+    const int b = x.b, tid = threadIdx.x, c = tid & 15, r = tid >> 4;
+    const bool speaks = x.j == 0 && x.h == 0 && x.kv == 0 && tid == 0;
     const int s = a.start ? a.start[b] : 0;
     const int m = a.n_new ? min(max(a.n_new[b], 0), a.n) : a.n;
     if (m == 0) return;
     if (s < 0) {
-        if (jx == 0 && h == 0 && tid == 0) blk_status(D, QEVICT_ERR_INVALID_ARG, b, s);
+        if (speaks) blk_status(D, QEVICT_ERR_INVALID_ARG, b, s);
         return;
     }
-    if ((int64_t)s + m > D.capacity && jx == 0 && h == 0 && tid == 0)
-        blk_status(D, QEVICT_ERR_CAPACITY, b, s);
+    if ((int64_t)s + m > D.capacity && speaks) blk_status(D, QEVICT_ERR_CAPACITY, b, s);
     const int e = (int)min((int64_t)s + m, (int64_t)D.capacity);
-    const int jb = (s >> 6) + jx;
+    const int jb = (s >> 6) + x.j;
     if (e <= s || jb * kBlk >= e) return;
-    const __nv_bfloat16 *kin = a.k + (int64_t)b * a.n * a.k_stride + h * kHeadDim + 8 * c;
-    const __nv_bfloat16 *vin = a.v + (int64_t)b * a.n * a.v_stride + h * kHeadDim + 8 * c;
-    if (a.weights && tid < kBlk) {
+    const int64_t stride = x.kv ? a.v_stride : a.k_stride;
+    const __nv_bfloat16 *in = (x.kv ? a.v : a.k) + (int64_t)b * a.n * stride + x.h * kHeadDim + 8 * c;
+    const int half = x.kv * (kBlkBytes / 2), p0 = jb * kBlk + r;
+    if (a.weights && x.kv == 0 && tid < kBlk) {
         const int pos = jb * kBlk + tid;
-        if (pos >= s && pos < e) a.weights[pair * D.capacity + pos] = 0.f;
+        if (pos >= s && pos < e) a.weights[x.pair * D.capacity + pos] = 0.f;
     }
     const bool full = (jb + 1) * kBlk <= e;
-    uint4 k[4], v[4];
+    uint4 y[4];
+    const __nv_bfloat16 *at = in + (int64_t)(p0 - s) * stride;   // row r's; where the block begins before the tokens, not read
+    if (jb * kBlk >= s && full) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = r + 16 * i, pos = jb * kBlk + t;
-        k[i] = v[i] = make_uint4(0, 0, 0, 0);
-        if (pos >= s && pos < e) {
-            k[i] = *reinterpret_cast<const uint4 *>(kin + (pos - s) * a.k_stride);
-            v[i] = *reinterpret_cast<const uint4 *>(vin + (pos - s) * a.v_stride);
-        } else if (pos < s && full) {
-            const uint8_t *o = D.open + blk_open_off(pair, jb, t) + blk_open_chunk(t, c);
-            k[i] = *reinterpret_cast<const uint4 *>(o);
-            v[i] = *reinterpret_cast<const uint4 *>(o + kBlkBytes / 2);
-        }
-    }
-    uint2 top = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        top.x = amax2(top.x, k[i]);
-        top.y = amax2(top.y, v[i]);
-    }
-    top.x = max(top.x & 0xffffu, top.x >> 16);
-    top.y = max(top.y & 0xffffu, top.y >> 16);
-    uint2 amax = cta_max(top, sm);   // all rows of the slot are read by now
-    if (amax.x >= 0x7f80u || amax.y >= 0x7f80u) {
-        if (tid == 0) blk_status(D, QEVICT_ERR_DEVICE, b, jb);
-        top = make_uint2(0, 0);
+        for (int i = 0; i < 4; ++i) y[i] = __ldcs(reinterpret_cast<const uint4 *>(at + 16 * i * stride));
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            k[i] = finite8(k[i]);
-            v[i] = finite8(v[i]);
-            top.x = amax2(top.x, k[i]);
-            top.y = amax2(top.y, v[i]);
+            const int t = r + 16 * i, pos = p0 + 16 * i;
+            y[i] = make_uint4(0, 0, 0, 0);
+            if (pos >= s && pos < e) y[i] = __ldcs(reinterpret_cast<const uint4 *>(at + 16 * i * stride));
+            else if (pos < s && full)
+                y[i] = *reinterpret_cast<const uint4 *>(D.open + blk_open_off(x.pair, jb, t) + half + blk_open_chunk(t, c));
         }
-        top.x = max(top.x & 0xffffu, top.x >> 16);
-        top.y = max(top.y & 0xffffu, top.y >> 16);
-        amax = cta_max(top, sm);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = amax2(top, y[i]);
+    BlockScale q;
+    const uint32_t amax = cta_scale<FMT>(max(top & 0xffffu, top >> 16) << 16, sm, q);   // all rows of the slot are read by now
+    if (amax >= 0x7f800000u) {
+        if (tid == 0) blk_status(D, QEVICT_ERR_DEVICE, b, jb);
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[i] = finite8(y[i]);
+            top = amax2(top, y[i]);
+        }
+        __syncthreads();
+        cta_scale<FMT>(max(top & 0xffffu, top >> 16) << 16, sm, q);
     }
     if (full) {
-        const BlockScale qk = blk_scale<FMT>(__uint_as_float(amax.x << 16));
-        const BlockScale qv = blk_scale<FMT>(__uint_as_float(amax.y << 16));
-        if (tid == 0) D.scale[pair * D.NB + jb] = make_float2(qk.s, qv.s);
-        uint8_t *o = D.codes + blk_code_off(D, pair, jb) + 8 * (c & 1);
+        if (tid == 0) reinterpret_cast<float *>(D.scale + x.pair * D.NB + jb)[x.kv] = q.s;
+        uint8_t *o = D.codes + blk_code_off(D, x.pair, jb) + half + 8 * (c & 1) + blk_chunk(r, c >> 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = r + 16 * i;
-            float x[8];
-            unpack8(k[i], x);
-            *reinterpret_cast<uint2 *>(o + blk_chunk(t, c >> 1)) = blk_codes<FMT>(x, qk);
-            unpack8(v[i], x);
-            *reinterpret_cast<uint2 *>(o + kBlkBytes / 2 + blk_chunk(t, c >> 1)) = blk_codes<FMT>(x, qv);
+        for (int i = 0; i < 4; ++i) {   // rows 16 apart have their chunks at the same places
+            uint64_t z[4];
+            unpack8(y[i], z);
+            *reinterpret_cast<uint2 *>(o + 16 * i * kHeadDim) = blk_codes<FMT>(z, q);
         }
     }
     // The new rows of the last full block and of the open one, into their slots. Where the
     // first block's CTA has read rows from a slot, it writes both itself, behind its reads.
     const int last = (e >> 6) - 1;
     const bool alone = (s & (kBlk - 1)) != 0;
-    if (jb >= last && (jx == 0 || !alone)) {
+    if (jb >= last && (x.j == 0 || !alone)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = r + 16 * i, pos = jb * kBlk + t;
-            if (pos < s || pos >= e) continue;
-            uint8_t *o = D.open + blk_open_off(pair, jb, t) + blk_open_chunk(t, c);
-            *reinterpret_cast<uint4 *>(o) = k[i];
-            *reinterpret_cast<uint4 *>(o + kBlkBytes / 2) = v[i];
+            if (pos >= s && pos < e)
+                *reinterpret_cast<uint4 *>(D.open + blk_open_off(x.pair, jb, t) + half + blk_open_chunk(t, c)) = y[i];
         }
     }
-    if (jx == 0 && alone) {
+    if (x.j == 0 && alone) {
         for (int j = max(last, jb + 1); j * kBlk < e; ++j)
-            for (int t = r; t < kBlk && j * kBlk + t < e; t += 16) {
-                const int64_t i = j * kBlk + t - s;
-                uint8_t *o = D.open + blk_open_off(pair, j, t) + blk_open_chunk(t, c);
-                *reinterpret_cast<uint4 *>(o) = finite8(*reinterpret_cast<const uint4 *>(kin + i * a.k_stride));
-                *reinterpret_cast<uint4 *>(o + kBlkBytes / 2) =
-                    finite8(*reinterpret_cast<const uint4 *>(vin + i * a.v_stride));
-            }
+            for (int t = r; t < kBlk && j * kBlk + t < e; t += 16)
+                *reinterpret_cast<uint4 *>(D.open + blk_open_off(x.pair, j, t) + half + blk_open_chunk(t, c)) =
+                    finite8(*reinterpret_cast<const uint4 *>(in + (int64_t)(j * kBlk + t - s) * stride));
     }
 }
 
 // One CTA: the rows that lie in one block of one (sequence, KV head).
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) block_read_kernel(const BlockDev D, const BlockReadArgs a, int nbx) {
-    const int64_t u = blockIdx.x;
-    const int h = (int)(u % D.Hkv), jx = (int)(u / D.Hkv % nbx), b = (int)(u / D.Hkv / nbx);
-    const int64_t pair = (int64_t)b * D.Hkv + h;
+__global__ void __launch_bounds__(kThreads) block_read_kernel(const BlockDev D, const BlockReadArgs a) {
+    const Place x(D);
     const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-    const int len = blk_len(D, a.kv_len, b);
-    const int64_t first = a.first ? a.first[b] : 0;
-    const int64_t jb = max(first >> 6, (int64_t)0) + jx;
+    const int len = blk_len(D, a.kv_len, x.b);
+    const int64_t first = a.first ? a.first[x.b] : 0;
+    const int64_t jb = max(first >> 6, (int64_t)0) + x.j;
     if (jb * kBlk >= len) return;
     const bool full = (jb + 1) * kBlk <= len;
-    const float2 s = full ? D.scale[pair * D.NB + jb] : make_float2(0.f, 0.f);
-    const uint8_t *in = D.codes + blk_code_off(D, pair, (int)jb) + 8 * (c & 1);
+    const int half = x.kv * (kBlkBytes / 2);
+    const float s = full ? reinterpret_cast<const float *>(D.scale + x.pair * D.NB + jb)[x.kv] : 0.f;
+    const uint8_t *in = D.codes + blk_code_off(D, x.pair, (int)jb) + half + 8 * (c & 1);
+    __nv_bfloat16 *out = (x.kv ? a.v : a.k) + ((int64_t)x.b * a.n * D.Hkv + x.h) * kHeadDim + 8 * c;
+    uint4 y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = r + 16 * i;
-        const int64_t pos = jb * kBlk + t, row = pos - first;
-        if (row < 0 || row >= a.n || pos >= len) continue;
-        uint4 k, v;
         if (full) {
-            float x[8];
+            const uint2 code = *reinterpret_cast<const uint2 *>(in + blk_chunk(t, c >> 1));
+            y[i].x = code.x;
+            y[i].y = code.y;
+        } else {
+            y[i] = *reinterpret_cast<const uint4 *>(D.open + blk_open_off(x.pair, (int)jb, t) + half + blk_open_chunk(t, c));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t pos = jb * kBlk + r + 16 * i, row = pos - first;
+        if (row < 0 || row >= a.n || pos >= len) continue;
+        if (full) {
+            uint64_t z[4];
+            blk_values<FMT>(make_uint2(y[i].x, y[i].y), s, z);
             uint32_t w[4];
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint2 code = *reinterpret_cast<const uint2 *>(in + kv * (kBlkBytes / 2) + blk_chunk(t, c >> 1));
-                blk_values<FMT>(code, kv ? s.y : s.x, x);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                    w[j] = *reinterpret_cast<const uint32_t *>(&p);
-                }
-                (kv ? v : k) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = f2_unpack(z[j]);
+                const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+                w[j] = *reinterpret_cast<const uint32_t *>(&p);
             }
-        } else {
-            const uint8_t *o = D.open + blk_open_off(pair, (int)jb, t) + blk_open_chunk(t, c);
-            k = *reinterpret_cast<const uint4 *>(o);
-            v = *reinterpret_cast<const uint4 *>(o + kBlkBytes / 2);
+            y[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        const int64_t at = (((int64_t)b * a.n + row) * D.Hkv + h) * kHeadDim + 8 * c;
-        *reinterpret_cast<uint4 *>(a.k + at) = k;
-        *reinterpret_cast<uint4 *>(a.v + at) = v;
+        *reinterpret_cast<uint4 *>(out + row * D.Hkv * kHeadDim) = y[i];
     }
 }
 
 // ---- eviction ---------------------------------------------------------------
-constexpr int kSelCtas = 8;                           // CTAs (a cluster) that rank a pair's tokens
-constexpr int kSelWarps = kSelCtas * kThreads / 32;   // each ranks a run of tokens of its own
+constexpr int kMoveCtas = 8;                // CTAs (a cluster) that move a pair's tokens in place
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kSelCtas = 8;                 // CTAs (a cluster) that rank a pair's tokens, at most
+constexpr int kSelTokens = 32768;           // tokens for which one more CTA is taken
+constexpr int kSelBins = 2048, kSelReps = 4;   // copies of a CTA's histogram, against lanes that meet in a bin
+constexpr int kSelKeys = 40960;             // keys of a CTA that are kept in shared memory, at most
+constexpr int kSelFixed = (kSelReps + 2) * kSelBins * 4;   // bytes of shared memory before the keys
 
 // a weight as an integer of the same order; NaN last, -0 as 0
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -216,65 +217,94 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// One cluster per (sequence, KV head): the `want`-th largest key of the candidates by
-// four passes over eight bits each, the CTAs' histograms added in distributed shared memory;
-// then each warp counts its run's keys above it and equal to it, and with the counts of all
-// warps before it gives every kept token its rank.
-__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kThreads)
-    block_select_kernel(const BlockDev D, const BlockEvictArgs a) {
-    __shared__ uint32_t hist[2][256];
-    __shared__ uint32_t sum[256], found[2];
-    __shared__ uint2 count[kThreads / 32];
-    const int64_t pair = blockIdx.x / kSelCtas;
-    const int rank = blockIdx.x % kSelCtas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// One cluster per (sequence, KV head): the `want`-th largest key of the candidates by passes over eleven, eleven and ten
+// bits, the CTAs' histograms added in distributed shared memory; then each warp counts its run's keys above it and equal to
+// it, and with the counts of all warps before it gives every kept token its rank. Bound by latency: one read of the weights
+// (then kept in shared memory: CACHED), three passes of one cluster barrier each, one more for the counts. Short contexts
+// take a cluster of one CTA, whose barrier is the CTA's own.
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDev D, const BlockEvictArgs a, int ctas) {
+    extern __shared__ __align__(16) uint32_t sel[];
+    uint32_t *rep = sel, *hists = rep + kSelReps * kSelBins, *keys = hists + 2 * kSelBins;   // keys: CACHED, this CTA's
+    __shared__ uint32_t warp_sum[kSelWarps], found[2];
+    __shared__ uint2 count[kSelWarps];
+    const int64_t pair = blockIdx.x / ctas;
+    const int rank = blockIdx.x % ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = (int)(pair / D.Hkv);
     const int len = blk_len(D, a.kv_len, b), c = len & ~(kBlk - 1);
     int32_t *kept = a.kept + pair * a.keep;
     if (c <= a.keep) {   // nothing leaves
-        for (int i = rank * kThreads + tid; i < a.keep; i += kSelCtas * kThreads) kept[i] = i < c ? i : -1;
+        for (int i = rank * kSelThreads + tid; i < a.keep; i += ctas * kSelThreads) kept[i] = i < c ? i : -1;
         return;
     }
     const float *w = a.weights + pair * D.capacity;
     const int cand = c - a.recent;
+    // a run of tokens to each warp, in order
+    const int run = ((c + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31;
+    const int lo = rank * kSelWarps * run, hi = min(lo + kSelWarps * run, c), hi_cand = min(hi, cand);
+    if (CACHED)
+        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelThreads) {   // c is a multiple of 64: whole groups of four
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(w + i));
+            *reinterpret_cast<uint4 *>(keys + i - lo) =
+                make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+        }
+    auto key_of = [&](int i) { return CACHED ? keys[i - lo] : weight_key(w[i]); };
     uint32_t want = a.keep - a.recent;   // of the candidates
     uint32_t prefix = 0;
-    if (want > 0) {
-        for (int pass = 0; pass < 4; ++pass) {
-            const int shift = 24 - 8 * pass;
-            uint32_t *hs = hist[pass & 1];
-            hs[tid] = 0;
-            __syncthreads();
-            for (int i = rank * kThreads + tid; i < cand; i += kSelCtas * kThreads) {
-                const uint32_t key = weight_key(w[i]);
-                if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&hs[(key >> shift) & 255], 1u);
-            }
-            __syncwarp();
-            cl_sync();
-            uint32_t n = 0;
-            for (int i = 0; i < kSelCtas; ++i)
-                n += (uint32_t)cl_ldi(cl_addr(smem_u32(&hs[tid]), i));
-            sum[tid] = n;
-            __syncthreads();
-            // the bin, from the top, in which the wanted key lies
-            uint32_t above = 0;
-            for (int i = tid + 1; i < 256; ++i) above += sum[i];
-            if (above < want && above + n >= want) {
-                found[0] = tid;
-                found[1] = want - above;
-            }
-            __syncthreads();
-            prefix = prefix << 8 | found[0];
-            want = found[1];
+    if (want == 0) prefix = ~0u;   // no key is above it, and none of those equal to it is wanted
+    for (int pass = 0; pass < 3 && a.keep > a.recent; ++pass) {
+        const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        uint32_t *hist = hists + (pass & 1) * kSelBins;
+        for (int i = tid; i < kSelReps * kSelBins / 4; i += kSelThreads)
+            reinterpret_cast<uint4 *>(rep)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        for (int i = lo + tid; i < hi_cand; i += kSelThreads) {
+            const uint32_t key = key_of(i);
+            if (pass == 0 || (key >> (shift + bits)) == prefix)
+                atomicAdd(&rep[((key >> shift) & ((1u << bits) - 1)) * kSelReps + lane % kSelReps], 1u);
         }
-    } else {
-        prefix = ~0u;   // no key is above it, and none of those equal to it is wanted
+        __syncthreads();
+#pragma unroll
+        for (int i = tid; i < kSelBins; i += kSelThreads) {
+            const uint4 x = reinterpret_cast<const uint4 *>(rep)[i];
+            hist[i] = x.x + x.y + x.z + x.w;
+        }
+        __syncwarp();
+        cl_sync();
+        uint32_t n0 = 0, n1 = 0;   // bins 2 tid and 2 tid + 1 of all CTAs
+#pragma unroll
+        for (int i = 0; i < kSelCtas; ++i) {
+            if (i >= ctas) continue;
+            const float2 x = cl_ld2(cl_addr(smem_u32(hist + 2 * tid), i));
+            n0 += __float_as_uint(x.x);
+            n1 += __float_as_uint(x.y);
+        }
+        // the bin, from the top, in which the wanted key lies
+        uint32_t from = n0 + n1;   // of the bins from this thread's on
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const uint32_t x = __shfl_down_sync(~0u, from, s);
+            if (lane + s < 32) from += x;
+        }
+        if (lane == 0) warp_sum[warp] = from;
+        __syncthreads();
+        from += __reduce_add_sync(~0u, lane > warp ? warp_sum[lane] : 0u);
+        const uint32_t above = from - n0 - n1;
+        if (above < want && from >= want) {
+            const bool upper = above + n1 >= want;
+            found[0] = 2 * tid + (upper ? 1 : 0);
+            found[1] = want - above - (upper ? 0 : n1);
+        }
+        __syncthreads();
+        prefix = prefix << bits | found[0];
+        want = found[1];
     }
-    // runs of tokens, a warp each, in order
-    const int run = ((c + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int lo = min((rank * (kThreads / 32) + warp) * run, c), hi = min(lo + run, c);
+    if (CACHED) __syncthreads();   // the keys, where no pass has met
+    const int wlo = min(lo + warp * run, hi), whi = min(wlo + run, hi);
     uint32_t above = 0, equal = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t key = i < cand ? weight_key(w[i]) : 0;
+    for (int i = wlo + lane; i < whi; i += 32) {
+        const uint32_t key = key_of(i);
         if (i >= cand || key > prefix) ++above;
         else if (key == prefix) ++equal;
     }
@@ -284,17 +314,17 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kThreads)
     __syncwarp();
     cl_sync();
     above = equal = 0;
-    for (int i = lane; i < rank * (kThreads / 32) + warp; i += 32) {
-        const uint32_t at = cl_addr(smem_u32(&count[i % (kThreads / 32)]), i / (kThreads / 32));
-        above += (uint32_t)cl_ldi(at);
-        equal += (uint32_t)cl_ldi(at + 4);
+    for (int i = lane; i < rank * kSelWarps + warp; i += 32) {
+        const float2 x = cl_ld2(cl_addr(smem_u32(&count[i % kSelWarps]), i / kSelWarps));
+        above += __float_as_uint(x.x);
+        equal += __float_as_uint(x.y);
     }
     above = __reduce_add_sync(~0u, above);
     equal = __reduce_add_sync(~0u, equal);
-    for (int i0 = lo; i0 < hi; i0 += 32) {
+    for (int i0 = wlo; i0 < whi; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t key = i < cand ? weight_key(w[i]) : 0;
-        const bool up = i < hi && (i >= cand || key > prefix), eq = i < hi && !up && key == prefix;
+        const uint32_t key = i < whi ? key_of(i) : 0;
+        const bool up = i < whi && (i >= cand || key > prefix), eq = i < whi && !up && key == prefix;
         const uint32_t mu = __ballot_sync(~0u, up), me = __ballot_sync(~0u, eq), below = (1u << lane) - 1;
         const uint32_t e = equal + __popc(me & below);
         if (up || (eq && e < want)) kept[above + __popc(mu & below) + min(e, want)] = i;
@@ -305,56 +335,52 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kThreads)
     cl_sync();   // no CTA leaves while others read its counts
 }
 
-// What a thread holds of a block on its way: channels 8 c .. + 7 of rows r + 16 i
+// What a thread holds of a block's keys or values on their way: channels 8 c .. + 7 of rows r + 16 i
 struct Moved {
-    uint2 k[4], v[4];
-    float2 s[4];
+    uint2 code[4];
+    float s[4];
     float w;   // threads 0 .. 63: the weight of row tid
 };
 
-__device__ __forceinline__ void load_moved(const BlockDev &D, int64_t pair, const int32_t *kept, int block, int c_len,
-                                           const float *w, Moved &m) {
+__device__ __forceinline__ void load_moved(const BlockDev &D, int64_t pair, int kv, const int32_t *kept, int block,
+                                           int c_len, const float *w, Moved &m) {
     const int tid = threadIdx.x, c = tid & 15, r = tid >> 4;
+    const uint8_t *in = D.codes + blk_code_off(D, pair, 0) + kv * (kBlkBytes / 2) + 8 * (c & 1);
+    const float *scale = reinterpret_cast<const float *>(D.scale + pair * D.NB) + kv;
+    int idx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) idx[i] = min(max(kept[block * kBlk + r + 16 * i], 0), c_len - 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int idx = min(max(kept[block * kBlk + r + 16 * i], 0), c_len - 1), j = idx >> 6, t = idx & (kBlk - 1);
-        const uint8_t *in = D.codes + blk_code_off(D, pair, j) + blk_chunk(t, c >> 1) + 8 * (c & 1);
-        m.k[i] = *reinterpret_cast<const uint2 *>(in);
-        m.v[i] = *reinterpret_cast<const uint2 *>(in + kBlkBytes / 2);
-        m.s[i] = D.scale[pair * D.NB + j];
+        m.code[i] = *reinterpret_cast<const uint2 *>(in + (int64_t)(idx[i] >> 6) * kBlkBytes + blk_chunk(idx[i] & (kBlk - 1), c >> 1));
+        m.s[i] = scale[2 * (idx[i] >> 6)];
     }
-    m.w = 0.f;
-    if (w && tid < kBlk) m.w = w[min(max(kept[block * kBlk + tid], 0), c_len - 1)];
+    m.w = w && tid < kBlk ? w[min(max(kept[block * kBlk + tid], 0), c_len - 1)] : 0.f;
 }
 
 template <int FMT>
-__device__ __forceinline__ void store_moved(const BlockDev &D, int64_t pair, int block, const Moved &m, float *w_out,
-                                            uint2 *sm) {
+__device__ __forceinline__ void store_moved(const BlockDev &D, int64_t pair, int kv, int block, const Moved &m, float *w_out,
+                                            ScaleRoom &sm) {
     const int tid = threadIdx.x, c = tid & 15, r = tid >> 4;
-    float x[8];
-    uint2 top = make_uint2(0, 0);
+    uint64_t x[4][4];
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        blk_values<FMT>(m.k[i], m.s[i].x, x);
+        blk_values<FMT>(m.code[i], m.s[i], x[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top.x = max(top.x, __float_as_uint(fabsf(x[j])));
-        blk_values<FMT>(m.v[i], m.s[i].y, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top.y = max(top.y, __float_as_uint(fabsf(x[j])));
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = f2_unpack(x[i][j]);
+            top = max3(top, fabsf(f.x), fabsf(f.y));
+        }
     }
-    const uint2 amax = cta_max(top, sm);
-    const BlockScale qk = blk_scale<FMT>(__uint_as_float(amax.x)), qv = blk_scale<FMT>(__uint_as_float(amax.y));
-    if (tid == 0) D.scale[pair * D.NB + block] = make_float2(qk.s, qv.s);
+    BlockScale q;
+    cta_scale<FMT>(__float_as_uint(top), sm, q);
+    if (tid == 0) reinterpret_cast<float *>(D.scale + pair * D.NB + block)[kv] = q.s;
     if (w_out && tid < kBlk) w_out[block * kBlk + tid] = m.w;
-    uint8_t *o = D.codes + blk_code_off(D, pair, block) + 8 * (c & 1);
+    uint8_t *o = D.codes + blk_code_off(D, pair, block) + kv * (kBlkBytes / 2) + 8 * (c & 1) + blk_chunk(r, c >> 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = r + 16 * i;
-        blk_values<FMT>(m.k[i], m.s[i].x, x);
-        *reinterpret_cast<uint2 *>(o + blk_chunk(t, c >> 1)) = blk_codes<FMT>(x, qk);
-        blk_values<FMT>(m.v[i], m.s[i].y, x);
-        *reinterpret_cast<uint2 *>(o + kBlkBytes / 2 + blk_chunk(t, c >> 1)) = blk_codes<FMT>(x, qv);
-    }
+    for (int i = 0; i < 4; ++i)   // rows 16 apart have their chunks at the same places
+        *reinterpret_cast<uint2 *>(o + 16 * i * kHeadDim) = blk_codes<FMT>(x[i], q);
 }
 
 // The open block's rows and weights, and the new length. Its slot follows its new place.
@@ -370,47 +396,48 @@ __device__ __forceinline__ void move_open(const BlockDev &D, const BlockDev &to,
         for (int i = tid; i < 2 * kBlkBytes / 16; i += kThreads) out[i] = in[i];
 }
 
-// Into another cache: one CTA per new block, the last one for the open block.
+// Into another cache: a CTA for the keys and one for the values of each new block, the last ones for the open block.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
-    block_move_kernel(const BlockDev D, const BlockDev to, const BlockEvictArgs a, int nbx) {
-    __shared__ uint2 sm[kThreads / 32];
-    const int64_t u = blockIdx.x;
-    const int h = (int)(u % D.Hkv), j = (int)(u / D.Hkv % nbx), b = (int)(u / D.Hkv / nbx);
-    const int64_t pair = (int64_t)b * D.Hkv + h;
-    const int len = blk_len(D, a.kv_len, b), c = len & ~(kBlk - 1), kept = min(c, a.keep);
-    if (j == nbx - 1) {
-        move_open(D, to, a, pair, len, c, kept);
-    } else if (j * kBlk < kept) {
+    block_move_kernel(const BlockDev D, const BlockDev to, const BlockEvictArgs a) {
+    __shared__ ScaleRoom sm;
+    const Place x(D);
+    const int len = blk_len(D, a.kv_len, x.b), c = len & ~(kBlk - 1), kept = min(c, a.keep);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection has ended
+    if (x.j == gridDim.y - 1) {
+        if (x.kv == 0) move_open(D, to, a, x.pair, len, c, kept);
+    } else if (x.j * kBlk < kept) {
+        const bool weights = a.weights_out && x.kv == 0;
         Moved m;
-        load_moved(D, pair, a.kept + pair * a.keep, j, c, a.weights_out ? a.weights + pair * D.capacity : nullptr, m);
-        store_moved<FMT>(to, pair, j, m, a.weights_out ? a.weights_out + pair * to.capacity : nullptr, sm);
+        load_moved(D, x.pair, x.kv, a.kept + x.pair * a.keep, x.j, c, weights ? a.weights + x.pair * D.capacity : nullptr, m);
+        store_moved<FMT>(to, x.pair, x.kv, x.j, m, weights ? a.weights_out + x.pair * to.capacity : nullptr, sm);
     }
 }
 
-// In place: a cluster per (sequence, KV head) goes over the new blocks in rounds of one per
+// In place: a cluster per (sequence, KV head), keys and values, goes over the new blocks in rounds of one per
 // CTA. A token only ever moves towards the front, so what round n reads lies at or behind
 // the blocks that it writes, and a barrier between a round's reads and its writes suffices.
 template <int FMT>
-__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kMoveCtas, 1, 1) __launch_bounds__(kThreads)
     block_compact_kernel(const BlockDev D, const BlockEvictArgs a) {
-    __shared__ uint2 sm[kThreads / 32];
-    const int64_t pair = blockIdx.x / kSelCtas;
-    const int rank = blockIdx.x % kSelCtas, b = (int)(pair / D.Hkv);
+    __shared__ ScaleRoom sm;
+    const int64_t pair = blockIdx.x / (2 * kMoveCtas);
+    const int rank = blockIdx.x % kMoveCtas, kv = blockIdx.x / kMoveCtas & 1, b = (int)(pair / D.Hkv);
     const int len = blk_len(D, a.kv_len, b), c = len & ~(kBlk - 1), kept = min(c, a.keep);
-    float *w = a.weights_out ? a.weights_out + pair * D.capacity : nullptr;
+    float *w = a.weights_out && kv == 0 ? a.weights_out + pair * D.capacity : nullptr;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection has ended
     if (c > kept) {
-        for (int j0 = 0; j0 * kBlk < kept; j0 += kSelCtas) {
+        for (int j0 = 0; j0 * kBlk < kept; j0 += kMoveCtas) {
             const int j = j0 + rank;
             Moved m;
-            if (j * kBlk < kept) load_moved(D, pair, a.kept + pair * a.keep, j, c, w, m);
+            if (j * kBlk < kept) load_moved(D, pair, kv, a.kept + pair * a.keep, j, c, w ? a.weights + pair * D.capacity : nullptr, m);
             __syncwarp();
-            cl_sync();
-            if (j * kBlk < kept) store_moved<FMT>(D, pair, j, m, w, sm);
+            cl_sync();   // also behind the last round's reads of `sm`
+            if (j * kBlk < kept) store_moved<FMT>(D, pair, kv, j, m, w, sm);
         }
     }
     // the last round's reads are behind a barrier: the open block's weights may go where they lay
-    if (rank == 0) move_open(D, D, a, pair, len, c, kept);
+    if (rank == 0 && kv == 0) move_open(D, D, a, pair, len, c, kept);
 }
 
 }  // namespace
@@ -418,34 +445,61 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kThreads)
 #define BY_FORMAT(fmt, kernel) ((fmt) == QEVICT_BLOCK_INT8 ? kernel<QEVICT_BLOCK_INT8> : kernel<QEVICT_BLOCK_E4M3>)
 
 cudaError_t launch_block_append(const BlockDev &D, int fmt, const BlockAppendArgs &a, cudaStream_t s) {
-    const int nbx = a.n == 1 ? 1 : (a.n + kBlk - 2) / kBlk + 1;   // blocks that n tokens can touch
-    const int64_t grid = (int64_t)D.B * D.Hkv * nbx;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    BY_FORMAT(fmt, block_append_kernel)<<<(unsigned)grid, kThreads, 0, s>>>(D, a, nbx);
+    const int blocks = a.n == 1 ? 1 : (a.n + kBlk - 2) / kBlk + 1;   // that n tokens can touch
+    BY_FORMAT(fmt, block_append_kernel)<<<places(D, blocks), kThreads, 0, s>>>(D, a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_block_read(const BlockDev &D, int fmt, const BlockReadArgs &a, cudaStream_t s) {
-    const int nbx = min((a.n + kBlk - 2) / kBlk + 1, D.NB);
-    const int64_t grid = (int64_t)D.B * D.Hkv * nbx;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    BY_FORMAT(fmt, block_read_kernel)<<<(unsigned)grid, kThreads, 0, s>>>(D, a, nbx);
+    BY_FORMAT(fmt, block_read_kernel)<<<places(D, min((a.n + kBlk - 2) / kBlk + 1, D.NB)), kThreads, 0, s>>>(D, a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, const BlockEvictArgs &a,
                                cudaStream_t s) {
     const int64_t pairs = (int64_t)D.B * D.Hkv;
-    const int nbx = a.keep / kBlk + 1;
-    if (pairs * kSelCtas > 0x7fffffffll || pairs * nbx > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    block_select_kernel<<<(unsigned)(pairs * kSelCtas), kThreads, 0, s>>>(D, a);
-    cudaError_t e = cudaGetLastError();
+    // the selection's keys in shared memory where the longest run of tokens that the capacity allows fits
+    int ctas = 1;
+    while (ctas < kSelCtas && ctas * kSelTokens < D.capacity) ctas *= 2;
+    const int run = ((D.capacity + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31, keys = run * kSelWarps;
+    const bool cached = keys <= kSelKeys;
+    cudaError_t e = once_per_device(0, [&] {
+        const cudaError_t r = cudaFuncSetAttribute(block_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kSelFixed + kSelKeys * 4);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(block_select_kernel<false>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSelFixed);
+    });
     if (e != cudaSuccess) return e;
-    if (to.codes == D.codes)
-        BY_FORMAT(fmt, block_compact_kernel)<<<(unsigned)(pairs * kSelCtas), kThreads, 0, s>>>(D, a);
-    else
-        BY_FORMAT(fmt, block_move_kernel)<<<(unsigned)(pairs * nbx), kThreads, 0, s>>>(D, to, a, nbx);
-    return cudaGetLastError();
+    {
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = ctas;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(pairs * ctas));
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.dynamicSmemBytes = kSelFixed + (cached ? keys * 4 : 0);
+        cfg.stream = s;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, cached ? block_select_kernel<true> : block_select_kernel<false>, D, a, ctas);
+        if (e != cudaSuccess) return e;
+    }
+    // the moving kernel's launch overlaps the selection, for whose end it waits
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (to.codes == D.codes) {
+        cfg.gridDim = dim3((unsigned)(2 * pairs * kMoveCtas));
+        return cudaLaunchKernelEx(&cfg, BY_FORMAT(fmt, block_compact_kernel), D, a);
+    }
+    cfg.gridDim = places(D, a.keep / kBlk + 1);
+    return cudaLaunchKernelEx(&cfg, BY_FORMAT(fmt, block_move_kernel), D, to, a);
 }
 
 }  // namespace qevict

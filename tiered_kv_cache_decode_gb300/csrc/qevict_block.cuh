@@ -10,7 +10,8 @@ namespace qevict {
 constexpr int kBlk = QEVICT_BLOCK_TOKENS;      // tokens that share a scale
 constexpr int kBlkBytes = 2 * kBlk * kHeadDim; // a block's codes of K, then of V
 constexpr int kOpenHalf = 32;                  // tokens of half an open block: as many bytes as a block's codes
-constexpr int kMaxBlkQueries = 8;
+constexpr int kMaxBlkQueries = QEVICT_BLOCK_MAX_QUERIES;
+constexpr int kMaxBlkTokens = 1 << 21;         // of a sequence, and of a call (blocks are a grid's second dimension)
 constexpr int kMaxBlkCtas = 192;               // CTAs of an attention launch (152 SMs, one each)
 
 // A layer's memory. "pair" = sequence * Hkv + KV head.
@@ -113,57 +114,108 @@ __device__ __forceinline__ __half2 blk_half2(uint32_t w) {
 // The codes of a block's scale. s = fl32(amax / Q); code = round(fl32(x / s)), to the
 // nearest, ties to even. The quotient comes from the reciprocal and two FMAs, which
 // round it as the division does while nothing underflows; below 2^-60 (values of no
-// model) the division itself is used, and the quotient clamped (s is then rounded to few
-// bits). amax is finite.
+// model) both sides are first multiplied by 2^80, which changes no quotient, and the
+// quotient is clamped (s is then rounded to few bits). amax is finite.
 struct BlockScale {
-    float s, r;   // r = 0: divide
+    float s, up, d, r;   // up 1 or 2^80; d = s up, r its reciprocal (s = 0: 0)
 };
 template <int FMT>
 __device__ __forceinline__ BlockScale blk_scale(float amax) {
     BlockScale q;
     q.s = __fdiv_rn(amax, FMT == QEVICT_BLOCK_INT8 ? 127.f : 448.f);
-    q.r = q.s >= 0x1p-60f ? __frcp_rn(q.s) : 0.f;
+    q.up = q.s >= 0x1p-60f ? 1.f : 0x1p80f;
+    q.d = q.s * q.up;
+    q.r = q.s > 0.f ? __frcp_rn(q.d) : 0.f;
     return q;
 }
-__device__ __forceinline__ float blk_quotient(float x, const BlockScale &q, float top) {
-    if (q.r != 0.f) return div_by_recip(x, q.s, q.r);
-    return q.s > 0.f ? fminf(fmaxf(__fdiv_rn(x, q.s), -top), top) : 0.f;
+// two fp32 operations in one instruction, each rounded as usual
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-// eight codes
+__device__ __forceinline__ float2 f2_unpack(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Eight codes of four pairs of values. The quotient is that of div_by_recip (qevict_div.cuh), two at a time.
 template <int FMT>
-__device__ __forceinline__ uint2 blk_codes(const float *x, const BlockScale &q) {
-    uint2 r;
-    uint32_t *w = &r.x;
+__device__ __forceinline__ uint2 blk_codes(const uint64_t *x, const BlockScale &q) {
+    constexpr float top = FMT == QEVICT_BLOCK_INT8 ? 127.f : 448.f;
+    const uint64_t r2 = f2_pack(q.r, q.r), nd2 = f2_pack(-q.d, -q.d);
+    uint64_t z[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i, ++w) {
-        float y[4];
+    for (int j = 0; j < 4; ++j) z[j] = x[j];
+    if (q.up != 1.f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = blk_quotient(x[4 * i + j], q, FMT == QEVICT_BLOCK_INT8 ? 127.f : 448.f);
+        for (int j = 0; j < 4; ++j) z[j] = f2_mul(z[j], f2_pack(q.up, q.up));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t q0 = f2_mul(z[j], r2);
+        z[j] = f2_fma(f2_fma(q0, nd2, z[j]), r2, q0);
+    }
+    if (q.up != 1.f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 y = f2_unpack(z[j]);
+            z[j] = f2_pack(fminf(fmaxf(y.x, -top), top), fminf(fmaxf(y.y, -top), top));
+        }
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
         if constexpr (FMT == QEVICT_BLOCK_INT8) {
-            uint32_t u[4];   // 1.5 * 2^23 + 128 + y: rounded to an integer, code + 128 in the low byte
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(__fadd_rn(y[j], 12583040.f));
-            *w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+            // 1.5 * 2^23 + 128 + y: rounded to an integer, code + 128 in the low byte
+            const uint64_t magic = f2_pack(12583040.f, 12583040.f);
+            const float2 a = f2_unpack(f2_add(z[2 * i], magic)), b = f2_unpack(f2_add(z[2 * i + 1], magic));
+            w[i] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                               __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
         } else {
+            const float2 a = f2_unpack(z[2 * i]), b = f2_unpack(z[2 * i + 1]);
             asm("{\n\t.reg .b16 l, h;\n\t"
                 "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
                 "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
                 "mov.b32 %0, {l, h};\n\t}"
-                : "=r"(*w)
-                : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+                : "=r"(w[i])
+                : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
         }
     }
-    return r;
+    return make_uint2(w[0], w[1]);
 }
-// eight values, fl32(code * s)
+// eight codes as four pairs of values fl32(code * s)
 template <int FMT>
-__device__ __forceinline__ void blk_values(uint2 c, float s, float *x) {
+__device__ __forceinline__ void blk_values(uint2 c, float s, uint64_t *x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w = i < 2 ? c.x : c.y;
-        const float2 f = __half22float2((i & 1) ? blk_half2<FMT, true>(w) : blk_half2<FMT>(w));
-        x[2 * i] = __fmul_rn(f.x, s);
-        x[2 * i + 1] = __fmul_rn(f.y, s);
+        uint64_t y;
+        if constexpr (FMT == QEVICT_BLOCK_INT8) {
+            // 2^23 + code + 128 has the held code in its low byte
+            const uint32_t a = __byte_perm(w, 0x4B000000u, (i & 1) ? 0x7652 : 0x7650);
+            const uint32_t b = __byte_perm(w, 0x4B000000u, (i & 1) ? 0x7653 : 0x7651);
+            y = f2_add(f2_pack(__uint_as_float(a), __uint_as_float(b)), f2_pack(-8388736.f, -8388736.f));
+        } else {
+            const float2 f = __half22float2((i & 1) ? blk_half2<FMT, true>(w) : blk_half2<FMT>(w));
+            y = f2_pack(f.x, f.y);
+        }
+        x[i] = f2_mul(y, f2_pack(s, s));
     }
 }
 

@@ -50,14 +50,14 @@ qevict_status check_config(const qevict_block_config &f) {
         return fail(QEVICT_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads, at most %d per KV head",
                     kMaxG);
     if (f.head_dim != kHeadDim) return fail(QEVICT_ERR_INVALID_ARG, "head_dim must be %d", kHeadDim);
-    if (f.capacity < 1 || f.capacity > 1 << 24)
-        return fail(QEVICT_ERR_INVALID_ARG, "capacity must be in [1, 2^24]");
+    if (f.capacity < 1 || f.capacity > kMaxBlkTokens)
+        return fail(QEVICT_ERR_INVALID_ARG, "capacity must be in [1, 2^21]");
     if (f.format != QEVICT_BLOCK_INT8 && f.format != QEVICT_BLOCK_E4M3)
         return fail(QEVICT_ERR_INVALID_ARG, "format must be QEVICT_BLOCK_INT8 or QEVICT_BLOCK_E4M3");
     if (f.score_queries < 0 || f.score_queries > kMaxBlkQueries)
         return fail(QEVICT_ERR_INVALID_ARG, "score_queries must be in [0, %d]", kMaxBlkQueries);
-    if ((int64_t)f.batch * f.num_kv_heads > 1 << 20)
-        return fail(QEVICT_ERR_INVALID_ARG, "batch x num_kv_heads must be at most 2^20");
+    if (f.batch > 65535 || (int64_t)f.batch * f.num_kv_heads > 1 << 20)
+        return fail(QEVICT_ERR_INVALID_ARG, "batch must be at most 65535, batch x num_kv_heads at most 2^20");
     if ((int64_t)f.batch * f.num_kv_heads * ((f.capacity + kBlk - 1) / kBlk + 2) >= 1 << 30)
         return fail(QEVICT_ERR_INVALID_ARG, "batch x num_kv_heads x blocks must be below 2^30");
     return QEVICT_OK;
@@ -179,7 +179,7 @@ qevict_status qevict_block_append(qevict_block_cache *c, int32_t layer, const vo
     qevict_status st = check_call(c, layer);
     if (st) return st;
     if (!k || !v) return fail(QEVICT_ERR_INVALID_ARG, "k and v must not be NULL");
-    if (n < 1 || n > 1 << 24) return fail(QEVICT_ERR_INVALID_ARG, "n (%d) must be in [1, 2^24]", n);
+    if (n < 1 || n > kMaxBlkTokens) return fail(QEVICT_ERR_INVALID_ARG, "n (%d) must be in [1, 2^21]", n);
     const int64_t row = (int64_t)c->cfg.num_kv_heads * kHeadDim;
     for (const int64_t x : {k_stride, v_stride})
         if (x < row || x % 8 || x > (int64_t)1 << 32)
@@ -246,7 +246,7 @@ qevict_status qevict_block_read(qevict_block_cache *c, int32_t layer, const int3
     qevict_status st = check_call(c, layer);
     if (st) return st;
     if (!kv_len || !k || !v) return fail(QEVICT_ERR_INVALID_ARG, "kv_len, k and v must not be NULL");
-    if (n < 1 || n > 1 << 24) return fail(QEVICT_ERR_INVALID_ARG, "n (%d) must be in [1, 2^24]", n);
+    if (n < 1 || n > kMaxBlkTokens) return fail(QEVICT_ERR_INVALID_ARG, "n (%d) must be in [1, 2^21]", n);
     st = check_align((uintptr_t)k | (uintptr_t)v, 16, "k and v");
     if (!st) st = check_align((uintptr_t)kv_len | (uintptr_t)first, 4, "kv_len and first");
     if (st) return st;
@@ -280,8 +280,10 @@ qevict_status qevict_block_evict(qevict_block_cache *c, int32_t layer, const int
                     "destination's capacity without the open block)", keep, kBlk, kBlk, to->capacity - kBlk);
     if (recent < 0 || recent > keep)
         return fail(QEVICT_ERR_INVALID_ARG, "recent (%d) must be in [0, keep]", recent);
-    st = check_align((uintptr_t)kv_len | (uintptr_t)weights | (uintptr_t)weights_out | (uintptr_t)new_len |
-                     (uintptr_t)kept, 4, "kv_len, weights, new_len and kept");
+    st = check_align((uintptr_t)weights, 16, "weights");
+    if (!st)
+        st = check_align((uintptr_t)kv_len | (uintptr_t)weights_out | (uintptr_t)new_len | (uintptr_t)kept, 4,
+                         "kv_len, weights_out, new_len and kept");
     if (st) return st;
     const int64_t B = c->cfg.batch, pairs = B * c->cfg.num_kv_heads;
     const bool own = weights_out == weights && to->capacity == c->capacity;
