@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) block_read_kernel(const BlockDev D, 
 constexpr int kMoveCtas = 8;                // CTAs (a cluster) that move a pair's tokens in place
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kSelCtas = 8;                 // CTAs (a cluster) that rank a pair's tokens, at most
-constexpr int kSelTokens = 32768;           // tokens for which one more CTA is taken
+constexpr int kSelTokens = 8192;            // tokens for which one more CTA is taken
 constexpr int kSelBins = 2048, kSelReps = 4;   // copies of a CTA's histogram, against lanes that meet in a bin
 constexpr int kSelKeys = 40960;             // keys of a CTA that are kept in shared memory, at most
 constexpr int kSelFixed = (kSelReps + 2) * kSelBins * 4;   // bytes of shared memory before the keys
@@ -240,29 +240,35 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
     }
     const float *w = a.weights + pair * D.capacity;
     const int cand = c - a.recent;
-    // a run of tokens to each warp, in order
-    const int run = ((c + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31;
-    const int lo = rank * kSelWarps * run, hi = min(lo + kSelWarps * run, c), hi_cand = min(hi, cand);
+    // a run of tokens to each warp, in order, four at a time to a lane (c is a multiple of 64)
+    const int run = ((c + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 127) & ~127;
+    const int lo = rank * kSelWarps * run, hi = min(lo + kSelWarps * run, c);
+    auto load4 = [&](int i) {   // the recent tokens' keys are above all
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(w + i));
+        return make_uint4(i < cand ? weight_key(x.x) : ~0u, i + 1 < cand ? weight_key(x.y) : ~0u,
+                          i + 2 < cand ? weight_key(x.z) : ~0u, i + 3 < cand ? weight_key(x.w) : ~0u);
+    };
     if (CACHED)
-        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelThreads) {   // c is a multiple of 64: whole groups of four
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(w + i));
-            *reinterpret_cast<uint4 *>(keys + i - lo) =
-                make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
-        }
-    auto key_of = [&](int i) { return CACHED ? keys[i - lo] : weight_key(w[i]); };
+        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelThreads) *reinterpret_cast<uint4 *>(keys + i - lo) = load4(i);
+    auto keys4 = [&](int i) { return CACHED ? *reinterpret_cast<const uint4 *>(keys + i - lo) : load4(i); };
     uint32_t want = a.keep - a.recent;   // of the candidates
     uint32_t prefix = 0;
-    if (want == 0) prefix = ~0u;   // no key is above it, and none of those equal to it is wanted
-    for (int pass = 0; pass < 3 && a.keep > a.recent; ++pass) {
+    if (want == 0) prefix = ~0u - 1;   // the recent ones' keys alone are above it, and none is equal to it
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        if (a.keep == a.recent) break;
         const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         uint32_t *hist = hists + (pass & 1) * kSelBins;
         for (int i = tid; i < kSelReps * kSelBins / 4; i += kSelThreads)
             reinterpret_cast<uint4 *>(rep)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        for (int i = lo + tid; i < hi_cand; i += kSelThreads) {
-            const uint32_t key = key_of(i);
-            if (pass == 0 || (key >> (shift + bits)) == prefix)
-                atomicAdd(&rep[((key >> shift) & ((1u << bits) - 1)) * kSelReps + lane % kSelReps], 1u);
+        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelThreads) {
+            const uint4 k4 = keys4(i);
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k[j] != ~0u && (pass == 0 || (k[j] >> (shift + bits)) == prefix))
+                    atomicAdd(&rep[((k[j] >> shift) & ((1u << bits) - 1)) * kSelReps + lane % kSelReps], 1u);
         }
         __syncthreads();
 #pragma unroll
@@ -303,10 +309,10 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
     if (CACHED) __syncthreads();   // the keys, where no pass has met
     const int wlo = min(lo + warp * run, hi), whi = min(wlo + run, hi);
     uint32_t above = 0, equal = 0;
-    for (int i = wlo + lane; i < whi; i += 32) {
-        const uint32_t key = key_of(i);
-        if (i >= cand || key > prefix) ++above;
-        else if (key == prefix) ++equal;
+    for (int i = wlo + 4 * lane; i < whi; i += 128) {
+        const uint4 k = keys4(i);
+        above += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+        equal += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
     }
     above = __reduce_add_sync(~0u, above);
     equal = __reduce_add_sync(~0u, equal);
@@ -314,61 +320,82 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
     __syncwarp();
     cl_sync();
     above = equal = 0;
-    for (int i = lane; i < rank * kSelWarps + warp; i += 32) {
-        const float2 x = cl_ld2(cl_addr(smem_u32(&count[i % kSelWarps]), i / kSelWarps));
+#pragma unroll
+    for (int i = 0; i < kSelCtas; ++i) {   // of the warps before this one
+        if (i > rank || (i == rank && lane >= warp)) continue;
+        const float2 x = cl_ld2(cl_addr(smem_u32(&count[lane]), i));
         above += __float_as_uint(x.x);
         equal += __float_as_uint(x.y);
     }
     above = __reduce_add_sync(~0u, above);
     equal = __reduce_add_sync(~0u, equal);
-    for (int i0 = wlo; i0 < whi; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < whi ? key_of(i) : 0;
-        const bool up = i < whi && (i >= cand || key > prefix), eq = i < whi && !up && key == prefix;
-        const uint32_t mu = __ballot_sync(~0u, up), me = __ballot_sync(~0u, eq), below = (1u << lane) - 1;
-        const uint32_t e = equal + __popc(me & below);
-        if (up || (eq && e < want)) kept[above + __popc(mu & below) + min(e, want)] = i;
-        above += __popc(mu);
-        equal += __popc(me);
+    for (int i0 = wlo; i0 < whi; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        const uint4 k4 = i < whi ? keys4(i) : make_uint4(0, 0, 0, 0);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        uint32_t mine = 0;   // above in the low half, equal in the high one
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mine += i < whi ? (k[j] > prefix ? 1u : k[j] == prefix ? 1u << 16 : 0u) : 0u;
+        uint32_t sum = mine;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const uint32_t x = __shfl_up_sync(~0u, sum, s);
+            if (lane >= s) sum += x;
+        }
+        uint32_t up = above + ((sum - mine) & 0xffffu), eq = equal + ((sum - mine) >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i >= whi) break;
+            if (k[j] > prefix) {
+                kept[up + min(eq, want)] = i + j;
+                ++up;
+            } else if (k[j] == prefix) {
+                if (eq < want) kept[up + eq] = i + j;
+                ++eq;
+            }
+        }
+        sum = __shfl_sync(~0u, sum, 31);
+        above += sum & 0xffffu;
+        equal += sum >> 16;
     }
     __syncwarp();
     cl_sync();   // no CTA leaves while others read its counts
 }
 
-// What a thread holds of a block's keys or values on their way: channels 8 c .. + 7 of rows r + 16 i
+// What a thread holds of a block's keys or values on their way: 16 channels (a chunk) of rows r and r + 32
 struct Moved {
-    uint2 code[4];
-    float s[4];
+    uint4 code[2];
+    float s[2];
     float w;   // threads 0 .. 63: the weight of row tid
 };
 
-__device__ __forceinline__ void load_moved(const BlockDev &D, int64_t pair, int kv, const int32_t *kept, int block,
-                                           int c_len, const float *w, Moved &m) {
-    const int tid = threadIdx.x, c = tid & 15, r = tid >> 4;
-    const uint8_t *in = D.codes + blk_code_off(D, pair, 0) + kv * (kBlkBytes / 2) + 8 * (c & 1);
+__device__ __forceinline__ void load_moved(const BlockDev &D, int64_t pair, int kv, const int32_t *kept, int block, int c_len,
+                                           const float *w, Moved &m) {
+    const int tid = threadIdx.x, c = tid & 7;
+    const uint8_t *in = D.codes + blk_code_off(D, pair, 0) + kv * (kBlkBytes / 2);
     const float *scale = reinterpret_cast<const float *>(D.scale + pair * D.NB) + kv;
-    int idx[4];
+    kept += block * kBlk;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) idx[i] = min(max(kept[block * kBlk + r + 16 * i], 0), c_len - 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m.code[i] = *reinterpret_cast<const uint2 *>(in + (int64_t)(idx[i] >> 6) * kBlkBytes + blk_chunk(idx[i] & (kBlk - 1), c >> 1));
-        m.s[i] = scale[2 * (idx[i] >> 6)];
+    for (int i = 0; i < 2; ++i) {
+        const int x = min(max(kept[(tid >> 3) + 32 * i], 0), c_len - 1);
+        m.code[i] = *reinterpret_cast<const uint4 *>(in + (int64_t)(x >> 6) * kBlkBytes + blk_chunk(x & (kBlk - 1), c));
+        m.s[i] = scale[2 * (x >> 6)];
     }
-    m.w = w && tid < kBlk ? w[min(max(kept[block * kBlk + tid], 0), c_len - 1)] : 0.f;
+    m.w = w && tid < kBlk ? w[min(max(kept[tid], 0), c_len - 1)] : 0.f;
 }
 
 template <int FMT>
 __device__ __forceinline__ void store_moved(const BlockDev &D, int64_t pair, int kv, int block, const Moved &m, float *w_out,
                                             ScaleRoom &sm) {
-    const int tid = threadIdx.x, c = tid & 15, r = tid >> 4;
-    uint64_t x[4][4];
+    const int tid = threadIdx.x;
+    uint64_t x[2][8];
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        blk_values<FMT>(m.code[i], m.s[i], x[i]);
+    for (int i = 0; i < 2; ++i) {
+        blk_values<FMT>(make_uint2(m.code[i].x, m.code[i].y), m.s[i], x[i]);
+        blk_values<FMT>(make_uint2(m.code[i].z, m.code[i].w), m.s[i], x[i] + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const float2 f = f2_unpack(x[i][j]);
             top = max3(top, fabsf(f.x), fabsf(f.y));
         }
@@ -377,10 +404,12 @@ __device__ __forceinline__ void store_moved(const BlockDev &D, int64_t pair, int
     cta_scale<FMT>(__float_as_uint(top), sm, q);
     if (tid == 0) reinterpret_cast<float *>(D.scale + pair * D.NB + block)[kv] = q.s;
     if (w_out && tid < kBlk) w_out[block * kBlk + tid] = m.w;
-    uint8_t *o = D.codes + blk_code_off(D, pair, block) + kv * (kBlkBytes / 2) + 8 * (c & 1) + blk_chunk(r, c >> 1);
+    uint8_t *o = D.codes + blk_code_off(D, pair, block) + kv * (kBlkBytes / 2) + blk_chunk(tid >> 3, tid & 7);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)   // rows 16 apart have their chunks at the same places
-        *reinterpret_cast<uint2 *>(o + 16 * i * kHeadDim) = blk_codes<FMT>(x[i], q);
+    for (int i = 0; i < 2; ++i) {   // rows 32 apart have their chunks at the same places
+        const uint2 lo = blk_codes<FMT>(x[i], q), hi = blk_codes<FMT>(x[i] + 4, q);
+        *reinterpret_cast<uint4 *>(o + 32 * i * kHeadDim) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
 }
 
 // The open block's rows and weights, and the new length. Its slot follows its new place.
@@ -398,7 +427,7 @@ __device__ __forceinline__ void move_open(const BlockDev &D, const BlockDev &to,
 
 // Into another cache: a CTA for the keys and one for the values of each new block, the last ones for the open block.
 template <int FMT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
     block_move_kernel(const BlockDev D, const BlockDev to, const BlockEvictArgs a) {
     __shared__ ScaleRoom sm;
     const Place x(D);
@@ -430,7 +459,8 @@ __global__ void __cluster_dims__(kMoveCtas, 1, 1) __launch_bounds__(kThreads)
         for (int j0 = 0; j0 * kBlk < kept; j0 += kMoveCtas) {
             const int j = j0 + rank;
             Moved m;
-            if (j * kBlk < kept) load_moved(D, pair, kv, a.kept + pair * a.keep, j, c, w ? a.weights + pair * D.capacity : nullptr, m);
+            if (j * kBlk < kept)
+                load_moved(D, pair, kv, a.kept + pair * a.keep, j, c, w ? a.weights + pair * D.capacity : nullptr, m);
             __syncwarp();
             cl_sync();   // also behind the last round's reads of `sm`
             if (j * kBlk < kept) store_moved<FMT>(D, pair, kv, j, m, w, sm);
@@ -461,7 +491,7 @@ cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, c
     // the selection's keys in shared memory where the longest run of tokens that the capacity allows fits
     int ctas = 1;
     while (ctas < kSelCtas && ctas * kSelTokens < D.capacity) ctas *= 2;
-    const int run = ((D.capacity + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31, keys = run * kSelWarps;
+    const int run = ((D.capacity + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 127) & ~127, keys = run * kSelWarps;
     const bool cached = keys <= kSelKeys;
     cudaError_t e = once_per_device(0, [&] {
         const cudaError_t r = cudaFuncSetAttribute(block_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,

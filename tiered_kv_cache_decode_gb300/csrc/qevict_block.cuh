@@ -79,7 +79,8 @@ struct BlockAttendArgs {
 
 cudaError_t launch_block_append(const BlockDev &D, int fmt, const BlockAppendArgs &a, cudaStream_t s);
 cudaError_t launch_block_read(const BlockDev &D, int fmt, const BlockReadArgs &a, cudaStream_t s);
-cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, const BlockEvictArgs &a, cudaStream_t s);
+cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, const BlockEvictArgs &a,
+                               cudaStream_t s);
 cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArgs &a, int num_sms, cudaStream_t s);
 int64_t blk_part_floats(int G);   // of `part`, for the calls of a handle with G query heads per KV head
 
