@@ -503,16 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
     }
 }
 
-// Behind the attention: the first pairs x rows CTAs add up the parts of the pairs that lie in several runs, one row
-// each; the others turn the logits that the attention left into the tokens' weights, `tile` blocks of a pair each.
-__global__ void __launch_bounds__(kThreads) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room, int tile) {
+// Behind the attention: the first CTAs turn the logits that it left into the tokens' weights, `tile` blocks of a pair
+// each; then pairs x rows CTAs add up the parts of the pairs that lie in several runs, one row each.
+__global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room, int tile) {
     __shared__ float red[kWarps][kRec];
     __shared__ float lse[kMaxBlkQueries * kMaxG];   // of the pair's rows, log2 domain
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.n_q * D.G;
     const int64_t pairs = (int64_t)D.B * D.Hkv;
-    const bool join = blockIdx.x < pairs * R;
-    const int tiles = (D.NB + tile - 1) / tile;
-    const int64_t x = join ? blockIdx.x : blockIdx.x - pairs * R, pair = join ? x / R : x / tiles;
+    const int tiles = a.weights ? (D.NB + tile - 1) / tile : 0;
+    const bool join = blockIdx.x >= pairs * tiles;
+    const int64_t x = join ? blockIdx.x - pairs * tiles : blockIdx.x, pair = join ? x / R : x / tiles;
     const int b = (int)(pair / D.Hkv), h = (int)(pair % D.Hkv), len = blk_len(D, a.kv_len, b), n = units_of(len);
     int before;
     const int total = count_units(D, a.kv_len, b, &before);
@@ -587,46 +587,68 @@ __global__ void __launch_bounds__(kThreads) block_join_kernel(const BlockDev D, 
     }
     const int j0 = (int)(x % tiles) * tile;
     if (j0 * kBlk >= len) return;
-    for (int row = warp; row < R; row += kWarps) {
+    // their log-sum-exps: half a warp to a row, a pass over its parts with a running maximum
+    for (int row = tid >> 4; row < ((R + 1) & ~1); row += kThreads / 16) {   // both halves of a warp go round alike
         float m = -INFINITY, l = 0.f;
-        if (c0 == c1) {
-            if (lane == 0) lse[row] = a.row_lse[pair * R + row];
-            continue;
+        if (c0 != c1 && row < R)
+#pragma unroll 2
+            for (int c = c0 + (tid & 15); c <= c1; c += 16) {
+                const float2 ml = *reinterpret_cast<const float2 *>(part(c, row) + kHeadDim);
+                const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+                l = fmaf(ml.y, tc_ex2(ml.x - ref), l * tc_ex2(m - ref));
+                m = top;
+            }
+        __syncwarp();
+#pragma unroll
+        for (int s = 8; s; s >>= 1) {
+            const float m2 = __shfl_xor_sync(~0u, m, s), l2 = __shfl_xor_sync(~0u, l, s);
+            const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.f : top;
+            l = fmaf(l2, tc_ex2(m2 - ref), l * tc_ex2(m - ref));
+            m = top;
         }
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c, row)[kHeadDim]);
-        for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
-        const float ref = m == -INFINITY ? 0.f : m;
-        for (int c = c0 + lane; c <= c1; c += 32) l = fmaf(part(c, row)[kHeadDim + 1], tc_ex2(part(c, row)[kHeadDim] - ref), l);
-        for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
-        if (lane == 0) lse[row] = row_lse(m, l);
+        if ((tid & 15) == 0 && row < R) lse[row] = c0 == c1 ? a.row_lse[pair * R + row] : row_lse(m, l);
     }
     __syncthreads();
-    // four tokens to a thread at a time
+    // four tokens of each of two blocks to a thread at a time, eight loads on their way
+    constexpr int kEach = kThreads / 16;
     const int t = 4 * (tid & 15);
-#pragma unroll 2
-    for (int j = j0 + (tid >> 4); j < j0 + tile; j += kThreads / 16) {
-        const int pos = j * kBlk + t;
-        if (pos >= len) return;
+    const float inv = 1.f / D.G;
+    for (int j = j0 + (tid >> 4); j < j0 + tile; j += 2 * kEach) {
+        const int pos[2] = {j * kBlk + t, j + kEach < j0 + tile ? (j + kEach) * kBlk + t : len};
+        if (pos[0] >= len) return;
         const float4 *g = reinterpret_cast<const float4 *>(a.logits + (pair * D.NB + j) * R * kBlk + t);
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int row = 0; row < R; ++row) {
-            const float4 y = __ldcs(g + row * (kBlk / 4));
-            const int last = len - a.n_q + row / D.G;
-            const float z[4] = {y.x, y.y, y.z, y.w};
+        float w[2][4] = {};
+        for (int r0 = 0; r0 < R; r0 += 4) {
+            float4 y[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] += pos + e <= last ? tc_ex2(z[e] - lse[row]) : 0.f;
+            for (int b2 = 0; b2 < 2; ++b2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r0 + i < R && pos[b2] < len) y[b2][i] = __ldcs(g + (b2 * kEach * R + r0 + i) * (kBlk / 4));
+#pragma unroll
+            for (int b2 = 0; b2 < 2; ++b2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (r0 + i >= R || pos[b2] >= len) continue;
+                    const float z[4] = {y[b2][i].x, y[b2][i].y, y[b2][i].z, y[b2][i].w}, ref = lse[r0 + i];
+                    const int last = len - a.n_q + (r0 + i) / D.G;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[b2][e] += pos[b2] + e <= last ? tc_ex2(z[e] - ref) : 0.f;
+                }
         }
-        float *o = a.weights + pair * D.capacity + pos;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] /= D.G;
-        if (pos + 4 <= len && !(reinterpret_cast<uintptr_t>(o) & 15)) {
-            float4 *o4 = reinterpret_cast<float4 *>(o);
-            const float4 y = a.accumulate ? *o4 : make_float4(0.f, 0.f, 0.f, 0.f);
-            *o4 = make_float4(y.x + w[0], y.y + w[1], y.z + w[2], y.w + w[3]);
-        } else {
-            for (int e = 0; e < 4; ++e)
-                if (pos + e < len) o[e] = a.accumulate ? o[e] + w[e] : w[e];
+        for (int b2 = 0; b2 < 2; ++b2) {
+            if (pos[b2] >= len) continue;
+            float *o = a.weights + pair * D.capacity + pos[b2];
+            if (pos[b2] + 4 <= len && !(reinterpret_cast<uintptr_t>(o) & 15)) {
+                float4 *o4 = reinterpret_cast<float4 *>(o);
+                const float4 y = a.accumulate ? *o4 : make_float4(0.f, 0.f, 0.f, 0.f);
+                *o4 = make_float4(fmaf(w[b2][0], inv, y.x), fmaf(w[b2][1], inv, y.y), fmaf(w[b2][2], inv, y.z),
+                                  fmaf(w[b2][3], inv, y.w));
+            } else {
+                for (int e = 0; e < 4; ++e)
+                    if (pos[b2] + e < len) o[e] = fmaf(w[b2][e], inv, a.accumulate ? o[e] : 0.f);
+            }
         }
     }
 }
@@ -654,8 +676,8 @@ cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArg
     const cudaError_t e = fmt == I ? (nt == 1 ? launch_attend<I, 1>(D, a, grid, groups, s) : launch_attend<I, 2>(D, a, grid, groups, s))
                                    : (nt == 1 ? launch_attend<E, 1>(D, a, grid, groups, s) : launch_attend<E, 2>(D, a, grid, groups, s));
     if (e != cudaSuccess) return e;
-    // blocks whose weights a CTA writes: 16 at a time, as many as leave about six CTAs to an SM
-    const int64_t pairs = (int64_t)D.B * D.Hkv, each = pairs * D.NB / (6 * num_sms);
+    // blocks whose weights a CTA writes: 16 at a time, as many as leave about four CTAs to an SM
+    const int64_t pairs = (int64_t)D.B * D.Hkv, each = pairs * D.NB / (4 * num_sms);
     const int tile = each < 16 ? 16 : each > 64 ? 64 : (int)(each + 15) & ~15;
     const int64_t ctas = pairs * R + (a.weights ? pairs * ((D.NB + tile - 1) / tile) : 0);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
