@@ -108,11 +108,11 @@ __device__ __forceinline__ void copy_half(uint32_t dst, const uint8_t *src, uint
 template <bool BF>
 __device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -301,21 +301,30 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
                 uint32_t base = wait_half();
                 float x[NT][8][2];
                 const uint32_t k0 = base + n * kHeadDim + (((2 * q) ^ n) << 4), k1 = base + n * kHeadDim + (((2 * q + 1) ^ n) << 4);
+                // two tiles of 8 tokens at a time: their chains of products overlap
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const uint4 lo = lds128(k0 + t * 8 * kHeadDim), hi = lds128(k1 + t * 8 * kHeadDim);
-                    const uint32_t kw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int t = 0; t < 8; t += 2) {
+                    float c[2][4] = {};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma<false>(c, qf[0][i][0], NT == 2 ? qf[NT - 1][i][0] : 0u, qf[0][i][1],
-                                   NT == 2 ? qf[NT - 1][i][1] : 0u, bits(blk_half2<FMT>(kw[i])),
-                                   bits(blk_half2<FMT, true>(kw[i])));
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t ka = half ? k1 : k0;
+                        const uint4 ta = lds128(ka + t * 8 * kHeadDim), tb = lds128(ka + (t + 1) * 8 * kHeadDim);
+                        const uint32_t kw[2][4] = {{ta.x, ta.y, ta.z, ta.w}, {tb.x, tb.y, tb.z, tb.w}};
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        x[j][t][0] = c[2 * j];
-                        x[j][t][1] = c[2 * j + 1];
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                mma<false>(c[e], qf[0][4 * half + i][0], NT == 2 ? qf[NT - 1][4 * half + i][0] : 0u,
+                                           qf[0][4 * half + i][1], NT == 2 ? qf[NT - 1][4 * half + i][1] : 0u,
+                                           bits(blk_half2<FMT>(kw[e][i])), bits(blk_half2<FMT, true>(kw[e][i])));
                     }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            x[j][t + e][0] = c[e][2 * j];
+                            x[j][t + e][1] = c[e][2 * j + 1];
+                        }
                 }
                 done_half();
                 uint32_t p[NT][8];
@@ -354,23 +363,31 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
                 base = wait_half();
                 const uint32_t v0 = base + lane * kHeadDim;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 va = ldsm_t(v0 + ((i ^ (lane & 7)) << 4));
-                    const uint4 vb = ldsm_t(v0 + 32 * kHeadDim + ((i ^ (lane & 7)) << 4));
-                    const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-                    float c[NT][4] = {};
+                for (int i = 0; i < 8; i += 2) {   // two sets of 16 channels at a time
+                    float c[2][NT][4] = {};
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        uint32_t a0, a1, a2, a3;
-                        pair_halves<FMT>(vw[2 * t], a0, a1);
-                        pair_halves<FMT>(vw[2 * t + 1], a2, a3);
+                    for (int half = 0; half < 2; ++half) {   // 32 tokens each
+                        uint4 v[2];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) mma<false>(c[j], a0, a1, a2, a3, p[j][2 * t], p[j][2 * t + 1]);
+                        for (int e = 0; e < 2; ++e) v[e] = ldsm_t(v0 + half * 32 * kHeadDim + (((i + e) ^ (lane & 7)) << 4));
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t a0, a1, a2, a3;
+                                pair_halves<FMT>(t ? v[e].z : v[e].x, a0, a1);
+                                pair_halves<FMT>(t ? v[e].w : v[e].y, a2, a3);
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+                                    mma<false>(c[e][j], a0, a1, a2, a3, p[j][4 * half + 2 * t], p[j][4 * half + 2 * t + 1]);
+                            }
                     }
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) r.o[j][i][e] = fmaf(c[j][e], sc.y, r.o[j][i][e]);
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) r.o[j][i + e][g] = fmaf(c[e][j][g], sc.y, r.o[j][i + e][g]);
                 }
                 done_half();
             } else {
