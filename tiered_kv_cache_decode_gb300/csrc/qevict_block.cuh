@@ -12,7 +12,6 @@ constexpr int kBlkBytes = 2 * kBlk * kHeadDim; // a block's codes of K, then of 
 constexpr int kOpenHalf = 32;                  // tokens of half an open block: as many bytes as a block's codes
 constexpr int kMaxBlkQueries = QEVICT_BLOCK_MAX_QUERIES;
 constexpr int kMaxBlkTokens = 1 << 21;         // of a sequence, and of a call (blocks are a grid's second dimension)
-constexpr int kMaxBlkCtas = 192;               // CTAs of an attention launch (152 SMs, one each)
 
 // A layer's memory. "pair" = sequence * Hkv + KV head.
 //  codes  [pair][NB][K, V][64 tokens][128 channels], a byte each. The eight
@@ -82,7 +81,7 @@ cudaError_t launch_block_read(const BlockDev &D, int fmt, const BlockReadArgs &a
 cudaError_t launch_block_evict(const BlockDev &D, const BlockDev &to, int fmt, const BlockEvictArgs &a,
                                cudaStream_t s);
 cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArgs &a, int num_sms, cudaStream_t s);
-int64_t blk_part_floats(int G);   // of `part`, for the calls of a handle with G query heads per KV head
+int64_t blk_part_floats(int G, int num_sms);   // of `part`, for the calls of a handle with G query heads per KV head
 
 __device__ __forceinline__ void blk_status(const BlockDev &D, int code, int b, int info) {
     if (atomicCAS(D.status, 0, code) == 0) {

@@ -114,7 +114,7 @@ qevict_status qevict_block_create(const qevict_block_config *config, const qevic
     const size_t pairs = (size_t)f.batch * f.num_kv_heads;
     // every allocation first, so that a failing allocator leaves nothing behind
     const size_t o_lse = 256, o_part = o_lse + up256(pairs * kMaxBlkQueries * c->G * 4);
-    const size_t base_bytes = o_part + (size_t)blk_part_floats(c->G) * 4;
+    const size_t base_bytes = o_part + (size_t)blk_part_floats(c->G, c->num_sms) * 4;
     const size_t logit_bytes = pairs * c->capacity * c->G * f.score_queries * 4;
     const size_t o_scale = up256(pairs * c->NB * (size_t)kBlkBytes), o_open = o_scale + up256(pairs * c->NB * 8);
     const size_t layer_bytes = o_open + pairs * 4 * (size_t)kBlkBytes;

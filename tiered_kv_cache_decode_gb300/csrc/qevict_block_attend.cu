@@ -8,14 +8,14 @@
 // A unit is what one pair of bulk copies brings: a block's codes, or 32 rows of an open block, 16 KiB either way. The
 // units of all (sequence, KV head) pairs, in one row, are divided evenly over the device's warps, whatever the
 // lengths: each warp takes a run of them through a ring of its own (no warps ever meet), and keeps a running
-// maximum, sum and output for 8 or 16 rows:
+// maximum, sum and output for 8 rows:
 //   S = Q K^T      m16n8k16, rows x tokens (8 of the 16 rows used): a key's row is the operand as it lies, each
 //                  lane 32 consecutive channels of a token; the query's fragments follow that order of channels.
 //   O^T += V^T P   m16n8k16, channels x rows: S's registers are P's operand; V comes transposed from ldmatrix
 //                  (which moves pairs of channels; their bytes are put in order on the way to fp16).
 // Codes become fp16 exactly (int8 and e4m3 alike). A query row is scaled by a power of two into fp16's range:
 // exact down to 2^-28 of its largest channel. Scales of K go into the factor of the logits, scales of V into an
-// FMA per output after a block's product. More than 16 rows: 2 or 4 warps share a ring, 16 rows each.
+// FMA per output after a block's product. More than 8 rows: warps share a ring, 8 rows each.
 // A second kernel, launched while the first runs, adds up the parts of pairs that lie in several runs.
 #include "qevict_block.cuh"
 #include "qevict_tc.cuh"
@@ -23,7 +23,7 @@
 namespace qevict {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8;
+constexpr int kThreads = 256, kWarps = 8;          // of the joining kernel
 constexpr int kHalf = kBlkBytes / 2;               // what one copy brings: K or V of a unit
 // Of kHalf bytes, 2 for each warp: 128 KiB on their way to an SM. With 3 for each the memory system serves the SMs less
 // evenly (the slowest took 17 % longer than the median for as many bytes: 4 x 128K 175 us against 158), with 1 it idles (190).
@@ -147,43 +147,35 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
-__device__ __forceinline__ float quad_max(float x) {
-    x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-    return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-}
-
-// What a warp keeps of its 8 NT rows: lane (n, q) = (lane / 4, lane % 4) has the maxima (log2 domain) of rows
-// 8 j + n and its own share of their sums, and of O^T rows 8 j + 2 q, + 1 of channels 16 i + 2 n (o[j][i][0..1]) and
-// 16 i + 2 n + 1 (o[j][i][2..3]).
-template <int NT>
+// What a warp keeps of its 8 rows: lane (n, q) = (lane / 4, lane % 4) has the maximum (log2 domain) of row n and its own
+// share of its sum, and of O^T rows 2 q, 2 q + 1 of channels 16 i + 2 n (o[i][0..1]) and 16 i + 2 n + 1 (o[i][2..3]).
 struct Rows {
-    float m[NT], l[NT], o[NT][8][4];
+    float m, l, o[8][4];
     __device__ __forceinline__ void clear() {
+        m = -INFINITY;
+        l = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            m[j] = -INFINITY;
-            l[j] = 0.f;
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][i][e] = 0.f;
-        }
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     }
-    // moves a maximum; what the exponentials are taken against
-    __device__ __forceinline__ float raise(int j, float top, int q) {
-        const float m1 = fmaxf(m[j], top), ref = m1 == -INFINITY ? 0.f : m1;
-        if (__any_sync(~0u, m1 > m[j])) {
-            const float f = tc_ex2(m[j] - ref);   // 0 for the first keys
+    // moves the maximum; what the exponentials are taken against
+    __device__ __forceinline__ float raise(float top, int q) {
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float m1 = fmaxf(m, top), ref = m1 == -INFINITY ? 0.f : m1;
+        if (__any_sync(~0u, m1 > m)) {
+            const float f = tc_ex2(m - ref);   // 0 for the first keys; 1 for the rows that stay
             const float f0 = __shfl_sync(~0u, f, 8 * q), f1 = __shfl_sync(~0u, f, 8 * q + 4);
-            l[j] *= f;
+            l *= f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                o[j][i][0] *= f0;
-                o[j][i][1] *= f1;
-                o[j][i][2] *= f0;
-                o[j][i][3] *= f1;
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
             }
-            m[j] = m1;
+            m = m1;
         }
         return ref;
     }
@@ -192,15 +184,15 @@ struct Rows {
 // log-sum-exp of a row from its maximum and sum, log2 domain; a row that sees nothing has a sum of 0
 __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
-template <int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDev D, const BlockAttendArgs a, int groups) {
+template <int FMT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const BlockDev D, const BlockAttendArgs a, int groups) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t ring = smem_u32(smem), full = ring + kSlots * kHalf, empty = full + kSlots * 8;
     volatile int *stop = reinterpret_cast<int *>(smem + kSlots * kHalf + 2 * kSlots * 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, q = lane & 3;
-    const int streams = kWarps / groups, stream = warp % streams, group = warp / streams;
+    const int streams = WARPS / groups, stream = warp % streams, group = warp / streams;
     const int slots = kSlots / streams, slot0 = stream * slots;
-    const int R = a.n_q * D.G, room = 8 * NT * groups;
+    const int R = a.n_q * D.G, room = 8 * groups;
     if (tid < kSlots) {
         tc_mbar_init(full + 8 * tid, 1);
         tc_mbar_init(empty + 8 * tid, groups);
@@ -212,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int runs = min((int)gridDim.x * streams, total), run = stream * gridDim.x + blockIdx.x;
-    if (run >= runs) return;
+    if (run >= runs || group >= groups) return;
     const int begin = (int)((int64_t)total * run / runs), end = (int)((int64_t)total * (run + 1) / runs);
     Unit w;
     w.find(D, a.kv_len, begin);
@@ -257,49 +249,49 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
     };
 
     constexpr float kLog2e = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
+    const int row = 8 * group + n;   // this lane's row of a pair
     for (int at = begin; at < end;) {
         const int b = w.b, h = w.h, u0 = w.u, len = w.len, nb = len >> 6, u1 = min(w.n, u0 + end - at);
         const int64_t pair = (int64_t)b * D.Hkv + h;
         const bool whole = u0 == 0 && u1 == w.n;
         at += u1 - u0;
-        // the rows' queries: channels 32 q .. 32 q + 31 as fp16 fragments, scaled by a power of two
-        uint32_t qf[NT][8][2];
-        float scale[NT];
-        int row[NT], last[NT];   // this lane's rows of the pair, the last token that each sees
-        const __nv_bfloat16 *qrow[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            row[j] = 8 * (NT * group + j) + n;
-            const int i = min(row[j] / D.G, a.n_q - 1);
-            last[j] = len - a.n_q + i;
-            qrow[j] = a.q + (((int64_t)b * a.n_q + i) * D.Hq + h * D.G + row[j] % D.G) * kHeadDim + 32 * q;
-            uint4 x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = row[j] < R ? __ldg(reinterpret_cast<const uint4 *>(qrow[j]) + e) : make_uint4(0, 0, 0, 0);
-            const uint32_t *xw = &x[0].x;
+        // the row's query: channels 32 q .. 32 q + 31 as fp16 fragments, scaled by a power of two
+        const int i_q = min(row / D.G, a.n_q - 1), last = len - a.n_q + i_q;   // last: the last token that the row sees
+        const uint4 *qrow = reinterpret_cast<const uint4 *>(
+            a.q + (((int64_t)b * a.n_q + i_q) * D.Hq + h * D.G + row % D.G) * kHeadDim + 32 * q);
+        uint32_t qf[16];
+        float scale;
+        {
             uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = __vmaxu2(top, xw[e] & 0x7fff7fffu);
+            for (int e = 0; e < 4; ++e) {
+                const uint4 x = row < R ? __ldg(qrow + e) : make_uint4(0, 0, 0, 0);
+                qf[4 * e] = x.x;
+                qf[4 * e + 1] = x.y;
+                qf[4 * e + 2] = x.z;
+                qf[4 * e + 3] = x.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = __vmaxu2(top, qf[e] & 0x7fff7fffu);
             top = max(top & 0xffffu, top >> 16);
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             // the largest channel into [2^14, 2^15); an infinite or NaN row stays so
             const int e2 = top >= 0x7f80u ? 14 : min(max((int)(top >> 7) - 127, -112), 127);
             const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
-            scale[j] = __uint_as_float((uint32_t)(127 - 14 + e2) << 23) * kLog2e;
+            scale = __uint_as_float((uint32_t)(127 - 14 + e2) << 23) * kLog2e;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                qf[j][e >> 1][e & 1] = bits(__floats2half2_rn(__uint_as_float(xw[e] << 16) * up,
-                                                              __uint_as_float(xw[e] & 0xffff0000u) * up));
+                qf[e] = bits(__floats2half2_rn(__uint_as_float(qf[e] << 16) * up, __uint_as_float(qf[e] & 0xffff0000u) * up));
         }
-        Rows<NT> r;
+        Rows r;
         r.clear();
         for (int u = u0; u < u1; ++u) {
+            float *logits = a.weights && row < R ? a.logits + ((pair * D.NB + min(u, nb)) * R + row) * kBlk + 2 * q : nullptr;
             if (u < nb) {
                 const float2 sc = __ldg(D.scale + pair * D.NB + u);
                 uint32_t base = wait_half();
-                float x[NT][8][2];
+                float x[8][2];
                 const uint32_t k0 = base + n * kHeadDim + (((2 * q) ^ n) << 4), k1 = base + n * kHeadDim + (((2 * q + 1) ^ n) << 4);
                 // two tiles of 8 tokens at a time: their chains of products overlap
 #pragma unroll
@@ -314,57 +306,49 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
-                                mma<false>(c[e], qf[0][4 * half + i][0], NT == 2 ? qf[NT - 1][4 * half + i][0] : 0u,
-                                           qf[0][4 * half + i][1], NT == 2 ? qf[NT - 1][4 * half + i][1] : 0u,
+                                mma<false>(c[e], qf[8 * half + 2 * i], 0u, qf[8 * half + 2 * i + 1], 0u,
                                            bits(blk_half2<FMT>(kw[e][i])), bits(blk_half2<FMT, true>(kw[e][i])));
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            x[j][t + e][0] = c[e][2 * j];
-                            x[j][t + e][1] = c[e][2 * j + 1];
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        x[t + e][0] = c[e][0];
+                        x[t + e][1] = c[e][1];
+                    }
                 }
                 done_half();
-                uint32_t p[NT][8];
+                const float f = sc.x * scale;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const float f = sc.x * scale[j];
+                for (int t = 0; t < 8; ++t) {
+                    x[t][0] *= f;
+                    x[t][1] *= f;
+                }
+                if (logits) {
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        x[j][t][0] *= f;
-                        x[j][t][1] *= f;
-                    }
-                    if (a.weights && row[j] < R) {
-                        float *g = a.logits + ((pair * D.NB + u) * R + row[j]) * kBlk + 2 * q;
+                    for (int t = 0; t < 8; ++t) *reinterpret_cast<float2 *>(logits + 8 * t) = make_float2(x[t][0], x[t][1]);
+                }
+                if (u * kBlk + kBlk - 1 > len - a.n_q) {
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            *reinterpret_cast<float2 *>(g + 8 * t) = make_float2(x[j][t][0], x[j][t][1]);
-                    }
-                    if (u * kBlk + kBlk - 1 > len - a.n_q) {
+                    for (int t = 0; t < 8; ++t)
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
+                        for (int e = 0; e < 2; ++e)
+                            if (u * kBlk + 8 * t + 2 * q + e > last) x[t][e] = -INFINITY;
+                }
+                float top = x[0][0];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (u * kBlk + 8 * t + 2 * q + e > last[j]) x[j][t][e] = -INFINITY;
-                    }
-                    float top = x[j][0][0];
+                for (int t = 0; t < 8; ++t) top = max3(top, x[t][0], x[t][1]);
+                const float ref = r.raise(top, q);
+                uint32_t p[8];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) top = fmaxf(top, fmaxf(x[j][t][0], x[j][t][1]));
-                    const float ref = r.raise(j, quad_max(top), q);
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const float p0 = tc_ex2(x[j][t][0] - ref), p1 = tc_ex2(x[j][t][1] - ref);
-                        r.l[j] += p0 + p1;
-                        p[j][t] = bits(__floats2half2_rn(p0, p1));   // against the running maximum: 2^-12 of a term
-                    }
+                for (int t = 0; t < 8; ++t) {
+                    const float p0 = tc_ex2(x[t][0] - ref), p1 = tc_ex2(x[t][1] - ref);
+                    r.l += p0 + p1;
+                    p[t] = bits(__floats2half2_rn(p0, p1));   // against the running maximum: 2^-12 of a term
                 }
                 base = wait_half();
                 const uint32_t v0 = base + lane * kHeadDim;
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {   // two sets of 16 channels at a time
-                    float c[2][NT][4] = {};
+                    float c[2][4] = {};
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {   // 32 tokens each
                         uint4 v[2];
@@ -377,93 +361,74 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
                                 uint32_t a0, a1, a2, a3;
                                 pair_halves<FMT>(t ? v[e].z : v[e].x, a0, a1);
                                 pair_halves<FMT>(t ? v[e].w : v[e].y, a2, a3);
-#pragma unroll
-                                for (int j = 0; j < NT; ++j)
-                                    mma<false>(c[e][j], a0, a1, a2, a3, p[j][4 * half + 2 * t], p[j][4 * half + 2 * t + 1]);
+                                mma<false>(c[e], a0, a1, a2, a3, p[4 * half + 2 * t], p[4 * half + 2 * t + 1]);
                             }
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) r.o[j][i + e][g] = fmaf(c[e][j][g], sc.y, r.o[j][i + e][g]);
+                        for (int g = 0; g < 4; ++g) r.o[i + e][g] = fmaf(c[e][g], sc.y, r.o[i + e][g]);
                 }
                 done_half();
             } else {
                 // 32 bf16 rows of the open block
                 const int t0 = nb * kBlk + (u - nb) * kOpenHalf;
                 uint32_t base = wait_half();
-                float x[NT][4][2];
+                float x[4][2];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint4 k = lds128(base + blk_open_chunk(8 * t + n, 4 * q + i));
-                        uint4 y[NT];
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            y[j] = row[j] < R ? __ldg(reinterpret_cast<const uint4 *>(qrow[j]) + i) : make_uint4(0, 0, 0, 0);
-                        const uint4 z = NT == 2 ? y[NT - 1] : make_uint4(0, 0, 0, 0);
-                        mma<true>(c, y[0].x, z.x, y[0].y, z.y, k.x, k.y);
-                        mma<true>(c, y[0].z, z.z, y[0].w, z.w, k.z, k.w);
+                        const uint4 y = row < R ? __ldg(qrow + i) : make_uint4(0, 0, 0, 0);
+                        mma<true>(c, y.x, 0u, y.y, 0u, k.x, k.y);
+                        mma<true>(c, y.z, 0u, y.w, 0u, k.z, k.w);
                     }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        x[j][t][0] = c[2 * j] * kLog2e;
-                        x[j][t][1] = c[2 * j + 1] * kLog2e;
-                    }
+                    x[t][0] = c[0] * kLog2e;
+                    x[t][1] = c[1] * kLog2e;
                 }
                 done_half();
-                uint32_t p[NT][4], pl[NT][4];   // each probability as two bf16 parts
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if (a.weights && row[j] < R) {
-                        float *g = a.logits + ((pair * D.NB + nb) * R + row[j]) * kBlk + (u - nb) * kOpenHalf + 2 * q;
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            *reinterpret_cast<float2 *>(g + 8 * t) = make_float2(x[j][t][0], x[j][t][1]);
-                    }
-                    float top = -INFINITY;
+                if (logits) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
+                        *reinterpret_cast<float2 *>(logits + (u - nb) * kOpenHalf + 8 * t) = make_float2(x[t][0], x[t][1]);
+                }
+                float top = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (t0 + 8 * t + 2 * q + e > last[j]) x[j][t][e] = -INFINITY;
-                            top = fmaxf(top, x[j][t][e]);
-                        }
-                    const float ref = r.raise(j, quad_max(top), q);
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const float p0 = tc_ex2(x[j][t][0] - ref), p1 = tc_ex2(x[j][t][1] - ref);
-                        r.l[j] += p0 + p1;
-                        p[j][t] = pack_bf(p0, p1);
-                        pl[j][t] = pack_bf(p0 - __uint_as_float(p[j][t] << 16),
-                                           p1 - __uint_as_float(p[j][t] & 0xffff0000u));
+                    for (int e = 0; e < 2; ++e) {
+                        if (t0 + 8 * t + 2 * q + e > last) x[t][e] = -INFINITY;
+                        top = fmaxf(top, x[t][e]);
                     }
+                const float ref = r.raise(top, q);
+                uint32_t p[4], pl[4];   // each probability as two bf16 parts
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float p0 = tc_ex2(x[t][0] - ref), p1 = tc_ex2(x[t][1] - ref);
+                    r.l += p0 + p1;
+                    p[t] = pack_bf(p0, p1);
+                    pl[t] = pack_bf(p0 - __uint_as_float(p[t] << 16), p1 - __uint_as_float(p[t] & 0xffff0000u));
                 }
                 base = wait_half();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint4 va = ldsm_t(base + blk_open_chunk(lane, 2 * i));
                     const uint4 vb = ldsm_t(base + blk_open_chunk(lane, 2 * i + 1));
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma<true>(c, va.x, vb.x, va.y, vb.y, p[0], p[1]);
+                    mma<true>(c, va.z, vb.z, va.w, vb.w, p[2], p[3]);
+                    mma<true>(c, va.x, vb.x, va.y, vb.y, pl[0], pl[1]);
+                    mma<true>(c, va.z, vb.z, va.w, vb.w, pl[2], pl[3]);
+                    // c: channels n and 8 + n of the 16; the accumulators hold 2 n and 2 n + 1
+                    const int s0 = ((2 * n) & 7) * 4 + q, s1 = s0 + 4;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        float c[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma<true>(c, va.x, vb.x, va.y, vb.y, p[j][0], p[j][1]);
-                        mma<true>(c, va.z, vb.z, va.w, vb.w, p[j][2], p[j][3]);
-                        mma<true>(c, va.x, vb.x, va.y, vb.y, pl[j][0], pl[j][1]);
-                        mma<true>(c, va.z, vb.z, va.w, vb.w, pl[j][2], pl[j][3]);
-                        // c: channels n and 8 + n of the 16; the accumulators hold 2 n and 2 n + 1
-                        const int s0 = ((2 * n) & 7) * 4 + q, s1 = s0 + 4;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float lo0 = __shfl_sync(~0u, c[e], s0), hi0 = __shfl_sync(~0u, c[2 + e], s0);
-                            const float lo1 = __shfl_sync(~0u, c[e], s1), hi1 = __shfl_sync(~0u, c[2 + e], s1);
-                            r.o[j][i][e] += n < 4 ? lo0 : hi0;
-                            r.o[j][i][2 + e] += n < 4 ? lo1 : hi1;
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        const float lo0 = __shfl_sync(~0u, c[e], s0), hi0 = __shfl_sync(~0u, c[2 + e], s0);
+                        const float lo1 = __shfl_sync(~0u, c[e], s1), hi1 = __shfl_sync(~0u, c[2 + e], s1);
+                        r.o[i][e] += n < 4 ? lo0 : hi0;
+                        r.o[i][2 + e] += n < 4 ? lo1 : hi1;
                     }
                 }
                 done_half();
@@ -472,38 +437,32 @@ __global__ void __launch_bounds__(kThreads, 1) block_attend_kernel(const BlockDe
         // the run's part of the pair: its result, or one of the parts that the joining kernel adds up (a run has at
         // most two: of the pair that it begins inside of, and of the one that it ends inside of)
         float *part = a.part + ((int64_t)run * 2 + (u0 == 0 ? 1 : 0)) * room * kRec;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float l = r.l[j] + __shfl_xor_sync(~0u, r.l[j], 1);
-            l += __shfl_xor_sync(~0u, l, 2);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            if (q == 0 && row[j] < R) {
-                if (whole) {
-                    const float lse = row_lse(r.m[j], l);
-                    if (a.lse)
-                        a.lse[((int64_t)b * D.Hq + h * D.G + row[j] % D.G) * a.n_q + row[j] / D.G] = lse * 0.6931471805599453f;
-                    if (a.weights) a.row_lse[pair * R + row[j]] = lse;
-                } else {
-                    *reinterpret_cast<float2 *>(part + row[j] * kRec + kHeadDim) = make_float2(r.m[j], l);
-                }
+        float l = r.l + __shfl_xor_sync(~0u, r.l, 1);
+        l += __shfl_xor_sync(~0u, l, 2);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (q == 0 && row < R) {
+            if (whole) {
+                const float lse = row_lse(r.m, l);
+                if (a.lse) a.lse[((int64_t)b * D.Hq + h * D.G + row % D.G) * a.n_q + i_q] = lse * 0.6931471805599453f;
+                if (a.weights) a.row_lse[pair * R + row] = lse;
+            } else {
+                *reinterpret_cast<float2 *>(part + row * kRec + kHeadDim) = make_float2(r.m, l);
             }
+        }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float f = __shfl_sync(~0u, inv, 8 * q + 4 * e);
-                const int rr = 8 * (NT * group + j) + 2 * q + e;
-                if (rr >= R) continue;
-                if (whole) {
-                    __nv_bfloat16 *o =
-                        a.out + (((int64_t)b * a.n_q + rr / D.G) * D.Hq + h * D.G + rr % D.G) * kHeadDim + 2 * n;
+        for (int e = 0; e < 2; ++e) {
+            const float f = __shfl_sync(~0u, inv, 8 * q + 4 * e);
+            const int rr = 8 * group + 2 * q + e;
+            if (rr >= R) continue;
+            if (whole) {
+                __nv_bfloat16 *o = a.out + (((int64_t)b * a.n_q + rr / D.G) * D.Hq + h * D.G + rr % D.G) * kHeadDim + 2 * n;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint32_t *>(o + 16 * i) = pack_bf(r.o[j][i][e] * f, r.o[j][i][2 + e] * f);
-                } else {
-                    float *o = part + rr * kRec + 2 * n;
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint32_t *>(o + 16 * i) = pack_bf(r.o[i][e] * f, r.o[i][2 + e] * f);
+            } else {
+                float *o = part + rr * kRec + 2 * n;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float2 *>(o + 16 * i) = make_float2(r.o[j][i][e], r.o[j][i][2 + e]);
-                }
+                for (int i = 0; i < 8; ++i) *reinterpret_cast<float2 *>(o + 16 * i) = make_float2(r.o[i][e], r.o[i][2 + e]);
             }
         }
         if (at < end) w.next(D, a.kv_len, u1 - u0);
@@ -672,26 +631,32 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
 
 }  // namespace
 
-int64_t blk_part_floats(int G) { return (int64_t)kMaxBlkCtas * 2 * (kMaxBlkQueries * G > 8 ? 16 : 8) * kWarps * kRec; }
+// Warps of a CTA: 8 for up to 8 rows (the memory bounds them; 128 KiB are on their way either way). More rows share a
+// ring, a warp for every 8, and there arithmetic bounds: 12 warps, what the registers allow (5 queries of 4 x 8K 41 us,
+// 43.5 with 8 warps of 16 rows, which share the codes' way to fp16, 43 with 16 warps).
+constexpr int kFewWarps = 8, kManyWarps = 12;
 
-template <int FMT, int NT>
+int64_t blk_part_floats(int G, int num_sms) {
+    // runs x rows of a part: a ring's runs times its warps' rows, at most 8 rows to a warp
+    const int rows = kMaxBlkQueries * G > 8 ? 8 * kManyWarps : 8 * kFewWarps;
+    return (int64_t)num_sms * 2 * rows * kRec;
+}
+
+template <int FMT, int WARPS>
 static cudaError_t launch_attend(const BlockDev &D, const BlockAttendArgs &a, int grid, int groups, cudaStream_t s) {
     cudaError_t e = once_per_device(0, [&] {
-        return cudaFuncSetAttribute(block_attend_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        return cudaFuncSetAttribute(block_attend_kernel<FMT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    block_attend_kernel<FMT, NT><<<grid, kThreads, kSmemBytes, s>>>(D, a, groups);
+    block_attend_kernel<FMT, WARPS><<<grid, 32 * WARPS, kSmemBytes, s>>>(D, a, groups);
     return cudaGetLastError();
 }
 
 cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArgs &a, int num_sms, cudaStream_t s) {
-    // 8 rows to a warp, or 16 where there are more than 8: both forms of S cost the same products, and 16 rows share
-    // the codes' way to fp16; 2 or 4 warps then share a ring
-    const int R = a.n_q * D.G, nt = R <= 8 ? 1 : 2, groups = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-    const int grid = num_sms < kMaxBlkCtas ? num_sms : kMaxBlkCtas;
-    constexpr int I = QEVICT_BLOCK_INT8, E = QEVICT_BLOCK_E4M3;
-    const cudaError_t e = fmt == I ? (nt == 1 ? launch_attend<I, 1>(D, a, grid, groups, s) : launch_attend<I, 2>(D, a, grid, groups, s))
-                                   : (nt == 1 ? launch_attend<E, 1>(D, a, grid, groups, s) : launch_attend<E, 2>(D, a, grid, groups, s));
+    const int R = a.n_q * D.G, groups = (R + 7) / 8, warps = groups == 1 ? kFewWarps : kManyWarps;
+    constexpr int I = QEVICT_BLOCK_INT8, E = QEVICT_BLOCK_E4M3, F = kFewWarps, M = kManyWarps;
+    const cudaError_t e = fmt == I ? (groups == 1 ? launch_attend<I, F>(D, a, num_sms, groups, s) : launch_attend<I, M>(D, a, num_sms, groups, s))
+                                   : (groups == 1 ? launch_attend<E, F>(D, a, num_sms, groups, s) : launch_attend<E, M>(D, a, num_sms, groups, s));
     if (e != cudaSuccess) return e;
     // blocks whose weights a CTA writes: 16 at a time, as many as leave about four CTAs to an SM
     const int64_t pairs = (int64_t)D.B * D.Hkv, each = pairs * D.NB / (4 * num_sms);
@@ -708,7 +673,7 @@ cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArg
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_join_kernel, D, a, grid * (kWarps / groups), 8 * nt * groups, tile);
+    return cudaLaunchKernelEx(&cfg, block_join_kernel, D, a, num_sms * (warps / groups), 8 * groups, tile);
 }
 
 }  // namespace qevict
