@@ -673,10 +673,13 @@ qevict_status qevict_decode_attention_static_scratch(qevict_cache *cache, int32_
  *
  * Lengths are the caller's: each call takes the positions it works on from the
  * caller's device memory (so a replayed graph follows them), and the layers of
- * a model can share them. A sequence may be set back by passing a smaller start
- * or length: exact down to the first token of the last full block (its rows,
- * too, are kept as bf16), as for drafted tokens that are rejected, but not behind
- * an eviction.
+ * a model can share them. What lies before a length has to have been appended.
+ * A sequence may be set back by passing a smaller start or length, as for drafted
+ * tokens that are rejected: with e the longest it has been since it was last
+ * filled from position 0, exactly down to position 64 (floor(e / 64) - 1) (the
+ * rows of the last full block are kept as bf16 too); after an eviction down to
+ * the first token of the open block. Further back the calls do not check, and
+ * the rows of the block that is cut are not those that were appended.
  *
  * Conventions, errors and status word are those of the other calls. Calls on one
  * layer are ordered; attention calls of one handle share its scratch, so they
@@ -750,10 +753,14 @@ qevict_status qevict_block_append(qevict_block_cache *cache, int32_t layer, cons
  *           over the queries of the mean over the head's Hq / Hkv query heads of
  *           its probabilities, added (accumulate nonzero) or written; others are
  *           left as they were. Needs score_queries >= n_q (INVALID_ARG).
- * A query that sees no token gets out 0, lse -inf, and gives no weight. Sums run in a
- * fixed order: every call gives the same bits. out, lse and weights must not
- * overlap one another or an input (INVALID_ARG). Waits are for the kernel's own
- * copies, as in qevict_span_attention. */
+ * A query that sees no token gets out 0, lse -inf, and gives no weight. One that holds
+ * an infinity or a NaN gets an undefined row (and weights of its KV head) and reaches
+ * no other. Sums run in a fixed order, in fp32: every call with the same lengths
+ * gives the same bits (how a sequence's tokens are divided over the GPU depends on
+ * the whole batch's). out, lse and weights must not overlap one another or an input
+ * (INVALID_ARG). Waits inside the kernel are for its own copies and have a limit of
+ * about two seconds; one that runs out sets QEVICT_ERR_TIMEOUT, and the outputs are
+ * then not valid. The kernel ends in any case. */
 qevict_status qevict_block_attention(qevict_block_cache *cache, int32_t layer, const void *q, int32_t n_q,
                                      const int32_t *kv_len, void *out, float *lse, float *weights,
                                      int32_t accumulate, void *stream);

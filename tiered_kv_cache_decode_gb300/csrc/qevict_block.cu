@@ -427,7 +427,7 @@ __device__ __forceinline__ void move_open(const BlockDev &D, const BlockDev &to,
 
 // Into another cache: a CTA for the keys and one for the values of each new block, the last ones for the open block.
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 6)
     block_move_kernel(const BlockDev D, const BlockDev to, const BlockEvictArgs a) {
     __shared__ ScaleRoom sm;
     const Place x(D);
