@@ -226,7 +226,7 @@ template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDev D, const BlockEvictArgs a, int ctas) {
     extern __shared__ __align__(16) uint32_t sel[];
     uint32_t *rep = sel, *hists = rep + kSelReps * kSelBins, *keys = hists + 2 * kSelBins;   // keys: CACHED, this CTA's
-    __shared__ uint32_t warp_sum[kSelWarps], found[2];
+    __shared__ uint32_t coarse[2][kSelBins / 32], found[2];   // coarse: sums of 32 bins
     __shared__ uint2 count[kSelWarps];
     const int64_t pair = blockIdx.x / ctas;
     const int rank = blockIdx.x % ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
                           i + 2 < cand ? weight_key(x.z) : ~0u, i + 3 < cand ? weight_key(x.w) : ~0u);
     };
     if (CACHED)
+#pragma unroll 4
         for (int i = lo + 4 * tid; i < hi; i += 4 * kSelThreads) *reinterpret_cast<uint4 *>(keys + i - lo) = load4(i);
     auto keys4 = [&](int i) { return CACHED ? *reinterpret_cast<const uint4 *>(keys + i - lo) : load4(i); };
     uint32_t want = a.keep - a.recent;   // of the candidates
@@ -271,42 +272,55 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
                     atomicAdd(&rep[((k[j] >> shift) & ((1u << bits) - 1)) * kSelReps + lane % kSelReps], 1u);
         }
         __syncthreads();
+        uint32_t *sums = coarse[pass & 1];
 #pragma unroll
         for (int i = tid; i < kSelBins; i += kSelThreads) {
             const uint4 x = reinterpret_cast<const uint4 *>(rep)[i];
-            hist[i] = x.x + x.y + x.z + x.w;
+            const uint32_t n = x.x + x.y + x.z + x.w, sum = __reduce_add_sync(~0u, n);
+            hist[i] = n;
+            if (lane == 0) sums[i / 32] = sum;
         }
         __syncwarp();
         cl_sync();
-        uint32_t n0 = 0, n1 = 0;   // bins 2 tid and 2 tid + 1 of all CTAs
+        if (warp == 0) {
+            // the 32 bins, from the top, in which the wanted key lies, then the bin: both from all CTAs' counts
+            uint32_t n0 = 0, n1 = 0;   // coarse bins 2 lane and 2 lane + 1
 #pragma unroll
-        for (int i = 0; i < kSelCtas; ++i) {
-            if (i >= ctas) continue;
-            const float2 x = cl_ld2(cl_addr(smem_u32(hist + 2 * tid), i));
-            n0 += __float_as_uint(x.x);
-            n1 += __float_as_uint(x.y);
-        }
-        // the bin, from the top, in which the wanted key lies
-        uint32_t from = n0 + n1;   // of the bins from this thread's on
+            for (int i = 0; i < kSelCtas; ++i) {
+                if (i >= ctas) continue;
+                const float2 x = cl_ld2(cl_addr(smem_u32(sums + 2 * lane), i));
+                n0 += __float_as_uint(x.x);
+                n1 += __float_as_uint(x.y);
+            }
+            auto from_here = [&](uint32_t n) {   // sum over this lane and those behind it
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const uint32_t x = __shfl_down_sync(~0u, from, s);
-            if (lane + s < 32) from += x;
-        }
-        if (lane == 0) warp_sum[warp] = from;
-        __syncthreads();
-        from += __reduce_add_sync(~0u, lane > warp ? warp_sum[lane] : 0u);
-        const uint32_t above = from - n0 - n1;
-        if (above < want && from >= want) {
-            const bool upper = above + n1 >= want;
-            found[0] = 2 * tid + (upper ? 1 : 0);
-            found[1] = want - above - (upper ? 0 : n1);
+                for (int s = 1; s < 32; s <<= 1) {
+                    const uint32_t x = __shfl_down_sync(~0u, n, s);
+                    if (lane + s < 32) n += x;
+                }
+                return n;
+            };
+            uint32_t above = from_here(n0 + n1) - n0 - n1;
+            bool upper = above + n1 >= want;
+            uint32_t rest = want - above - (upper ? 0 : n1);
+            const int l = 31 - __clz(__ballot_sync(~0u, above < want && above + n0 + n1 >= want));
+            const int group = __shfl_sync(~0u, 2 * lane + (upper ? 1 : 0), l);
+            rest = __shfl_sync(~0u, rest, l);
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < kSelCtas; ++i)
+                if (i < ctas) n += (uint32_t)cl_ldi(cl_addr(smem_u32(hist + 32 * group + lane), i));
+            above = from_here(n) - n;
+            if (above < rest && above + n >= rest) {
+                found[0] = 32 * group + lane;
+                found[1] = rest - above;
+            }
         }
         __syncthreads();
         prefix = prefix << bits | found[0];
         want = found[1];
     }
-    if (CACHED) __syncthreads();   // the keys, where no pass has met
+    __syncthreads();   // the keys, where no pass has met
     const int wlo = min(lo + warp * run, hi), whi = min(wlo + run, hi);
     uint32_t above = 0, equal = 0;
     for (int i = wlo + 4 * lane; i < whi; i += 128) {
@@ -332,31 +346,25 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
     for (int i0 = wlo; i0 < whi; i0 += 128) {
         const int i = i0 + 4 * lane;
         const uint4 k4 = i < whi ? keys4(i) : make_uint4(0, 0, 0, 0);
-        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-        uint32_t mine = 0;   // above in the low half, equal in the high one
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mine += i < whi ? (k[j] > prefix ? 1u : k[j] == prefix ? 1u << 16 : 0u) : 0u;
-        uint32_t sum = mine;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const uint32_t x = __shfl_up_sync(~0u, sum, s);
-            if (lane >= s) sum += x;
-        }
-        uint32_t up = above + ((sum - mine) & 0xffffu), eq = equal + ((sum - mine) >> 16);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w}, lower = (1u << lane) - 1;
+        uint32_t up = above, eq = equal;   // of the tokens before this lane's
+        bool is_up[4], is_eq[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (i >= whi) break;
-            if (k[j] > prefix) {
-                kept[up + min(eq, want)] = i + j;
-                ++up;
-            } else if (k[j] == prefix) {
-                if (eq < want) kept[up + eq] = i + j;
-                ++eq;
-            }
+            is_up[j] = i < whi && k[j] > prefix;
+            is_eq[j] = i < whi && k[j] == prefix;
+            const uint32_t mu = __ballot_sync(~0u, is_up[j]), me = __ballot_sync(~0u, is_eq[j]);
+            up += __popc(mu & lower);
+            eq += __popc(me & lower);
+            above += __popc(mu);
+            equal += __popc(me);
         }
-        sum = __shfl_sync(~0u, sum, 31);
-        above += sum & 0xffffu;
-        equal += sum >> 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (is_up[j] || (is_eq[j] && eq < want)) kept[up + min(eq, want)] = i + j;
+            up += is_up[j];
+            eq += is_eq[j];
+        }
     }
     __syncwarp();
     cl_sync();   // no CTA leaves while others read its counts
