@@ -72,7 +72,7 @@ struct BlockAttendArgs {
     int accumulate;
     // scratch of the handle
     float *part;
-    float *logits;                   // [pair][NB][rows][64] where weights are wanted
+    float *logits;                   // [pair][NB][8][rows][8 tokens] where weights are wanted
     float *row_lse;                  // [pair][rows], log2 domain
 };
 

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
         Rows r;
         r.clear();
         for (int u = u0; u < u1; ++u) {
-            float *logits = a.weights && row < R ? a.logits + ((pair * D.NB + min(u, nb)) * R + row) * kBlk + 2 * q : nullptr;
+            float *logits = a.weights && row < R ? a.logits + (pair * D.NB + min(u, nb)) * R * kBlk + row * 8 + 2 * q : nullptr;
             if (u < nb) {
                 const float2 sc = __ldg(D.scale + pair * D.NB + u);
                 uint32_t base = wait_half();
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                 }
                 if (logits) {
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) *reinterpret_cast<float2 *>(logits + 8 * t) = make_float2(x[t][0], x[t][1]);
+                    for (int t = 0; t < 8; ++t) *reinterpret_cast<float2 *>(logits + t * R * 8) = make_float2(x[t][0], x[t][1]);
                 }
                 if (u * kBlk + kBlk - 1 > len - a.n_q) {
 #pragma unroll
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                 if (logits) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        *reinterpret_cast<float2 *>(logits + (u - nb) * kOpenHalf + 8 * t) = make_float2(x[t][0], x[t][1]);
+                        *reinterpret_cast<float2 *>(logits + ((u - nb) * 4 + t) * R * 8) = make_float2(x[t][0], x[t][1]);
                 }
                 float top = -INFINITY;
 #pragma unroll
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
     for (int j = j0 + (tid >> 4); j < j0 + tile; j += 2 * kEach) {
         const int pos[2] = {j * kBlk + t, j + kEach < j0 + tile ? (j + kEach) * kBlk + t : len};
         if (pos[0] >= len) return;
-        const float4 *g = reinterpret_cast<const float4 *>(a.logits + (pair * D.NB + j) * R * kBlk + t);
+        const float4 *g = reinterpret_cast<const float4 *>(a.logits + (pair * D.NB + j) * R * kBlk + (t >> 3) * R * 8 + (t & 7));
         float w[2][4] = {};
         for (int r0 = 0; r0 < R; r0 += 4) {
             float4 y[2][4];
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
             for (int b2 = 0; b2 < 2; ++b2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (r0 + i < R && pos[b2] < len) y[b2][i] = __ldcs(g + (b2 * kEach * R + r0 + i) * (kBlk / 4));
+                    if (r0 + i < R && pos[b2] < len) y[b2][i] = __ldcs(g + b2 * kEach * R * (kBlk / 4) + (r0 + i) * 2);
 #pragma unroll
             for (int b2 = 0; b2 < 2; ++b2)
 #pragma unroll
