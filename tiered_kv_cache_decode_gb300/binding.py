@@ -617,15 +617,23 @@ class BlockCache(_Handle):
         Returns (out bf16, lse fp32 [B][Hq][n_q] or None). weights: each token's probabilities, summed over the
         queries and averaged over the query heads of its KV head, are added (or written)."""
         n_q = self._dense(q, self.Hq, "q")
-        if out is None:
-            out = self._new(q, stream)
-        if lse is None and want_lse:
-            lse = self._new(q, stream, torch.float32, (self.B, self.Hq, n_q))
         side, f32 = self._side, torch.float32
-        rc = self.lib.qevict_block_attention(
-            self.handle, layer, q.data_ptr(), n_q, side(kv_len, self._per_seq, torch.int32, "kv_len"),
-            side(out, q.shape, torch.bfloat16, "out"), side(lse, (self.B, self.Hq, n_q), f32, "lse"),
-            side(weights, self._per_token, f32, "weights"), 1 if accumulate else 0, self._raw_stream(stream))
+        at = side(kv_len, self._per_seq, torch.int32, "kv_len")
+        w = None if weights is None else side(weights, self._per_token, f32, "weights")
+        if out is None:   # what the call makes itself is not checked again
+            out = self._new(q, stream)
+            o = out.data_ptr()
+        else:
+            o = side(out, q.shape, torch.bfloat16, "out")
+        if lse is not None:
+            ls = side(lse, (self.B, self.Hq, n_q), f32, "lse")
+        elif want_lse:
+            lse = self._new(q, stream, f32, (self.B, self.Hq, n_q))
+            ls = lse.data_ptr()
+        else:
+            ls = None
+        rc = self.lib.qevict_block_attention(self.handle, layer, q.data_ptr(), n_q, at, o, ls, w, 1 if accumulate else 0,
+                                             self._raw_stream(stream))
         if rc:
             self._check(rc)
         return out, lse
