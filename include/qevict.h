@@ -790,7 +790,7 @@ qevict_status qevict_block_read(qevict_block_cache *cache, int32_t layer, const 
  *  weights  fp32 [batch][Hkv][capacity], device, 16-byte aligned.
  *  weights_out  fp32 [batch][Hkv][capacity of the destination], or NULL: the weights
  *           of the tokens that stay, in their new places; places behind them are
- *           left as they were. May be `weights` itself where the capacities agree.
+ *           left as they were. In place it may be `weights` itself.
  *  new_len  int32 [batch], device, written: min(c, keep) + kv_len - c.
  *  kept     int32 [batch][Hkv][keep], device, written: the old positions of the tokens
  *           in full blocks, then -1.

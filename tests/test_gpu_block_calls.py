@@ -438,3 +438,42 @@ print("same bits")
 def test_first_calls_of_a_process_are_captured(sizes):
     r = subprocess.run([sys.executable, "-c", FIRST % sizes], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same bits" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("lens", [[130, 64], [500, 40]])
+def test_in_place_eviction_with_weights_elsewhere(lens):
+    """In place, the weights go to another tensor also where nothing leaves; into another layer they may not go to their
+    own (the moves are in no order)."""
+    B, Hkv, keep = 2, 2, 128
+    c = binding.BlockCache(B, 2, Hkv, Hkv, 512)
+    c.append(0, rand(1, B, 500, Hkv, D).cuda(), rand(2, B, 500, Hkv, D).cuda())
+    w = torch.rand(B, Hkv, c.capacity, generator=torch.Generator().manual_seed(1)).cuda()
+    out, kept_w = torch.full_like(w, 7.0), w.clone()
+    new_len, kept = c.evict(0, ints(*lens), keep, 10, w, weights_out=out)
+    assert torch.equal(w, kept_w)
+    for b, L in enumerate(lens):
+        full = L // T * T
+        for h in range(Hkv):
+            at = U.select(w[b, h].cpu().numpy(), full, keep, 10)
+            want = torch.cat([w[b, h][torch.from_numpy(at).cuda()], w[b, h, full:L]])
+            assert torch.equal(out[b, h, :len(want)], want) and torch.all(out[b, h, len(want):] == 7.0)
+            assert int(new_len[b]) == len(want)
+    with pytest.raises(binding.QevictError, match="INVALID_ARG"):
+        c.evict(0, ints(*lens), keep, 10, w, into=c, into_layer=1, weights_out=w)
+    assert c.status() == 0
+
+
+def test_attention_and_eviction_clamp_lengths():
+    B, Hq, Hkv, n = 3, 8, 2, 320
+    c = binding.BlockCache(B, 1, Hq, Hkv, n)
+    k = rand(1, B, n, Hkv, D).cuda()
+    c.append(0, k, k)
+    q = rand(2, B, 1, Hq, D).cuda()
+    got, want = c.attend(0, q, ints(-7, 2 ** 31 - 1, n + 1)), c.attend(0, q, ints(0, n, n))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    d = binding.BlockCache(B, 2, Hkv, Hkv, 128)
+    w = torch.rand(B, Hkv, n, device="cuda")
+    got = c.evict(0, ints(-2 ** 31, 2 ** 31 - 1, n + 64), 64, 3, w, into=d)
+    want = c.evict(0, ints(0, n, n), 64, 3, w, into=d, into_layer=1)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(d.read(0, got[0], 128), d.read(1, want[0], 128)))

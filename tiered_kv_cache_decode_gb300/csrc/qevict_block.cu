@@ -474,6 +474,9 @@ __global__ void __cluster_dims__(kMoveCtas, 1, 1) __launch_bounds__(kThreads)
             if (j * kBlk < kept) store_moved<FMT>(D, pair, kv, j, m, w, sm);
         }
     }
+    if (c <= kept && kv == 0 && a.weights_out && a.weights_out != a.weights)
+        for (int i = rank * kThreads + threadIdx.x; i < c; i += kMoveCtas * kThreads)
+            a.weights_out[pair * D.capacity + i] = a.weights[pair * D.capacity + i];
     // the last round's reads are behind a barrier: the open block's weights may go where they lay
     if (rank == 0 && kv == 0) move_open(D, D, a, pair, len, c, kept);
 }

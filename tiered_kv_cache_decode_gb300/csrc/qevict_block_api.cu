@@ -286,7 +286,7 @@ qevict_status qevict_block_evict(qevict_block_cache *c, int32_t layer, const int
                          "kv_len, weights_out, new_len and kept");
     if (st) return st;
     const int64_t B = c->cfg.batch, pairs = B * c->cfg.num_kv_heads;
-    const bool own = weights_out == weights && to->capacity == c->capacity;
+    const bool own = weights_out == weights && to == c && to_layer == layer;   // elsewhere tokens move in no order
     const Extent x[5] = {{kv_len, B * 4, "kv_len"}, {weights, pairs * (int64_t)c->capacity * 4, "weights"},
                          {own ? nullptr : weights_out, pairs * (int64_t)to->capacity * 4, "weights_out"},
                          {new_len, B * 4, "new_len"}, {kept, pairs * keep * 4, "kept"}};
