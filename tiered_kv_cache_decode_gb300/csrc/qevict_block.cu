@@ -67,8 +67,8 @@ struct Place {
 inline dim3 places(const BlockDev &D, int blocks) { return dim3(2u * D.Hkv, (unsigned)blocks, (unsigned)D.B); }
 
 // One CTA takes the keys or the values of one block of one (sequence, KV head). Thread: channels 8 c .. 8 c + 7 of rows
-// r + 16 i. Memory-bound: every row is read once and its codes written once (keys and values in CTAs of their own: 8
-// CTAs to an SM, 128 KiB of loads in flight).
+// r + 16 i. Memory-bound: every row is read once and its codes written once (keys and values in CTAs of their own, six
+// to an SM; with both in one CTA 53 us). A 32K prompt of 8 KV heads takes 34 us, 5.9 TB/s.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) block_append_kernel(const BlockDev D, const BlockAppendArgs a) {
     __shared__ ScaleRoom sm;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) block_append_kernel(const BlockDev D
     }
 }
 
-// One CTA: the rows that lie in one block of one (sequence, KV head).
+// One CTA: the keys or the values that lie in one block of one (sequence, KV head). 32K tokens of 8 KV heads: 29 us, 6.8 TB/s.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) block_read_kernel(const BlockDev D, const BlockReadArgs a) {
     const Place x(D);
@@ -221,7 +221,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // bits, the CTAs' histograms added in distributed shared memory; then each warp counts its run's keys above it and equal to
 // it, and with the counts of all warps before it gives every kept token its rank. Bound by latency: one read of the weights
 // (then kept in shared memory: CACHED), three passes of one cluster barrier each, one more for the counts. Short contexts
-// take a cluster of one CTA, whose barrier is the CTA's own.
+// take a cluster of one CTA, whose barrier is the CTA's own. 2K tokens 7 us, 32 pairs of 32K 15, 8 of 128K 19.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDev D, const BlockEvictArgs a, int ctas) {
     extern __shared__ __align__(16) uint32_t sel[];
@@ -434,6 +434,8 @@ __device__ __forceinline__ void move_open(const BlockDev &D, const BlockDev &to,
 }
 
 // Into another cache: a CTA for the keys and one for the values of each new block, the last ones for the open block.
+// 4 x 32K tokens of 8 KV heads to 6.5K: 28 us, 3.8 TB/s, bound by instructions (0.69 of the issue slots) and by the chain
+// of a block: positions, codes, two barriers (with the next block's loads under it 35, a warp to a block 32 us).
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 6)
     block_move_kernel(const BlockDev D, const BlockDev to, const BlockEvictArgs a) {

@@ -2,7 +2,6 @@
 // points of qevict_block.cu and qevict_block_attend.cu.
 #pragma once
 
-#include "qevict_div.cuh"
 #include "qevict_internal.cuh"
 
 namespace qevict {
