@@ -225,7 +225,11 @@ class _Handle:
     def _tokens(self, t, heads, what):
         """(tokens, elements between consecutive tokens) of a bf16 [B][n][heads][128] (or, for one token,
         [B][heads][128]) tensor on the cache's device whose tokens are evenly spaced and dense inside."""
-        sh, st, B = t.shape, t.stride(), self.B
+        sh, B = t.shape, self.B
+        if t.is_contiguous() and len(sh) == 4 and sh[0] == B and sh[1] and sh[2] == heads and sh[3] == HEAD_DIM and \
+                t.dtype is torch.bfloat16 and t.device == self._dev:
+            return sh[1], heads * HEAD_DIM
+        st = t.stride()
         if len(sh) == 3:
             sh, st = (sh[0], 1, sh[1], sh[2]), (st[0], st[0], st[1], st[2])
         if len(sh) != 4 or sh[0] != B or sh[2] != heads or sh[3] != HEAD_DIM or t.dtype is not torch.bfloat16 or \
@@ -621,14 +625,15 @@ class BlockCache(_Handle):
         at = side(kv_len, self._per_seq, torch.int32, "kv_len")
         w = None if weights is None else side(weights, self._per_token, f32, "weights")
         if out is None:   # what the call makes itself is not checked again
-            out = self._new(q, stream)
+            out = torch.empty_like(q) if stream is None else self._new(q, stream)   # q is dense
             o = out.data_ptr()
         else:
             o = side(out, q.shape, torch.bfloat16, "out")
         if lse is not None:
             ls = side(lse, (self.B, self.Hq, n_q), f32, "lse")
         elif want_lse:
-            lse = self._new(q, stream, f32, (self.B, self.Hq, n_q))
+            shape = (self.B, self.Hq, n_q)
+            lse = torch.empty(shape, dtype=f32, device=self._dev) if stream is None else self._new(q, stream, f32, shape)
             ls = lse.data_ptr()
         else:
             ls = None
@@ -672,7 +677,7 @@ class BlockCache(_Handle):
         if at is None or w is None:
             raise ValueError("kv_len and weights must be given")
         if new_len is None:
-            new_len = self._new(kv_len, stream, i32, self._per_seq)
+            new_len = torch.empty_like(kv_len) if stream is None else self._new(kv_len, stream)
         if kept is None:
             kept = self._new(kv_len, stream, i32, (self.B, self.Hkv, max(keep, 0)))
         rc = self.lib.qevict_block_evict(
