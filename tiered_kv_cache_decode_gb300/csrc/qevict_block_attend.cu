@@ -480,14 +480,13 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
     }
 }
 
-// Behind the attention: the first CTAs turn the logits that it left into the tokens' weights, `tile` blocks of a pair
-// each; then pairs x rows CTAs add up the parts of the pairs that lie in several runs, one row each.
-__global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room, int tile) {
+// Behind the attention: the first CTAs turn the logits that it left into the tokens' weights, `tiles` CTAs to a pair, each
+// an equal share of its blocks; then pairs x rows CTAs add up the parts of the pairs that lie in several runs, one row each.
+__global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room, int tiles) {
     __shared__ float red[kWarps][kRec];
     __shared__ float lse[kMaxBlkQueries * kMaxG];   // of the pair's rows, log2 domain
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.n_q * D.G;
     const int64_t pairs = (int64_t)D.B * D.Hkv;
-    const int tiles = a.weights ? (D.NB + tile - 1) / tile : 0;
     const bool join = blockIdx.x >= pairs * tiles;
     const int64_t x = join ? blockIdx.x - pairs * tiles : blockIdx.x, pair = join ? x / R : x / tiles;
     const int b = (int)(pair / D.Hkv), h = (int)(pair % D.Hkv), len = blk_len(D, a.kv_len, b), n = units_of(len);
@@ -562,8 +561,11 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
         if (tid == 0 && out_lse) *out_lse = row_lse(m, l) * 0.6931471805599453f;
         return;
     }
-    const int j0 = (int)(x % tiles) * tile;
-    if (j0 * kBlk >= len) return;
+    constexpr int kEach = kThreads / 16;   // blocks at a time
+    const int blocks = (len + kBlk - 1) / kBlk, even = (blocks + tiles - 1) / tiles;
+    const int share = even <= kEach ? kEach : (even + 2 * kEach - 1) / (2 * kEach) * (2 * kEach);   // two at a time below
+    const int j0 = (int)(x % tiles) * share, j1 = min(j0 + share, blocks);
+    if (j0 >= blocks) return;
     // their log-sum-exps: half a warp to a row, a pass over its parts with a running maximum
     for (int row = tid >> 4; row < ((R + 1) & ~1); row += kThreads / 16) {   // both halves of a warp go round alike
         float m = -INFINITY, l = 0.f;
@@ -587,11 +589,10 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
     }
     __syncthreads();
     // four tokens of each of two blocks to a thread at a time, eight loads on their way
-    constexpr int kEach = kThreads / 16;
     const int t = 4 * (tid & 15);
     const float inv = 1.f / D.G;
-    for (int j = j0 + (tid >> 4); j < j0 + tile; j += 2 * kEach) {
-        const int pos[2] = {j * kBlk + t, j + kEach < j0 + tile ? (j + kEach) * kBlk + t : len};
+    for (int j = j0 + (tid >> 4); j < j1; j += 2 * kEach) {
+        const int pos[2] = {j * kBlk + t, j + kEach < j1 ? (j + kEach) * kBlk + t : len};
         if (pos[0] >= len) return;
         const float4 *g = reinterpret_cast<const float4 *>(a.logits + (pair * D.NB + j) * R * kBlk + (t >> 3) * R * 8 + (t & 7));
         float w[2][4] = {};
@@ -659,10 +660,10 @@ cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArg
     const cudaError_t e = fmt == I ? (groups == 1 ? launch_attend<I, F>(D, a, num_sms, groups, s) : launch_attend<I, M>(D, a, num_sms, groups, s))
                                    : (groups == 1 ? launch_attend<E, F>(D, a, num_sms, groups, s) : launch_attend<E, M>(D, a, num_sms, groups, s));
     if (e != cudaSuccess) return e;
-    // blocks whose weights a CTA writes: 16 at a time, as many as leave about four CTAs to an SM
-    const int64_t pairs = (int64_t)D.B * D.Hkv, each = pairs * D.NB / (4 * num_sms);
-    const int tile = each < 16 ? 16 : each > 64 ? 64 : (int)(each + 15) & ~15;
-    const int64_t ctas = pairs * R + (a.weights ? pairs * ((D.NB + tile - 1) / tile) : 0);
+    // CTAs that write weights: about four to an SM whatever the capacity, none for fewer than 16 blocks
+    const int64_t pairs = (int64_t)D.B * D.Hkv, many = (4 * (int64_t)num_sms + pairs - 1) / pairs, most = (D.NB + 15) / 16;
+    const int tiles = a.weights ? (int)(many < most ? many : most) : 0;
+    const int64_t ctas = pairs * R + pairs * tiles;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     // its launch overlaps the attention; it waits for that kernel's end before it reads what it left
     cudaLaunchConfig_t cfg{};
@@ -674,7 +675,7 @@ cudaError_t launch_block_attend(const BlockDev &D, int fmt, const BlockAttendArg
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_join_kernel, D, a, num_sms * (warps / groups), 8 * groups, tile);
+    return cudaLaunchKernelEx(&cfg, block_join_kernel, D, a, num_sms * (warps / groups), 8 * groups, tiles);
 }
 
 }  // namespace qevict
