@@ -746,8 +746,8 @@ qevict_status qevict_block_append(qevict_block_cache *cache, int32_t layer, cons
  *  kv_len   int32 [batch], device; clamped to [0, capacity].
  *  out      bf16 [batch][n_q][Hq][128], 16-byte aligned: softmax(q K^T / sqrt(128)) V
  *           over what the cache stands for. fp32 sums; probabilities enter their
- *           product with the codes as fp16 (relative to the largest of their block
- *           so far), with bf16 rows as two bf16 parts.
+ *           product with the codes as fp16 (11 bits down to 2^-29 of the largest
+ *           so far, 2^-40 of it at most below), with bf16 rows as two bf16 parts.
  *  lse      fp32 [batch][Hq][n_q] or NULL: log(sum(exp(q K^T / sqrt(128)))).
  *  weights  fp32 [batch][Hkv][capacity] or NULL: token j < kv_len[b] gets the sum
  *           over the queries of the mean over the head's Hq / Hkv query heads of

@@ -346,3 +346,31 @@ def test_eviction(fmt, Hkv, lens, keep, recent, ties, place):
                     full = torch.from_numpy(U.held(rows[:e - s].float().numpy().transpose(1, 0, 2), fmt)).bfloat16()
                     rows[:e - s] = full.transpose(0, 1)
                 assert torch.equal(a[b, s:n[b] + m].cpu(), rows) and torch.equal(a[b, :s], p[b, :s])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_keeps_what_a_sink_outweighs(fmt):
+    """One token outweighs each of 60,000 others by e^16 or e^17 (2^-24.5); together they have 0.3 to 0.7 % of the mass, and
+    values 512 times the one's, so that half of the output or more is theirs. Tolerance: half a step of the output, of
+    each probability 2^-12 (2^-40 of the largest below 2^-29 of it)."""
+    n = 60000
+    c = binding.BlockCache(1, 1, 2, 1, n, fmt)
+    k, v = torch.zeros(1, n, 1, D), torch.zeros(1, n, 1, D)
+    k[:, :, :, 0] = 1.0
+    k[:, 64 * 7, :, 0] = 2.0
+    v[:, :, :, :64] = 512.0
+    v[:, 64 * 7:64 * 8, :, :64] = 1.0
+    k[:, 64 * 7 + 1:64 * 8, :, 0] = 1.0
+    k, v = k.bfloat16(), v.bfloat16()
+    q = torch.zeros(1, 1, 2, D)
+    q[..., 0] = torch.tensor([17.0, 16.0]) * D ** 0.5
+    q = q.bfloat16()
+    ref = U.Cache(1, 1, c.capacity, fmt)
+    c.append(0, k.cuda(), v.cuda())
+    ref.append(k, v, [0], [n])
+    out, _ = c.attend(0, q.cuda(), ints([n]))
+    want, _, _, mag, low, big = U.attention(f64(q[0]), ref.values("k", 0, n), ref.values("v", 0, n))
+    assert np.all(want[0, :, :64] > 1.5)   # the others' part is as large as the sink's at least
+    off = 2.0 ** -20 * big
+    err = np.abs(f64(out[0]) - want)
+    assert np.all(err <= 2.0 ** -8 * np.abs(want) + (2.0 ** -12 + 2 * off) * mag + 2.0 ** -40 * low + 1e-6)

@@ -160,7 +160,9 @@ struct Rows {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     }
-    // moves the maximum; what the exponentials are taken against
+    // moves the maximum; what the exponentials are taken against: they reach up to 2^15, so that in fp16 a probability keeps
+    // its 11 bits down to 2^-29 of the largest, and sums and outputs are in that unit
+    static constexpr float kLift = 15.f;
     __device__ __forceinline__ float raise(float top, int q) {
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -178,7 +180,7 @@ struct Rows {
             }
             m = m1;
         }
-        return ref;
+        return ref - kLift;
     }
 };
 
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                 for (int t = 0; t < 8; ++t) {
                     const float p0 = tc_ex2(x[t][0] - ref), p1 = tc_ex2(x[t][1] - ref);
                     r.l += p0 + p1;
-                    p[t] = bits(__floats2half2_rn(p0, p1));   // against the running maximum: 2^-12 of a term
+                    p[t] = bits(__floats2half2_rn(p0, p1));   // off by 2^-12 of a term
                 }
                 base = wait_half();
                 const uint32_t v0 = base + lane * kHeadDim;
@@ -443,11 +445,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (q == 0 && row < R) {
             if (whole) {
-                const float lse = row_lse(r.m, l);
+                const float lse = row_lse(r.m - Rows::kLift, l);
                 if (a.lse) a.lse[((int64_t)b * D.Hq + h * D.G + row % D.G) * a.n_q + i_q] = lse * 0.6931471805599453f;
                 if (a.weights) a.row_lse[pair * R + row] = lse;
             } else {
-                *reinterpret_cast<float2 *>(part + row * kRec + kHeadDim) = make_float2(r.m, l);
+                *reinterpret_cast<float2 *>(part + row * kRec + kHeadDim) = make_float2(r.m - Rows::kLift, l);
             }
         }
 #pragma unroll
