@@ -150,19 +150,38 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
 }
 // What a warp keeps of its 8 rows: lane (n, q) = (lane / 4, lane % 4) has the maximum (log2 domain) of row n and its own
 // share of its sum, and of O^T rows 2 q, 2 q + 1 of channels 16 i + 2 n (o[i][0..1]) and 16 i + 2 n + 1 (o[i][2..3]).
+// Sums and outputs are relative to the maximum, times 2^15 while no block's scale (or 32 bf16 rows' product) reaches 2^64,
+// so that the smallest values keep their bits, and times 2^-40 from the first that does, so that no sum of up to 2^21
+// finite values passes fp32.
 struct Rows {
-    float m, l, o[8][4];
+    static constexpr float kLarge = 0x1p64f, kLess = 0x1p-55f;
+    float m, l, unit, o[8][4];   // unit: 2^-15 of that factor, 1 or kLess
     __device__ __forceinline__ void clear() {
         m = -INFINITY;
         l = 0.f;
+        unit = 1.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     }
-    // moves the maximum; what the exponentials are taken against: they reach up to 2^15, so that in fp16 a probability keeps
-    // its 11 bits down to 2^-29 of the largest, and sums and outputs are in that unit
-    static constexpr float kLift = 15.f;
+    // Powers of two that the probabilities carry into their product. In fp16 they reach up to 2^15, so that one keeps its
+    // 11 bits down to 2^-29 of the largest; with bf16 rows, whose exponent is fp32's, up to 2^-8, so that 32 of them times
+    // the largest values stay finite.
+    static constexpr float kLift = 15.f, kDrop = 8.f;
+    __device__ __forceinline__ float of_rows() const { return 0x1p23f * unit; }
+    // what sums and outputs are relative to, log2 domain
+    __device__ __forceinline__ float base() const { return m + (unit == 1.f ? -15.f : 40.f); }
+    __device__ __forceinline__ void less() {
+        if (unit != 1.f) return;
+        unit = kLess;
+        l *= kLess;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] *= kLess;
+    }
+    // moves the maximum; what the exponentials are taken against
     __device__ __forceinline__ float raise(float top, int q) {
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -180,7 +199,7 @@ struct Rows {
             }
             m = m1;
         }
-        return ref - kLift;
+        return ref;
     }
 };
 
@@ -339,14 +358,18 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                 float top = x[0][0];
 #pragma unroll
                 for (int t = 0; t < 8; ++t) top = max3(top, x[t][0], x[t][1]);
-                const float ref = r.raise(top, q);
+                const float ref = r.raise(top, q) - Rows::kLift;
+                if (sc.y >= Rows::kLarge) r.less();
                 uint32_t p[8];
+                float sum = 0.f;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const float p0 = tc_ex2(x[t][0] - ref), p1 = tc_ex2(x[t][1] - ref);
-                    r.l += p0 + p1;
+                    sum += p0 + p1;
                     p[t] = bits(__floats2half2_rn(p0, p1));   // off by 2^-12 of a term
                 }
+                r.l = fmaf(sum, r.unit, r.l);
+                const float vs = sc.y * r.unit;
                 base = wait_half();
                 const uint32_t v0 = base + lane * kHeadDim;
 #pragma unroll
@@ -370,7 +393,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) r.o[i + e][g] = fmaf(c[e][g], sc.y, r.o[i + e][g]);
+                        for (int g = 0; g < 4; ++g) r.o[i + e][g] = fmaf(c[e][g], vs, r.o[i + e][g]);
                 }
                 done_half();
             } else {
@@ -405,15 +428,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                         if (t0 + 8 * t + 2 * q + e > last) x[t][e] = -INFINITY;
                         top = fmaxf(top, x[t][e]);
                     }
-                const float ref = r.raise(top, q);
+                const float ref = r.raise(top, q) + Rows::kDrop;
                 uint32_t p[4], pl[4];   // each probability as two bf16 parts
+                float sum = 0.f;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const float p0 = tc_ex2(x[t][0] - ref), p1 = tc_ex2(x[t][1] - ref);
-                    r.l += p0 + p1;
+                    sum += p0 + p1;
                     p[t] = pack_bf(p0, p1);
                     pl[t] = pack_bf(p0 - __uint_as_float(p[t] << 16), p1 - __uint_as_float(p[t] & 0xffff0000u));
                 }
+                r.l = fmaf(sum, r.of_rows(), r.l);
                 base = wait_half();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -424,14 +449,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                     mma<true>(c, va.z, vb.z, va.w, vb.w, p[2], p[3]);
                     mma<true>(c, va.x, vb.x, va.y, vb.y, pl[0], pl[1]);
                     mma<true>(c, va.z, vb.z, va.w, vb.w, pl[2], pl[3]);
+                    const float top_c = max3(fmaxf(fabsf(c[0]), fabsf(c[1])), fabsf(c[2]), fabsf(c[3]));
+                    if (__any_sync(~0u, top_c >= Rows::kLarge)) r.less();
+                    const float back = r.of_rows();
                     // c: channels n and 8 + n of the 16; the accumulators hold 2 n and 2 n + 1
                     const int s0 = ((2 * n) & 7) * 4 + q, s1 = s0 + 4;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float lo0 = __shfl_sync(~0u, c[e], s0), hi0 = __shfl_sync(~0u, c[2 + e], s0);
                         const float lo1 = __shfl_sync(~0u, c[e], s1), hi1 = __shfl_sync(~0u, c[2 + e], s1);
-                        r.o[i][e] += n < 4 ? lo0 : hi0;
-                        r.o[i][2 + e] += n < 4 ? lo1 : hi1;
+                        r.o[i][e] = fmaf(n < 4 ? lo0 : hi0, back, r.o[i][e]);
+                        r.o[i][2 + e] = fmaf(n < 4 ? lo1 : hi1, back, r.o[i][2 + e]);
                     }
                 }
                 done_half();
@@ -445,11 +473,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (q == 0 && row < R) {
             if (whole) {
-                const float lse = row_lse(r.m - Rows::kLift, l);
+                const float lse = row_lse(r.base(), l);
                 if (a.lse) a.lse[((int64_t)b * D.Hq + h * D.G + row % D.G) * a.n_q + i_q] = lse * 0.6931471805599453f;
                 if (a.weights) a.row_lse[pair * R + row] = lse;
             } else {
-                *reinterpret_cast<float2 *>(part + row * kRec + kHeadDim) = make_float2(r.m - Rows::kLift, l);
+                *reinterpret_cast<float2 *>(part + row * kRec + kHeadDim) = make_float2(r.base(), l);
             }
         }
 #pragma unroll
