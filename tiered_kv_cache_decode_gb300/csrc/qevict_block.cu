@@ -226,8 +226,9 @@ template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDev D, const BlockEvictArgs a, int ctas) {
     extern __shared__ __align__(16) uint32_t sel[];
     uint32_t *rep = sel, *hists = rep + kSelReps * kSelBins, *keys = hists + 2 * kSelBins;   // keys: CACHED, this CTA's
-    __shared__ uint32_t coarse[2][kSelBins / 32], found[2];   // coarse: sums of 32 bins
+    __shared__ uint2 coarse[2][kSelBins / 64];   // sums of 32 bins, two at a time
     __shared__ uint2 count[kSelWarps];
+    __shared__ uint32_t found[2];
     const int64_t pair = blockIdx.x / ctas;
     const int rank = blockIdx.x % ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
                     atomicAdd(&rep[((k[j] >> shift) & ((1u << bits) - 1)) * kSelReps + lane % kSelReps], 1u);
         }
         __syncthreads();
-        uint32_t *sums = coarse[pass & 1];
+        uint32_t *sums = reinterpret_cast<uint32_t *>(coarse[pass & 1]);
 #pragma unroll
         for (int i = tid; i < kSelBins; i += kSelThreads) {
             const uint4 x = reinterpret_cast<const uint4 *>(rep)[i];
@@ -288,9 +289,9 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
 #pragma unroll
             for (int i = 0; i < kSelCtas; ++i) {
                 if (i >= ctas) continue;
-                const float2 x = cl_ld2(cl_addr(smem_u32(sums + 2 * lane), i));
-                n0 += __float_as_uint(x.x);
-                n1 += __float_as_uint(x.y);
+                const uint2 x = cl_pair(&coarse[pass & 1][lane], i);
+                n0 += x.x;
+                n1 += x.y;
             }
             auto from_here = [&](uint32_t n) {   // sum over this lane and those behind it
 #pragma unroll
@@ -337,9 +338,9 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDe
 #pragma unroll
     for (int i = 0; i < kSelCtas; ++i) {   // of the warps before this one
         if (i > rank || (i == rank && lane >= warp)) continue;
-        const float2 x = cl_ld2(cl_addr(smem_u32(&count[lane]), i));
-        above += __float_as_uint(x.x);
-        equal += __float_as_uint(x.y);
+        const uint2 x = cl_pair(&count[lane], i);
+        above += x.x;
+        equal += x.y;
     }
     above = __reduce_add_sync(~0u, above);
     equal = __reduce_add_sync(~0u, equal);

@@ -30,6 +30,7 @@ constexpr int kHalf = kBlkBytes / 2;               // what one copy brings: K or
 // evenly (the slowest took 17 % longer than the median for as many bytes: 4 x 128K 175 us against 158), with 1 it idles (190).
 constexpr int kSlots = 16;
 constexpr int kRec = kHeadDim + 4;                 // floats of a row of a partial result: output, maximum, sum
+static_assert(kRec % 4 == 0, "rows of whole float4");
 constexpr int kSmemBytes = kSlots * kHalf + 2 * kSlots * 8 + 16;
 
 __device__ __forceinline__ int units_of(int len) { return (len >> 6) + (((len & (kBlk - 1)) + kOpenHalf - 1) / kOpenHalf); }
@@ -513,7 +514,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
 // Behind the attention: the first CTAs turn the logits that it left into the tokens' weights, `tiles` CTAs to a pair, each
 // an equal share of its blocks; then pairs x rows CTAs add up the parts of the pairs that lie in several runs, one row each.
 __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev D, const BlockAttendArgs a, int max_runs, int room, int tiles) {
-    __shared__ float red[kWarps][kRec];
+    __shared__ float4 red4[kWarps][kRec / 4];
+    float (*red)[kRec] = reinterpret_cast<float (*)[kRec]>(red4);
     __shared__ float lse[kMaxBlkQueries * kMaxG];   // of the pair's rows, log2 domain
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.n_q * D.G;
     const int64_t pairs = (int64_t)D.B * D.Hkv;
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
                 o.w = fmaf(y[e].w, f, o.w);
             }
         }
-        *(reinterpret_cast<float4 *>(red[warp]) + lane) = o;
+        red4[warp][lane] = o;
         if (lane == 0) {
             red[warp][kHeadDim] = m;
             red[warp][kHeadDim + 1] = l;

@@ -258,6 +258,13 @@ __device__ __forceinline__ float2 cl_ld2(uint32_t addr) {
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
+// the pair at `p` of CTA `rank`; its type has to promise the alignment that the load needs
+template <class T>
+__device__ __forceinline__ uint2 cl_pair(const T *p, uint32_t rank) {
+    static_assert(sizeof(T) == 8 && alignof(T) >= 8, "a pair of words on an 8-byte boundary");
+    const float2 x = cl_ld2(cl_addr(smem_u32(p), rank));
+    return make_uint2(__float_as_uint(x.x), __float_as_uint(x.y));
+}
 __device__ __forceinline__ float cl_ld1(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
