@@ -716,7 +716,8 @@ typedef struct qevict_block_cache qevict_block_cache;
 qevict_status qevict_block_create(const qevict_block_config *config, const qevict_allocator *allocator, void *stream,
                                   qevict_block_cache **out);
 
-/* Synchronise the device's work on the handle's creation stream, free everything. */
+/* Synchronise the handle's creation stream, free everything. Work on other streams has to have ended (an allocator
+ * may give the memory to others at once), as has that of replayed graphs. */
 qevict_status qevict_block_destroy(qevict_block_cache *cache);
 
 /* The capacity in tokens (a multiple of 64), or -1 for NULL. */

@@ -1,0 +1,36 @@
+"""A cache in 8 bits that goes while calls on a side stream are still waiting to run: its memory is not used again
+before they have."""
+import pytest
+import torch
+
+from tiered_kv_cache_decode_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+def test_a_cache_that_goes_with_work_on_its_way():
+    B, Hq, Hkv, n = 2, 8, 2, 4000
+    g = torch.Generator().manual_seed(1)
+    k, v, q = (torch.randn(B, m, h, D, generator=g).bfloat16().cuda() for m, h in ((n, Hkv), (n, Hkv), (1, Hq)))
+    kv_len = torch.tensor([n, n - 77], dtype=torch.int32).cuda()
+    results = []
+    for side in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        c = binding.BlockCache(B, 1, Hq, Hkv, n)
+        side.wait_stream(torch.cuda.current_stream())
+        busy = torch.randn(4096, 4096, device="cuda")
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            for _ in range(40):   # some milliseconds before the calls
+                busy = (busy @ busy).clamp(-1, 1)
+        c.append(0, k, v, n_new=kv_len, stream=side)
+        out, lse = c.attend(0, q, kv_len, stream=side)
+        kr, vr = c.read(0, kv_len, n, stream=side)
+        bytes_held = B * Hkv * 2 * (n + 63) // 64 * 64 * D
+        del c
+        # what the allocator gives out now may be the cache's memory
+        others = [torch.full((bytes_held,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        results.append((out, lse, kr, vr))
+        del others, busy
+    assert all(torch.equal(a, b) for a, b in zip(*results))

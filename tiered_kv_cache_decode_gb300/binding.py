@@ -181,6 +181,11 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _capturing(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _DeviceArray:
     """Exposes a device pointer owned by the cache through __cuda_array_interface__."""
 
@@ -575,7 +580,9 @@ class TieredCache(_Handle):
 
 class BlockCache(_Handle):
     """Every token of ragged sequences in 8 bits, with a scale for each block of 64 tokens and KV head, on the
-    current CUDA device. Lengths and weights are the caller's tensors: int32 [B], fp32 [B][Hkv][capacity]."""
+    current CUDA device. Lengths and weights are the caller's tensors: int32 [B], fp32 [B][Hkv][capacity].
+    Calls may be on any streams, which have to exist until close(): it (also where the object goes) waits for them before
+    the memory goes back. Graphs that captured calls must not be running then, nor be replayed again."""
 
     def __init__(self, batch, num_layers, num_q_heads, num_kv_heads, capacity, fmt="int8", score_queries=1,
                  head_dim=HEAD_DIM, torch_allocator=True):
@@ -587,6 +594,7 @@ class BlockCache(_Handle):
                                score_queries)
         self.B, self.Hq, self.Hkv, self.fmt, self.layers = batch, num_q_heads, num_kv_heads, fmt, num_layers
         self.handle = ctypes.c_void_p()
+        self._home, self._streams = torch.cuda.current_stream(), {}   # the stream of creation; those of calls, by handle
         self.device = torch.cuda.current_device()
         self._dev = torch.device("cuda", self.device)
         self._alloc = self._torch_allocator() if torch_allocator else None
@@ -598,8 +606,21 @@ class BlockCache(_Handle):
 
     def close(self):
         if self.handle:
-            self._check(self.lib.qevict_block_destroy(self.handle))
-            self.handle = ctypes.c_void_p()
+            try:   # the memory goes back to the stream of the cache's creation, for which alone the call below waits
+                home = self._home
+                if not _capturing(home):
+                    for raw, s in self._streams.items():
+                        if raw != home.cuda_stream and not _capturing(s):   # a captured call's work is a graph's
+                            home.wait_stream(s)
+            finally:
+                rc, self.handle = self.lib.qevict_block_destroy(self.handle), ctypes.c_void_p()
+            self._check(rc)
+
+    def _raw_stream(self, stream):
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        raw = s.cuda_stream
+        self._streams[raw] = s
+        return raw
 
     def append(self, layer, k, v, start=None, n_new=None, weights=None, stream=None):
         """Tokens k, v [B][n][Hkv][128] (or [B][Hkv][128], one each; parts of a fused projection too) into positions
@@ -680,6 +701,8 @@ class BlockCache(_Handle):
             new_len = torch.empty_like(kv_len) if stream is None else self._new(kv_len, stream)
         if kept is None:
             kept = self._new(kv_len, stream, i32, (self.B, self.Hkv, max(keep, 0)))
+        if to is not self:
+            to._raw_stream(stream)   # its memory is in use there too
         rc = self.lib.qevict_block_evict(
             self.handle, layer, at, keep, recent, w, to.handle, into_layer,
             side(weights_out, to._per_token, f32, "weights_out"), side(new_len, self._per_seq, i32, "new_len"),
@@ -707,7 +730,7 @@ class BlockCache(_Handle):
         return self.lib.qevict_last_error().decode()
 
     def clear_status(self, stream=None):
-        self._check(self.lib.qevict_block_clear_status(self.handle, _stream(stream)))
+        self._check(self.lib.qevict_block_clear_status(self.handle, self._raw_stream(stream)))
 
 
 def decode_kch_slot(raw: torch.Tensor, Hkv: int, w: int, bits: int, kgw):
