@@ -1,5 +1,5 @@
-"""A cache in 8 bits that goes while calls on a side stream are still waiting to run: its memory is not used again
-before they have."""
+"""A cache in 8 bits that goes while calls on a side stream are still waiting to run (its memory is not used again before
+they have), or while another stream is captured."""
 import pytest
 import torch
 
@@ -34,3 +34,22 @@ def test_a_cache_that_goes_with_work_on_its_way():
         results.append((out, lse, kr, vr))
         del others, busy
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("torch_allocator", [True, False])
+def test_a_cache_may_go_while_another_stream_is_captured(torch_allocator):
+    """Closing one in the middle of a capture does not end that."""
+    old, c = (binding.BlockCache(1, 1, 4, 1, 256, torch_allocator=torch_allocator) for _ in range(2))
+    k = torch.randn(1, 200, 1, D, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    lens = torch.tensor([200], dtype=torch.int32).cuda()
+    k_out, v_out = (torch.zeros(1, 200, 1, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    old.append(0, k, k)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.append(0, k, k)
+        old.close()
+        c.read(0, lens, 200, k_out=k_out, v_out=v_out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert k_out[:, 192:].equal(k[:, 192:]) and k_out.equal(v_out) and k_out[:, :192].any() and c.status() == 0

@@ -166,8 +166,16 @@ qevict_status qevict_block_create(const qevict_block_config *config, const qevic
 
 qevict_status qevict_block_destroy(qevict_block_cache *c) {
     if (!c) return fail(QEVICT_ERR_INVALID_ARG, "cache is NULL");
-    cudaStreamSynchronize(c->stream);
+    // Also while the thread captures another stream (a handle that goes at any time): a wait in the usual mode would end
+    // that capture. The handle's own stream in capture holds nothing to wait for.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(c->stream, &state);
+    if (e == cudaSuccess && state == cudaStreamCaptureStatusNone) e = cudaStreamSynchronize(c->stream);
+    if (e != cudaSuccess) cudaGetLastError();
     release(c);
+    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
     return QEVICT_OK;
 }
 
