@@ -181,6 +181,13 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _fit(*numbers):
+    """Refuse what the library's int32 parameters would cut to another number."""
+    for x in numbers:
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{x} does not fit 32 bits")
+
+
 def _capturing(stream):
     with torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
@@ -590,6 +597,7 @@ class BlockCache(_Handle):
         self.lib = load()
         if fmt not in BLOCK_FORMATS:
             raise ValueError(f"fmt must be one of {sorted(BLOCK_FORMATS)}, got {fmt!r}")
+        _fit(batch, num_layers, num_q_heads, num_kv_heads, head_dim, capacity, score_queries)
         self.cfg = BlockConfig(batch, num_layers, num_q_heads, num_kv_heads, head_dim, capacity, BLOCK_FORMATS[fmt],
                                score_queries)
         self.B, self.Hq, self.Hkv, self.fmt, self.layers = batch, num_q_heads, num_kv_heads, fmt, num_layers
@@ -625,6 +633,7 @@ class BlockCache(_Handle):
     def append(self, layer, k, v, start=None, n_new=None, weights=None, stream=None):
         """Tokens k, v [B][n][Hkv][128] (or [B][Hkv][128], one each; parts of a fused projection too) into positions
         start[b] .. start[b] + n_new[b] - 1 (None: 0 and n); their weights, where given, become 0."""
+        _fit(layer)
         n, ks = self._tokens(k, self.Hkv, "k")
         nv, vs = self._tokens(v, self.Hkv, "v")
         if nv != n:
@@ -641,6 +650,7 @@ class BlockCache(_Handle):
         """Attention of q [B][n_q][Hq][128] (or [B][Hq][128]), the last positions of kv_len [B] tokens, n_q <= 8.
         Returns (out bf16, lse fp32 [B][Hq][n_q] or None). weights: each token's probabilities, summed over the
         queries and averaged over the query heads of its KV head, are added (or written)."""
+        _fit(layer)
         n_q = self._dense(q, self.Hq, "q")
         side, f32 = self._side, torch.float32
         at = side(kv_len, self._per_seq, torch.int32, "kv_len")
@@ -667,6 +677,7 @@ class BlockCache(_Handle):
     def read(self, layer, kv_len, n, first=None, k_out=None, v_out=None, stream=None):
         """(k, v) bf16 [B][n][Hkv][128]: what the cache holds at positions first[b] .. (None: 0 ..). Rows at positions
         outside [0, kv_len[b]) are left as they were (0 in tensors made here)."""
+        _fit(layer, n)
         shape, bf = (self.B, n, self.Hkv, HEAD_DIM), torch.bfloat16
         side, i32 = self._side, torch.int32
         at = side(kv_len, self._per_seq, i32, "kv_len")
@@ -688,6 +699,7 @@ class BlockCache(_Handle):
         """Keep, of each (sequence, KV head)'s tokens in full blocks, the last `recent` and those of the largest
         weights, `keep` (a multiple of 64) in all; in place, weights with them, or into layer `into_layer` of another
         BlockCache. Returns (new_len int32 [B], kept int32 [B][Hkv][keep]: the old positions, then -1)."""
+        _fit(layer, keep, recent, into_layer)
         to = self if into is None else into
         if into is None:
             into_layer = layer
@@ -714,6 +726,7 @@ class BlockCache(_Handle):
     def blocks(self, layer):
         """Host copies of a layer's full blocks: codes [B][Hkv][capacity / 64][K, V][64][128], int8 or float8_e4m3fn,
         and scales fp32 [B][Hkv][capacity / 64][K, V]."""
+        _fit(layer)
         c, s = ctypes.c_void_p(), ctypes.c_void_p()
         self._check(self.lib.qevict_block_view(self.handle, layer, ctypes.byref(c), ctypes.byref(s)))
         nb = self.capacity // BLOCK_TOKENS
