@@ -755,8 +755,10 @@ qevict_status qevict_block_append(qevict_block_cache *cache, int32_t layer, cons
  *           its probabilities, added (accumulate nonzero) or written; others are
  *           left as they were. Needs score_queries >= n_q (INVALID_ARG).
  * A query that sees no token gets out 0, lse -inf, and gives no weight. One that holds
- * an infinity or a NaN gets an undefined row (and weights of its KV head) and reaches
- * no other. Sums run in a fixed order, in fp32: every call with the same lengths
+ * an infinity or a NaN, or for which max |q| max |k| passes 2^120 (logits that fp32 does
+ * not hold), gets an undefined row (and weights of its KV head) and reaches no other;
+ * values may have any magnitude (where a sequence holds some above 2^64, outputs are off
+ * by up to 2^-90 besides). Sums run in a fixed order, in fp32: every call with the same lengths
  * gives the same bits (how a sequence's tokens are divided over the GPU depends on
  * the whole batch's). out, lse and weights must not overlap one another or an input
  * (INVALID_ARG). Waits inside the kernel are for its own copies and have a limit of
