@@ -220,8 +220,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // One cluster per (sequence, KV head): the `want`-th largest key of the candidates by passes over eleven, eleven and ten
 // bits, the CTAs' histograms added in distributed shared memory; then each warp counts its run's keys above it and equal to
 // it, and with the counts of all warps before it gives every kept token its rank. Bound by latency: one read of the weights
-// (then kept in shared memory: CACHED), three passes of one cluster barrier each, one more for the counts. Short contexts
-// take a cluster of one CTA, whose barrier is the CTA's own. 2K tokens 7 us, 32 pairs of 32K 15, 8 of 128K 19.
+// (then kept in shared memory: CACHED), three passes of one cluster barrier each, one more for the counts. Caches with
+// room for 8K tokens take a cluster of one CTA, whose barrier is the CTA's own, those with room for more up to eight; keys
+// are kept where a CTA's share of the room fits (40,960). The capacity decides both, whatever the lengths. 2K tokens 7 us, 32 pairs of 32K 15, 8 of 128K 19.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockDev D, const BlockEvictArgs a, int ctas) {
     extern __shared__ __align__(16) uint32_t sel[];
@@ -435,8 +436,9 @@ __device__ __forceinline__ void move_open(const BlockDev &D, const BlockDev &to,
 }
 
 // Into another cache: a CTA for the keys and one for the values of each new block, the last ones for the open block.
-// 4 x 32K tokens of 8 KV heads to 6.5K: 28 us, 3.8 TB/s, bound by instructions (0.69 of the issue slots) and by the chain
-// of a block: positions, codes, two barriers (with the next block's loads under it 35, a warp to a block 32 us).
+// 4 x 32K tokens of 8 KV heads to 6.5K: 28 us, 3.8 TB/s, bound by instructions (0.69 of the issue slots; 12.6 a code, of
+// which the conversion takes 7 and a thread's fixed part, spread over 32 codes, the rest) and by the chain of a block:
+// positions, codes, two barriers (with the next block's loads under it 35, a warp to a block 32 us).
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 6)
     block_move_kernel(const BlockDev D, const BlockDev to, const BlockEvictArgs a) {
@@ -456,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 6)
 
 // In place: a cluster per (sequence, KV head), keys and values, goes over the new blocks in rounds of one per
 // CTA. A token only ever moves towards the front, so what round n reads lies at or behind
-// the blocks that it writes, and a barrier between a round's reads and its writes suffices.
+// the blocks that it writes, and a barrier between a round's reads and its writes suffices. Bound by the chain of its
+// rounds, 8 blocks each: whole evictions of 4 x 32K to 6.5K 56 us (into another cache 42), of 128K to 13K 74 (36).
 template <int FMT>
 __global__ void __cluster_dims__(kMoveCtas, 1, 1) __launch_bounds__(kThreads)
     block_compact_kernel(const BlockDev D, const BlockEvictArgs a) {

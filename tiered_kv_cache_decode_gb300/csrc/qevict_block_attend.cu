@@ -28,6 +28,7 @@ constexpr int kThreads = 256, kWarps = 8;          // of the joining kernel
 constexpr int kHalf = kBlkBytes / 2;               // what one copy brings: K or V of a unit
 // Of kHalf bytes, 2 for each warp: 128 KiB on their way to an SM. With 3 for each the memory system serves the SMs less
 // evenly (the slowest took 17 % longer than the median for as many bytes: 4 x 128K 175 us against 158), with 1 it idles (190).
+// That is with a ring to a warp; six rings of 9 to 16 rows divide the slots to 2 each as well and leave 4 (96 KiB).
 constexpr int kSlots = 16;
 constexpr int kRec = kHeadDim + 4;                 // floats of a row of a partial result: output, maximum, sum
 static_assert(kRec % 4 == 0, "rows of whole float4");
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) block_attend_kernel(const Block
                 for (int t = 0; t < 8; ++t) {
                     const float p0 = tc_ex2(x[t][0] - ref), p1 = tc_ex2(x[t][1] - ref);
                     sum += p0 + p1;
-                    p[t] = bits(__floats2half2_rn(p0, p1));   // off by 2^-12 of a term
+                    p[t] = bits(__floats2half2_rn(p0, p1));   // off by 2^-11 of a term
                 }
                 r.l = fmaf(sum, r.unit, r.l);
                 const float vs = sc.y * r.unit;
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, 4) block_join_kernel(const BlockDev 
 
 // Warps of a CTA: 8 for up to 8 rows (the memory bounds them; 128 KiB are on their way either way). More rows share a
 // ring, a warp for every 8, and there arithmetic bounds: 12 warps, what the registers allow (5 queries of 4 x 8K 41 us,
-// 43.5 with 8 warps of 16 rows, which share the codes' way to fp16, 43 with 16 warps).
+// 43.5 with 8 warps of 16 rows, which share the codes' way to fp16, 43 with 16 warps). Rows that do not divide 12 warps
+// leave some idle: 33 to 40 rows two, 49 to 56 five, 57 to 64 four (4 x 8K with 64 rows 44 us, with weights 69).
 constexpr int kFewWarps = 8, kManyWarps = 12;
 
 int64_t blk_part_floats(int G, int num_sms) {
