@@ -53,3 +53,34 @@ def test_a_cache_may_go_while_another_stream_is_captured(torch_allocator):
     graph.replay()
     torch.cuda.synchronize()
     assert k_out[:, 192:].equal(k[:, 192:]) and k_out.equal(v_out) and k_out[:, :192].any() and c.status() == 0
+
+
+def test_a_cache_of_a_side_stream_may_go_while_another_is_captured():
+    """The wait for the side stream joins nothing to the capture, and its memory is not used before its work is done."""
+    n = 4000
+    k = torch.randn(2, n, 2, D, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    lens = torch.full((2,), n, dtype=torch.int32).cuda()
+    side, x = torch.cuda.Stream(), torch.zeros(8, device="cuda")
+    want = None
+    for closes in (False, True):
+        c = binding.BlockCache(2, 1, 4, 2, n)
+        busy = torch.randn(4096, 4096, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                busy = (busy @ busy).clamp(-1, 1)
+        c.append(0, k, k, stream=side)
+        got = c.read(0, lens, n, stream=side)
+        if closes:
+            with torch.cuda.graph(graph):
+                x += 1
+                c.close()
+                x += 1
+            graph.replay()
+        others = [torch.full((c.B * c.Hkv * 2 * c.capacity * D,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del others
+    assert torch.all(x == 2)
