@@ -167,7 +167,7 @@ qevict_status qevict_block_create(const qevict_block_config *config, const qevic
 qevict_status qevict_block_destroy(qevict_block_cache *c) {
     if (!c) return fail(QEVICT_ERR_INVALID_ARG, "cache is NULL");
     // Also while the thread captures another stream (a handle that goes at any time): a wait in the usual mode would end
-    // that capture. The handle's own stream in capture holds nothing to wait for.
+    // that capture. The handle's own stream, where that is the one in capture, cannot be waited for.
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
